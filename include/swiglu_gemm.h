@@ -262,6 +262,172 @@ int sg_interleave_gate_up(const void* W1, const void* W2, void* Wfused,
 int sg_silu_mul(const void* G, const void* U, void* Y, int64_t M, int64_t N,
                 int dtype, void* stream);
 
+/*
+ * Products grouped by expert (mixture-of-experts MLPs)
+ * ----------------------------------------------------
+ * The M rows of A are sorted by expert: expert e owns rows offsets[e] .. offsets[e+1]-1,
+ * R_e for short.  `offsets` is DEVICE memory, experts + 1 ascending int32 row numbers in
+ * [0, M] (experts 1..65536); an expert may own no row.  Rows before offsets[0] and from
+ * offsets[experts] on belong to no expert: they are neither read nor written.  The host
+ * never reads the offsets, so a call can be captured into a HIP graph and replayed with
+ * other offsets.  The kernels clamp each offset to [0, M]; a table that does not ascend
+ * gives unspecified rows of the output (nothing outside it is written).
+ * These calls allocate nothing and use no workspace: calls on different streams may
+ * overlap.  Results are run-to-run identical.
+ * Alignment: any element-aligned pointers and leading dimensions are accepted; 16-byte
+ * aligned operands with rows and strides of 16-byte multiples run on the direct-to-LDS
+ * tile kernels, others on a 64 x 64 tile kernel that loads element by element.
+ * A problem of more than 2^23 output tiles returns hipErrorInvalidConfiguration.
+ */
+
+/*
+ * sg_grouped_gemm: C[r] = alpha * scale[e] * A[r] * op(B_e) + beta * C_old[r] for r in R_e,
+ * B_e = B + e * strideB elements.
+ *  1 transB  'N': B_e stored K x N; 'T': B_e stored N x K (the input gradient of a
+ *            product with B_e stored K' x N' is the 'T' call with N = K', K = N').
+ *  2 experts, 3 offsets   see above.
+ *  4 M, 5 N, 6 K   >= 0; M: rows of A and C in all.
+ *  7 alpha   fp32 scalar.   8 scale   NULL, or `experts` fp32 factors (device memory).
+ *  9 A, 10 lda   M x K.   11 B, 12 ldb, 13 strideB (>= 0; 0: one weight for all).
+ *  14 beta   fp32 scalar; 0: C is write-only.   15 C, 16 ldc   M x N.
+ *  17 dtype  SG_F16, SG_BF16 (A, B, C), or SG_F8E4M3 (A, B; C bf16).
+ *  18 stream.
+ * Quick returns: M == 0 or N == 0 does nothing; K == 0 or alpha == 0 computes
+ * C = beta * C_old in the experts' rows.
+ * Invalid: -i for argument i as in sg_gemm (NULL operands that are read, leading
+ * dimensions too small, negative sizes or strides, unsupported dtype).
+ */
+int sg_grouped_gemm(char transB, int64_t experts, const int32_t* offsets, int64_t M, int64_t N,
+                    int64_t K, float alpha, const float* scale, const void* A, int64_t lda,
+                    const void* B, int64_t ldb, int64_t strideB, float beta, void* C,
+                    int64_t ldc, int dtype, void* stream);
+
+/*
+ * sg_grouped_gemm_wgrad: C_e = alpha * A[R_e]^T * D[R_e] + beta * C_e (K x N), the weight
+ * gradient of the product above with D the gradient of its output.  An expert without
+ * rows gets beta * C_e (zeros for beta == 0).
+ *  1 experts, 2 offsets   see above.   3 M, 4 N, 5 K   >= 0.   6 alpha   fp32 scalar.
+ *  7 A, 8 lda   M x K.   9 D, 10 ldd   M x N.   11 beta   fp32 scalar; 0: C write-only.
+ *  12 C, 13 ldc, 14 strideC   C_e = C + e * strideC elements; strideC >= (K-1)*ldc + N.
+ *  15 dtype  of A and D: SG_F16 or SG_BF16.   16 c_dtype   dtype or SG_F32.
+ *  17 stream.
+ * Quick returns: N == 0 or K == 0 does nothing; M == 0 or alpha == 0 computes
+ * C_e = beta * C_e.
+ */
+int sg_grouped_gemm_wgrad(int64_t experts, const int32_t* offsets, int64_t M, int64_t N,
+                          int64_t K, float alpha, const void* A, int64_t lda, const void* D,
+                          int64_t ldd, float beta, void* C, int64_t ldc, int64_t strideC,
+                          int dtype, int c_dtype, void* stream);
+
+/*
+ * sg_grouped_swiglu_gemm: Y[r] = SiLU(s_e * g) ⊙ (s_e * u), (g, u) = A[r] * (W1_e, W2_e),
+ * s_e = alpha * scale[e], from the column-interleaved W_fused of sg_swiglu_gemm for each
+ * expert.
+ *  1 experts, 2 offsets   see above.
+ *  3 A  M x K, 4 Wfused  experts x K x 2N, 5 Y  M x N; contiguous.
+ *  6 M, 7 N, 8 K   >= 0.
+ *  9 dtype   SG_F16, SG_BF16 (all three), or SG_F8E4M3 (A, W codes; Y bf16).
+ *  10 alpha  fp32, finite and > 0; 1.0 unless dtype is SG_F8E4M3.
+ *  11 scale  NULL, or `experts` fp32 factors (device memory; SG_F8E4M3 only).
+ *  12 stream.
+ * Quick returns: M == 0 or N == 0 does nothing; K == 0 writes Y = 0 in the experts' rows.
+ */
+int sg_grouped_swiglu_gemm(int64_t experts, const int32_t* offsets, const void* A,
+                           const void* Wfused, void* Y, int64_t M, int64_t N, int64_t K,
+                           int dtype, float alpha, const float* scale, void* stream);
+
+/*
+ * sg_grouped_swiglu_gemm_bwd: dH (M x 2N), the gradient of the gate and up products from
+ * the gradient dY (M x N) of Y.  The products are computed again from A and Wfused, so the
+ * forward need not keep them.  With sig = 1 / (1 + e^-g):
+ *     dH[r, 2n]   = dY * u * sig * (1 + g * (1 - sig))      dH[r, 2n+1] = dY * g * sig
+ * in fp32, rounded once.  dA is then sg_grouped_gemm('T', dH, Wfused) and the gradient of
+ * Wfused sg_grouped_gemm_wgrad(A, dH).
+ *  1 experts, 2 offsets, 3 A, 4 Wfused   as the forward.   5 dY  M x N, 6 dH  M x 2N;
+ *  contiguous.   7 M, 8 N, 9 K   >= 0.   10 dtype   SG_F16 or SG_BF16.   11 stream.
+ */
+int sg_grouped_swiglu_gemm_bwd(int64_t experts, const int32_t* offsets, const void* A,
+                               const void* Wfused, const void* dY, void* dH, int64_t M,
+                               int64_t N, int64_t K, int dtype, void* stream);
+
+/*
+ * Microscaled 4-bit floating point (OCP MX FP4)
+ * ---------------------------------------------
+ * A matrix of M rows and K columns is held as e2m1 codes (0, .5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) in blocks of 32 along a row, each with one e8m0 scale 2^(s - 127)
+ * (s == 255: every element of the block is NaN):
+ *   codes   M rows of SG_MXFP4_ROW_BYTES(K) bytes; element 2i in the low half of byte i;
+ *           the last block of a row is filled with zeros.
+ *   scales  SG_MXFP4_SCALE_BYTES(M, K) bytes: tiles of 32 rows x 8 blocks, 256 bytes each,
+ *           all tiles of 32 rows one after the other; the byte of row r, block b is at
+ *           256*((r/32)*ceil(K/256) + b/8) + 128*((b/4)%2) + 4*(r%32) + b%4.
+ *           Bytes of rows and blocks outside the matrix are not used.
+ * A batch of matrices follows one another, each with its own codes and tiles of scales.
+ * These calls allocate nothing and use no workspace.
+ */
+#define SG_MXFP4_ROW_BYTES(K) ((((int64_t)(K) + 31) / 32) * 16)
+#define SG_MXFP4_SCALE_BYTES(M, K) \
+    ((((int64_t)(M) + 31) / 32) * (((int64_t)(K) + 255) / 256) * 256)
+
+/*
+ * sg_mxfp4_quantize: codes and scales of X.  For each block, t = max |x|:
+ * scale 2^(floor(log2 t) - 2), not below 2^-127 (t == 0: 2^-127); codes x / scale rounded
+ * to the nearest e2m1 value, ties to the even code, saturating at +-6.  A block with an
+ * infinity or a NaN gets scale 255 and zero codes.
+ *  1 X, 2 ldx, 3 strideX   `batch` matrices M x K, strideX elements apart (>= 0).
+ *  4 batch (0..65535), 5 M, 6 K   >= 0.   7 dtype   of X: SG_F32, SG_F16 or SG_BF16.
+ *  8 codes, 9 scales   outputs, 4-byte aligned, or NULL.
+ *  10 values   NULL, or the values the codes and scales stand for, batch x M x K
+ *            contiguous, rounded to X's type (exact but for fp16 values below 2^-24 or
+ *            above 65504).
+ *  11 stream.
+ * Invalid: as above; codes, scales and values all NULL (-8).
+ */
+int sg_mxfp4_quantize(const void* X, int64_t ldx, int64_t strideX, int64_t batch, int64_t M,
+                      int64_t K, int dtype, void* codes, void* scales, void* values,
+                      void* stream);
+
+/*
+ * sg_mxfp4_dequantize: X = the values of codes and scales, rounded to X's type.
+ *  1 codes (4-byte aligned), 2 scales, 3 batch, 4 M, 5 K, 6 X, 7 ldx, 8 strideX
+ *  (>= (M-1)*ldx + K for more than one matrix), 9 dtype (SG_F32, SG_F16, SG_BF16), 10 stream.
+ */
+int sg_mxfp4_dequantize(const void* codes, const void* scales, int64_t batch, int64_t M,
+                        int64_t K, void* X, int64_t ldx, int64_t strideX, int dtype,
+                        void* stream);
+
+/*
+ * sg_mxfp4_tile_scales: scales stored as rows of bytes (`batch` matrices M x blocks, rows
+ * ld, matrices `stride` bytes apart) to the tiles above; padding becomes 0.
+ *  1 src, 2 ld, 3 stride, 4 batch, 5 M, 6 blocks, 7 dst (4-byte aligned), 8 stream.
+ */
+int sg_mxfp4_tile_scales(const void* src, int64_t ld, int64_t stride, int64_t batch, int64_t M,
+                         int64_t blocks, void* dst, void* stream);
+
+/*
+ * sg_mxfp4_gemm: C = alpha * A * B^T, A (M x K) and B (N x K) held as above, fp32 sums; or,
+ * with offsets, C[r] = alpha * A[r] * B_e^T for r in R_e, B a batch of `experts` matrices.
+ *  1 experts, 2 offsets   as the grouped products; offsets NULL with experts 1: every row.
+ *  3 M, 4 N, 5 K   >= 0.   6 alpha   fp32 scalar.
+ *  7 A codes (16-byte aligned), 8 A scales (4), 9 B codes (16), 10 B scales (4).
+ *  11 C, 12 ldc   M x N, written only.   13 dtype   of C: SG_F32, SG_F16 or SG_BF16.
+ *  14 stream.
+ * Quick returns: M == 0 or N == 0 does nothing; K == 0 or alpha == 0 writes zeros.
+ */
+int sg_mxfp4_gemm(int64_t experts, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                  float alpha, const void* A, const void* As, const void* B, const void* Bs,
+                  void* C, int64_t ldc, int dtype, void* stream);
+
+/*
+ * sg_mxfp4_swiglu_gemm: Y = SiLU(A * W1^T) ⊙ (A * W2^T) from W of 2N rows, gate and up
+ * interleaved (row 2n = W1's row n, row 2n+1 = W2's); offsets as sg_mxfp4_gemm.
+ *  1 experts, 2 offsets, 3 M, 4 N, 5 K; 6 A codes, 7 A scales, 8 W codes, 9 W scales;
+ *  10 Y  M x N contiguous; 11 dtype of Y: SG_F16 or SG_BF16; 12 stream.
+ */
+int sg_mxfp4_swiglu_gemm(int64_t experts, const int32_t* offsets, int64_t M, int64_t N,
+                         int64_t K, const void* A, const void* As, const void* W,
+                         const void* Ws, void* Y, int dtype, void* stream);
+
 /* Text for a status code returned by any sg_* call (static storage). */
 const char* sg_status_string(int status);
 

@@ -11,6 +11,17 @@ fails to load, every call raises.
     swiglu_gemm(A, Wfused, Y, scale_a=1, scale_w=1)          # Y written in place
     interleave_gate_up(W1, W2, out=None) -> Wfused
     silu_mul(G, U, Y)                                        # unfused activation
+
+Products whose rows are sorted by expert (offsets: experts + 1 int32 on the GPU), and
+microscaled 4-bit floating point:
+
+    grouped_gemm(A, B, C, offsets, transB='N', scale=None)   # C[rows of e] = A @ op(B[e])
+    grouped_gemm_wgrad(A, D, C, offsets)                     # C[e] = A[rows of e]^T @ D
+    grouped_swiglu_gemm(A, Wfused, Y, offsets)               # SwiGLU with experts' weights
+    grouped_swiglu_gemm_bwd(A, Wfused, dY, dH, offsets)      # its backward up to dH
+    mxfp4_quantize(X) -> codes, scales                       # and mxfp4_dequantize
+    mxfp4_gemm(A, As, B, Bs, C, offsets=None)                # C = A @ B^T
+    mxfp4_swiglu_gemm(A, As, W, Ws, Y, offsets=None)
 """
 from __future__ import annotations
 
@@ -75,6 +86,23 @@ def lib() -> ctypes.CDLL:
         L.sg_interleave_gate_up.restype = ctypes.c_int
         L.sg_silu_mul.argtypes = [vp, vp, vp, i64, i64, ctypes.c_int, vp]
         L.sg_silu_mul.restype = ctypes.c_int
+        ci = ctypes.c_int
+        experts = {
+            "sg_grouped_gemm": [c, i64, vp, i64, i64, i64, f32, vp, vp, i64, vp, i64, i64, f32,
+                                vp, i64, ci, vp],
+            "sg_grouped_gemm_wgrad": [i64, vp, i64, i64, i64, f32, vp, i64, vp, i64, f32, vp, i64,
+                                      i64, ci, ci, vp],
+            "sg_grouped_swiglu_gemm": [i64, vp, vp, vp, vp, i64, i64, i64, ci, f32, vp, vp],
+            "sg_grouped_swiglu_gemm_bwd": [i64, vp, vp, vp, vp, vp, i64, i64, i64, ci, vp],
+            "sg_mxfp4_quantize": [vp, i64, i64, i64, i64, i64, ci, vp, vp, vp, vp],
+            "sg_mxfp4_dequantize": [vp, vp, i64, i64, i64, vp, i64, i64, ci, vp],
+            "sg_mxfp4_tile_scales": [vp, i64, i64, i64, i64, i64, vp, vp],
+            "sg_mxfp4_gemm": [i64, vp, i64, i64, i64, f32, vp, vp, vp, vp, vp, i64, ci, vp],
+            "sg_mxfp4_swiglu_gemm": [i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, ci, vp],
+        }
+        for name, types in experts.items():
+            getattr(L, name).argtypes = types
+            getattr(L, name).restype = ci
         L.sg_status_string.argtypes = [ctypes.c_int]
         L.sg_status_string.restype = ctypes.c_char_p
         L.sg_last_config.argtypes = [ctypes.c_char_p, ctypes.c_int]
@@ -493,4 +521,361 @@ def silu_mul(G, U, Y):
     st = lib().sg_silu_mul(G.data_ptr(), U.data_ptr(),
                            Y.data_ptr(), M, N, _dtype_code(G), _stream(Y))
     _check(st, "sg_silu_mul")
+    return Y
+
+
+# ------------------------------------------------- products grouped by expert
+def _same_device(*ts):
+    """Every tensor on one GPU; a context that makes it the current device (the library
+    launches on the current device's kernels)."""
+    import torch
+    first = None
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("every tensor must be on the GPU")
+        if first is None:
+            first = t.device
+        elif t.device != first:
+            raise ValueError("every tensor must be on one device, got %s and %s"
+                             % (first, t.device))
+    return torch.cuda.device(first)
+
+
+def _experts(offsets, experts: int) -> None:
+    import torch
+    if offsets.dtype != torch.int32:
+        raise TypeError("offsets must be int32, not %s" % offsets.dtype)
+    if offsets.dim() != 1 or not offsets.is_contiguous() or offsets.numel() != experts + 1:
+        raise ValueError("offsets must be a contiguous vector of experts + 1 = %d row numbers"
+                         % (experts + 1))
+
+
+def _scale(scale, experts: int):
+    import torch
+    if scale is None:
+        return None
+    if scale.dtype != torch.float32:
+        raise TypeError("scale must be float32")
+    if scale.dim() != 1 or not scale.is_contiguous() or scale.numel() != experts:
+        raise ValueError("scale must be a contiguous vector of %d factors" % experts)
+    return scale.data_ptr()
+
+
+def _rows(t, name: str, cols: int) -> int:
+    """Leading dimension of a 2-D tensor of rows with `cols` columns."""
+    if t.dim() != 2 or t.size(1) != cols:
+        raise ValueError("%s has shape %s, expected rows of %d" % (name, tuple(t.shape), cols))
+    ld = _ld(t)
+    if ld < cols:
+        raise ValueError("%s: rows overlap (row stride %d, %d columns)" % (name, ld, cols))
+    return ld
+
+
+def _stack(t, name: str, disjoint: bool):
+    """Leading dimension and stride of a 3-D stack of row-major matrices, one an expert."""
+    if t.dim() != 3 or t.size(0) < 1:
+        raise ValueError("%s must be 3-D, one matrix for each expert" % name)
+    e, r, c = t.shape
+    if c > 1 and t.stride(2) != 1:
+        raise ValueError("%s: the last dimension must be contiguous (stride 1)" % name)
+    ld = max(t.stride(1), 1) if r > 1 else max(c, 1)
+    stride = t.stride(0) if e > 1 else 0
+    if ld < c or (disjoint and e > 1 and r and c and stride < (r - 1) * ld + c):
+        raise ValueError("%s: the matrices or their rows overlap" % name)
+    return ld, stride
+
+
+def grouped_gemm(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, transB: str = "N",
+                 scale=None):
+    """C[r] = alpha * scale[e] * A[r] @ op(B[e]) + beta * C[r] for the rows offsets[e] <= r <
+    offsets[e + 1] of each expert, in place on C; other rows stay as they are.  A [M, K];
+    B [experts, K, N], or [experts, N, K] with transB='T'; C [M, N] of A's dtype (bf16 for
+    e4m3 operands); scale: None or float32 [experts]."""
+    code = _dtype_code(A)
+    if code == SG_F32:
+        raise TypeError("grouped products take bf16, fp16 or e4m3 operands")
+    tb = transB.upper()
+    if tb not in ("N", "T"):
+        raise ValueError("transB must be 'N' or 'T'")
+    if A.dim() != 2:
+        raise ValueError("A must be 2-D")
+    if _tables()[0].get(B.dtype) != code:
+        raise TypeError("B must have A's dtype")
+    if C.dtype not in _out_dtypes(code):
+        raise TypeError("C has dtype %s, expected %s" % (C.dtype, _out_dtypes(code)[0]))
+    M, K = A.shape
+    ldb, sB = _stack(B, "B", False)
+    E, N = B.shape[0], B.shape[1] if tb == "T" else B.shape[2]
+    if (B.shape[2] if tb == "T" else B.shape[1]) != K:
+        raise ValueError("op(B) must have A's %d columns as rows" % K)
+    lda, ldc = _rows(A, "A", K), _rows(C, "C", N)
+    if C.shape[0] != M:
+        raise ValueError("C has %d rows, A %d" % (C.shape[0], M))
+    _experts(offsets, E)
+    sp = _scale(scale, E)
+    with _same_device(A, B, C, offsets, scale):
+        st = lib().sg_grouped_gemm(tb.encode(), E, offsets.data_ptr(), M, N, K, float(alpha), sp,
+                                   A.data_ptr(), lda, B.data_ptr(), ldb, sB, float(beta),
+                                   C.data_ptr(), ldc, code, _stream(C))
+    _check(st, "sg_grouped_gemm")
+    return C
+
+
+def grouped_gemm_wgrad(A, D, C, offsets, alpha: float = 1.0, beta: float = 0.0):
+    """C[e] = alpha * A[rows of e]^T @ D[rows of e] + beta * C[e], in place on C [experts, K,
+    N]: the gradient of grouped_gemm's weight from its input A [M, K] and the gradient D
+    [M, N] of its output (bf16 or fp16); C has their dtype or float32."""
+    import torch
+    code = _dtype_code(A)
+    if code not in (SG_F16, SG_BF16):
+        raise TypeError("the weight gradient takes bf16 or fp16 operands")
+    if D.dtype != A.dtype:
+        raise TypeError("D must have A's dtype")
+    if C.dtype not in (A.dtype, torch.float32):
+        raise TypeError("C has dtype %s, expected %s or float32" % (C.dtype, A.dtype))
+    if A.dim() != 2 or D.dim() != 2 or A.shape[0] != D.shape[0]:
+        raise ValueError("A and D must be 2-D with the same rows")
+    M, K = A.shape
+    N = D.shape[1]
+    ldc, sC = _stack(C, "C", True)
+    E = C.shape[0]
+    if tuple(C.shape[1:]) != (K, N):
+        raise ValueError("C has shape %s, expected (experts, %d, %d)" % (tuple(C.shape), K, N))
+    _experts(offsets, E)
+    lda, ldd = _rows(A, "A", K), _rows(D, "D", N)
+    with _same_device(A, D, C, offsets):
+        st = lib().sg_grouped_gemm_wgrad(E, offsets.data_ptr(), M, N, K, float(alpha),
+                                         A.data_ptr(), lda, D.data_ptr(), ldd, float(beta),
+                                         C.data_ptr(), ldc, sC, code, _dtype_code(C), _stream(C))
+    _check(st, "sg_grouped_gemm_wgrad")
+    return C
+
+
+def _grouped_swiglu(A, Wfused):
+    code = _dtype_code(A)
+    if code == SG_F32:
+        raise TypeError("SwiGLU takes bf16, fp16 or e4m3 operands")
+    if _tables()[0].get(Wfused.dtype) != code:
+        raise TypeError("Wfused must have A's dtype")
+    if A.dim() != 2 or Wfused.dim() != 3 or Wfused.shape[0] < 1:
+        raise ValueError("A must be 2-D and Wfused 3-D, one matrix for each expert")
+    M, K = A.shape
+    E, N2 = Wfused.shape[0], Wfused.shape[2]
+    if N2 % 2:
+        raise ValueError("Wfused must have an even number of columns (gate, up pairs)")
+    _contig(A, "A", (M, K))
+    _contig(Wfused, "Wfused", (E, K, N2))
+    return code, E, M, N2 // 2, K
+
+
+def grouped_swiglu_gemm(A, Wfused, Y, offsets, alpha: float = 1.0, scale=None):
+    """Y[r] = SiLU(s*A[r]@W1[e]) * (s*A[r]@W2[e]) for the rows of each expert, s = alpha *
+    scale[e], from the column-interleaved Wfused [experts, K, 2N] (interleave_gate_up on
+    each); A [M, K], Y [M, N], all contiguous.  alpha and scale: e4m3 operands only."""
+    code, E, M, N, K = _grouped_swiglu(A, Wfused)
+    if Y.dtype not in _out_dtypes(code):
+        raise TypeError("Y has dtype %s, expected %s" % (Y.dtype, _out_dtypes(code)[0]))
+    _contig(Y, "Y", (M, N))
+    _experts(offsets, E)
+    sp = _scale(scale, E)
+    with _same_device(A, Wfused, Y, offsets, scale):
+        st = lib().sg_grouped_swiglu_gemm(E, offsets.data_ptr(), A.data_ptr(), Wfused.data_ptr(),
+                                          Y.data_ptr(), M, N, K, code, float(alpha), sp,
+                                          _stream(Y))
+    _check(st, "sg_grouped_swiglu_gemm")
+    return Y
+
+
+def grouped_swiglu_gemm_bwd(A, Wfused, dY, dH, offsets):
+    """dH [M, 2N]: the gradient of gate and up (interleaved like Wfused's columns) from the
+    gradient dY [M, N] of grouped_swiglu_gemm's output; gate and up are computed again from A
+    and Wfused.  Then dA = grouped_gemm(dH, Wfused, dA, offsets, transB='T') and the weight's
+    gradient grouped_gemm_wgrad(A, dH, dW, offsets).  bf16 or fp16, all contiguous."""
+    code, E, M, N, K = _grouped_swiglu(A, Wfused)
+    if code == SG_F8E4M3:
+        raise TypeError("SwiGLU's backward takes bf16 or fp16 operands")
+    for t, name, n in ((dY, "dY", N), (dH, "dH", 2 * N)):
+        _contig(t, name, (M, n))
+        if t.dtype != A.dtype:
+            raise TypeError("%s must have A's dtype" % name)
+    _experts(offsets, E)
+    with _same_device(A, Wfused, dY, dH, offsets):
+        st = lib().sg_grouped_swiglu_gemm_bwd(E, offsets.data_ptr(), A.data_ptr(),
+                                              Wfused.data_ptr(), dY.data_ptr(), dH.data_ptr(),
+                                              M, N, K, code, _stream(dH))
+    _check(st, "sg_grouped_swiglu_gemm_bwd")
+    return dH
+
+
+# ------------------------------------------------- microscaled 4-bit floating point
+def mxfp4_shapes(rows: int, cols: int):
+    """(bytes of a row of codes, bytes of the scales) of a rows x cols matrix."""
+    return -(-cols // 32) * 16, -(-rows // 32) * -(-cols // 256) * 256
+
+
+def _mx_float(t, name: str) -> int:
+    code = _dtype_code(t)
+    if code == SG_F8E4M3:
+        raise TypeError("%s must be fp32, fp16 or bf16" % name)
+    return code
+
+
+def _mx_matrices(t, name: str):
+    """(batch, rows, cols, leading dimension, stride) of a 2-D or 3-D tensor."""
+    if t.dim() == 2:
+        r, c = t.shape
+        return 1, r, c, _rows(t, name, c), 0
+    ld, stride = _stack(t, name, False)
+    return t.shape[0], t.shape[1], t.shape[2], ld, stride
+
+
+def _mx_pair(codes, scales, name: str, rows: int, cols: int, batch=None):
+    import torch
+    nb, ns = mxfp4_shapes(rows, cols)
+    lead = () if batch is None else (batch,)
+    for t, what, shape in ((codes, "codes", lead + (rows, nb)), (scales, "scales", lead + (ns,))):
+        if t.dtype != torch.uint8:
+            raise TypeError("%s: %s must be uint8" % (name, what))
+        _contig(t, "%s: %s" % (name, what), shape)
+
+
+def mxfp4_quantize(X, codes=None, scales=None, values=None):
+    """X [rows, K] or [batch, rows, K] (fp32, fp16 or bf16; rows may be strided) as e2m1 codes
+    and e8m0 scales in blocks of 32: returns (codes [.., rows, 16*ceil(K/32)], scales [.., S]),
+    both uint8, S and the scales' tiles as in include/swiglu_gemm.h (mxfp4_shapes).  values: a
+    contiguous tensor like X that gets the values they stand for; codes and scales are then
+    written only where given, and (codes, scales) may be (None, None)."""
+    import torch
+    code = _mx_float(X, "X")
+    if X.dim() not in (2, 3):
+        raise ValueError("X must be 2-D or 3-D")
+    batch, M, K, ld, stride = _mx_matrices(X, "X")
+    nb, ns = mxfp4_shapes(M, K)
+    lead = tuple(X.shape[:-2])
+    if values is not None:
+        if values.dtype != X.dtype:
+            raise TypeError("values must have X's dtype")
+        _contig(values, "values", X.shape)
+    else:
+        if codes is None:
+            codes = torch.empty(lead + (M, nb), dtype=torch.uint8, device=X.device)
+        if scales is None:
+            scales = torch.empty(lead + (ns,), dtype=torch.uint8, device=X.device)
+    for t, what, shape in ((codes, "codes", lead + (M, nb)), (scales, "scales", lead + (ns,))):
+        if t is not None:
+            if t.dtype != torch.uint8:
+                raise TypeError("%s must be uint8" % what)
+            _contig(t, what, shape)
+    ptr = [t.data_ptr() if t is not None else None for t in (codes, scales, values)]
+    with _same_device(X, codes, scales, values):
+        st = lib().sg_mxfp4_quantize(X.data_ptr(), ld, stride, batch, M, K, code, *ptr,
+                                     _stream(X))
+    _check(st, "sg_mxfp4_quantize")
+    return codes, scales
+
+
+def mxfp4_dequantize(codes, scales, X):
+    """X [rows, K] or [batch, rows, K] = the values of codes and scales, in place on X (fp32,
+    fp16 or bf16, rounded once; rows may be strided)."""
+    code = _mx_float(X, "X")
+    if X.dim() not in (2, 3):
+        raise ValueError("X must be 2-D or 3-D")
+    batch, M, K, ld, stride = _mx_matrices(X, "X")
+    if X.dim() == 3:
+        _stack(X, "X", True)
+    _mx_pair(codes, scales, "the matrix", M, K, batch if X.dim() == 3 else None)
+    with _same_device(codes, scales, X):
+        st = lib().sg_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), batch, M, K,
+                                       X.data_ptr(), ld, stride, code,
+                                       _stream(X))
+    _check(st, "sg_mxfp4_dequantize")
+    return X
+
+
+def mxfp4_tile_scales(S):
+    """Scales stored as rows of bytes, S [rows, blocks] or [batch, rows, blocks] uint8, in the
+    tiles that mxfp4_gemm reads."""
+    import torch
+    if S.dtype != torch.uint8:
+        raise TypeError("scales must be uint8")
+    if S.dim() not in (2, 3):
+        raise ValueError("scales must be 2-D or 3-D")
+    batch, M, nb, ld, stride = _mx_matrices(S, "scales")
+    out = torch.empty(tuple(S.shape[:-2]) + (mxfp4_shapes(M, 32 * nb)[1],), dtype=torch.uint8,
+                      device=S.device)
+    with _same_device(S):
+        st = lib().sg_mxfp4_tile_scales(S.data_ptr(), ld, stride, batch, M, nb, out.data_ptr(),
+                                        _stream(S))
+    _check(st, "sg_mxfp4_tile_scales")
+    return out
+
+
+def _mx_product(A, As, B, Bs, offsets, out, rows_of_b):
+    """Checks of a 4-bit product: (experts, M, K) with K in whole blocks; rows_of_b: B's rows
+    for out's columns."""
+    import torch
+    if A.dim() != 2 or out.dim() != 2:
+        raise ValueError("A and the output must be 2-D")
+    E = 1
+    if offsets is not None:
+        if B.dim() != 3:
+            raise ValueError("with offsets the weight must be 3-D, one matrix for each expert")
+        E = B.shape[0]
+        _experts(offsets, E)
+    elif B.dim() != 2:
+        raise ValueError("without offsets the weight must be 2-D")
+    M, row = A.shape
+    if row % 16 or B.shape[-1] != row:
+        raise ValueError("the rows of codes must be of one length, whole blocks of 16 bytes")
+    K = row * 2
+    _mx_pair(A, As, "A", M, K)
+    _mx_pair(B, Bs, "the weight", rows_of_b, K, E if offsets is not None else None)
+    if out.shape[0] != M:
+        raise ValueError("the output has %d rows, A %d" % (out.shape[0], M))
+    for t, name in ((A, "A"), (B, "the weight's codes")):
+        if t.data_ptr() % 16:
+            raise ValueError("%s must be 16-byte aligned" % name)
+    for t in (As, Bs):
+        if t.data_ptr() % 4:
+            raise ValueError("scales must be 4-byte aligned")
+    return E, M, K
+
+
+def mxfp4_gemm(A, As, B, Bs, C, offsets=None, alpha: float = 1.0):
+    """C = alpha * A @ B^T of two matrices held as (codes, scales): A [M, K], B [N, K]; C [M, N]
+    fp32, fp16 or bf16, rows may be strided.  With offsets, B [experts, N, K] and the rows of
+    each expert meet its own matrix; rows of no expert stay as they are."""
+    code = _mx_float(C, "C")
+    if C.dim() != 2:
+        raise ValueError("A and the output must be 2-D")
+    N = C.shape[1]
+    E, M, K = _mx_product(A, As, B, Bs, offsets, C, N)
+    ldc = _rows(C, "C", N)
+    with _same_device(A, As, B, Bs, C, offsets):
+        st = lib().sg_mxfp4_gemm(E, offsets.data_ptr() if offsets is not None else None, M, N, K,
+                                 float(alpha), A.data_ptr(), As.data_ptr(), B.data_ptr(),
+                                 Bs.data_ptr(), C.data_ptr(), ldc, code, _stream(C))
+    _check(st, "sg_mxfp4_gemm")
+    return C
+
+
+def mxfp4_swiglu_gemm(A, As, W, Ws, Y, offsets=None):
+    """Y = SiLU(A @ W1^T) * (A @ W2^T) from W [2N, K] held as (codes, scales) with gate and up
+    rows interleaved (torch.stack((W1, W2), 1).flatten(0, 1) before quantising); Y [M, N]
+    contiguous, fp16 or bf16.  offsets as mxfp4_gemm."""
+    code = _dtype_code(Y)
+    if code not in (SG_F16, SG_BF16):
+        raise TypeError("Y must be fp16 or bf16")
+    if Y.dim() != 2:
+        raise ValueError("A and the output must be 2-D")
+    N = Y.shape[1]
+    E, M, K = _mx_product(A, As, W, Ws, offsets, Y, 2 * N)
+    _contig(Y, "Y", (M, N))
+    with _same_device(A, As, W, Ws, Y, offsets):
+        st = lib().sg_mxfp4_swiglu_gemm(E, offsets.data_ptr() if offsets is not None else None,
+                                        M, N, K, A.data_ptr(), As.data_ptr(), W.data_ptr(),
+                                        Ws.data_ptr(), Y.data_ptr(), code, _stream(Y))
+    _check(st, "sg_mxfp4_swiglu_gemm")
     return Y

@@ -18,9 +18,9 @@ LIB = os.path.join(HERE, "libswiglu_gemm.so")
 # MFMA ceiling that bench.py --mfma-ceiling reports
 DIAG_SRC = os.path.join(HERE, "diag", "mfma_loop.hip")
 DIAG_LIB = os.path.join(HERE, "libswiglu_gemm_diag.so")
-SOURCES = ["api.hip"] + ["inst_%s_%s.hip" % (d, t) for d in ("f16", "bf16", "e4m3")
+SOURCES = ["api.hip", "api_experts.hip", "inst_mx4.hip"] + ["inst_%s_%s.hip" % (d, t) for d in ("f16", "bf16", "e4m3")
                         for t in ("nn", "nt", "tn", "tt")] + \
-    ["inst_decode_%s.hip" % d for d in ("f16", "bf16", "e4m3")]
+    ["inst_%s_%s.hip" % (k, d) for k in ("decode", "grouped") for d in ("f16", "bf16", "e4m3")]
 ARCH = "gfx950"
 
 

@@ -1148,6 +1148,13 @@ int check_gemm(char transA, char transB, int64_t M, int64_t N, int64_t K, float 
 
 }  // namespace
 
+namespace sg {
+// the description sg_last_config() returns, for the entry points of api_experts.hip
+void set_last_config(const char* text) {
+    std::snprintf(g_last_cfg, sizeof(g_last_cfg), "%s", text);
+}
+}  // namespace sg
+
 extern "C" {
 
 int sg_gemm(char transA, char transB, int64_t M, int64_t N, int64_t K, float alpha,

@@ -1,0 +1,417 @@
+// api_experts.hip -- the C ABI of the products grouped by expert and of microscaled 4-bit
+// floating point: argument checks, kernel choice and launches on the caller's stream.
+// Declarations and contracts are in include/swiglu_gemm.h.  Nothing here allocates or keeps
+// a workspace.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+
+#include "grouped.hpp"
+#include "mx4.hpp"
+#include "swiglu_gemm.h"
+
+using namespace sg;
+
+namespace sg {
+void set_last_config(const char* text);   // api.hip
+}
+
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t)1 << 30;
+constexpr int64_t kMaxExperts = (int64_t)1 << 16;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;   // work-groups of one launch
+
+bool aligned(const void* p, int bytes) { return ((uintptr_t)p % bytes) == 0; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int status_of(hipError_t e) { return e == hipSuccess ? 0 : (int)e; }
+bool finite_positive(float x) { return std::isfinite(x) && x > 0.0f; }
+
+// Upper bound of the tiles of bm rows that `experts` runs of M rows in all can have: every
+// run that is not empty rounds up once.
+int64_t most_row_tiles(int64_t M, int64_t experts, int bm) {
+    const int64_t runs = experts < M ? experts : M;
+    return (M + runs * (bm - 1)) / bm;
+}
+
+template <typename... A>
+void describe(const char* format, A... args) {
+    char text[160];
+    std::snprintf(text, sizeof(text), format, args...);
+    set_last_config(text);
+}
+
+hipError_t launch_dt(int dtype, int epi, bool ta, bool tb, int cfg, const GroupedParams& q,
+                     int64_t blocks, hipStream_t st) {
+    if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
+    const unsigned b = (unsigned)blocks;
+    if (dtype == SG_F16) return launch_grouped<DT_F16>(epi, ta, tb, cfg, q, b, st);
+    if (dtype == SG_BF16) return launch_grouped<DT_BF16>(epi, ta, tb, cfg, q, b, st);
+    return launch_grouped<DT_E4M3>(epi, ta, tb, cfg, q, b, st);
+}
+
+// Products over the rows of each expert: chooses the tile and launches.
+int run_rows(const char* what, int epi, bool tb, int dtype, GroupedParams q, hipStream_t st) {
+    const int64_t M = q.rows, N = q.g.N;
+    q.g.group_m = 4;
+    q.g.tiles_n = (int)cdiv(N, 64);
+    describe("%s any 64x64x32", what);
+    return status_of(launch_dt(dtype, epi, false, tb, -1, q,
+                               most_row_tiles(M, q.experts, 64) * q.g.tiles_n, st));
+}
+
+int run_depth(const char* what, int epi, int dtype, GroupedParams q, hipStream_t st) {
+    q.g.group_m = 4;
+    q.g.tiles_m = (int)cdiv(q.g.M, 64);
+    q.g.tiles_n = (int)cdiv(q.g.N, 64);
+    describe("%s any 64x64x32", what);
+    return status_of(launch_dt(dtype, epi, true, false, -1, q,
+                               (int64_t)q.experts * q.g.tiles_m * q.g.tiles_n, st));
+}
+
+int run_mx4(const char* what, int epi, int dtype, MxParams x, hipStream_t st) {
+    GroupedParams& q = x.q;
+    q.g.group_m = 4;
+    q.g.tiles_n = (int)cdiv(q.g.N, 128);
+    const int64_t blocks = (q.offsets ? most_row_tiles(q.rows, q.experts, 32) : cdiv(q.rows, 32)) *
+                           q.g.tiles_n;
+    if (blocks > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
+    describe("%s any 32x128", what);
+    return status_of(launch_mx4(epi, dtype == SG_F16 ? DT_F16 : DT_BF16, -1, x, (unsigned)blocks,
+                                st));
+}
+
+}  // namespace
+
+extern "C" {
+
+int sg_grouped_gemm(char transB, int64_t experts, const int32_t* offsets, int64_t M, int64_t N,
+                    int64_t K, float alpha, const float* scale, const void* A, int64_t lda,
+                    const void* B, int64_t ldb, int64_t strideB, float beta, void* C,
+                    int64_t ldc, int dtype, void* stream) {
+    const bool tb = transB == 'T' || transB == 't';
+    if (!tb && transB != 'N' && transB != 'n') return -1;
+    if (experts < 1 || experts > kMaxExperts) return -2;
+    if (!offsets) return -3;
+    if (M < 0 || M > kMaxDim) return -4;
+    if (N < 0 || N > kMaxDim) return -5;
+    if (K < 0 || K > kMaxDim) return -6;
+    const bool reads = M > 0 && N > 0 && K > 0 && alpha != 0.0f;
+    if (reads && !A) return -9;
+    if (lda < (K > 1 ? K : 1)) return -10;
+    if (reads && !B) return -11;
+    const int64_t brow = tb ? K : N;
+    if (ldb < (brow > 1 ? brow : 1)) return -12;
+    if (strideB < 0) return -13;
+    if (M > 0 && N > 0 && !C) return -15;
+    if (ldc < (N > 1 ? N : 1)) return -16;
+    if (dtype != SG_F16 && dtype != SG_BF16 && dtype != SG_F8E4M3) return -17;
+    if (M == 0 || N == 0) return 0;
+    const int esz = dtype == SG_F8E4M3 ? 1 : 2;
+    GroupedParams q{};
+    q.g.A = static_cast<const uint16_t*>(A);
+    q.g.B = static_cast<const uint16_t*>(B);
+    q.g.C = C;
+    q.g.lda = lda;
+    q.g.ldb = ldb;
+    q.g.ldc = ldc;
+    q.g.N = (int)N;
+    q.g.K = alpha == 0.0f ? 0 : (int)K;
+    q.g.alpha = alpha;
+    q.g.beta = beta;
+    q.offsets = offsets;
+    q.scale = scale;
+    q.experts = (int)experts;
+    q.rows = (int)M;
+    q.sB = strideB * esz;
+    return run_rows("grouped_gemm", EPI_GEMM, tb, dtype, q, static_cast<hipStream_t>(stream));
+}
+
+int sg_grouped_gemm_wgrad(int64_t experts, const int32_t* offsets, int64_t M, int64_t N,
+                          int64_t K, float alpha, const void* A, int64_t lda, const void* D,
+                          int64_t ldd, float beta, void* C, int64_t ldc, int64_t strideC,
+                          int dtype, int c_dtype, void* stream) {
+    if (experts < 1 || experts > kMaxExperts) return -1;
+    if (!offsets) return -2;
+    if (M < 0 || M > kMaxDim) return -3;
+    if (N < 0 || N > kMaxDim) return -4;
+    if (K < 0 || K > kMaxDim) return -5;
+    const bool reads = M > 0 && N > 0 && K > 0 && alpha != 0.0f;
+    if (reads && !A) return -7;
+    if (lda < (K > 1 ? K : 1)) return -8;
+    if (reads && !D) return -9;
+    if (ldd < (N > 1 ? N : 1)) return -10;
+    if (N > 0 && K > 0 && !C) return -12;
+    if (ldc < (N > 1 ? N : 1)) return -13;
+    if (experts > 1 && N > 0 && K > 0 && strideC < (K - 1) * ldc + N) return -14;
+    if (dtype != SG_F16 && dtype != SG_BF16) return -15;
+    if (c_dtype != dtype && c_dtype != SG_F32) return -16;
+    if (N == 0 || K == 0) return 0;
+    const bool f32 = c_dtype == SG_F32;
+    GroupedParams q{};
+    q.g.A = static_cast<const uint16_t*>(A);
+    q.g.B = static_cast<const uint16_t*>(D);
+    q.g.C = C;
+    q.g.lda = lda;
+    q.g.ldb = ldd;
+    q.g.ldc = ldc;
+    q.g.M = (int)K;
+    q.g.N = (int)N;
+    q.g.alpha = alpha;
+    q.g.beta = beta;
+    q.offsets = offsets;
+    q.experts = (int)experts;
+    q.rows = reads ? (int)M : 0;      // nothing is summed, and nothing read, past row 0
+    q.sC = strideC * (f32 ? 4 : 2);
+    return run_depth("grouped_wgrad", f32 ? EPI_GEMM_F32 : EPI_GEMM, dtype, q,
+                     static_cast<hipStream_t>(stream));
+}
+
+int sg_grouped_swiglu_gemm(int64_t experts, const int32_t* offsets, const void* A,
+                           const void* Wfused, void* Y, int64_t M, int64_t N, int64_t K,
+                           int dtype, float alpha, const float* scale, void* stream) {
+    if (experts < 1 || experts > kMaxExperts) return -1;
+    if (!offsets) return -2;
+    const bool reads = M > 0 && N > 0 && K > 0;
+    if (reads && !A) return -3;
+    if (reads && !Wfused) return -4;
+    if (M > 0 && N > 0 && !Y) return -5;
+    if (M < 0 || M > kMaxDim) return -6;
+    if (N < 0 || N > kMaxDim / 2) return -7;
+    if (K < 0 || K > kMaxDim) return -8;
+    if (dtype != SG_F16 && dtype != SG_BF16 && dtype != SG_F8E4M3) return -9;
+    if (!finite_positive(alpha) || (dtype != SG_F8E4M3 && alpha != 1.0f)) return -10;
+    if (scale && dtype != SG_F8E4M3) return -11;
+    if (M == 0 || N == 0) return 0;
+    GroupedParams q{};
+    q.g.A = static_cast<const uint16_t*>(A);
+    q.g.B = static_cast<const uint16_t*>(Wfused);
+    q.g.C = Y;
+    q.g.lda = K;
+    q.g.ldb = 2 * N;
+    q.g.ldc = N;
+    q.g.N = (int)(2 * N);
+    q.g.K = (int)K;
+    q.g.alpha = alpha;
+    q.g.epi_flags = aligned(Y, 16) && N % 8 == 0 ? EPI_Y16 : 0;
+    q.offsets = offsets;
+    q.scale = scale;
+    q.experts = (int)experts;
+    q.rows = (int)M;
+    q.sB = K * 2 * N * (dtype == SG_F8E4M3 ? 1 : 2);
+    return run_rows("grouped_swiglu", EPI_SWIGLU, false, dtype, q,
+                    static_cast<hipStream_t>(stream));
+}
+
+int sg_grouped_swiglu_gemm_bwd(int64_t experts, const int32_t* offsets, const void* A,
+                               const void* Wfused, const void* dY, void* dH, int64_t M,
+                               int64_t N, int64_t K, int dtype, void* stream) {
+    if (experts < 1 || experts > kMaxExperts) return -1;
+    if (!offsets) return -2;
+    const bool reads = M > 0 && N > 0 && K > 0;
+    if (reads && !A) return -3;
+    if (reads && !Wfused) return -4;
+    if (M > 0 && N > 0 && !dY) return -5;
+    if (M > 0 && N > 0 && !dH) return -6;
+    if (M < 0 || M > kMaxDim) return -7;
+    if (N < 0 || N > kMaxDim / 2) return -8;
+    if (K < 0 || K > kMaxDim) return -9;
+    if (dtype != SG_F16 && dtype != SG_BF16) return -10;
+    if (M == 0 || N == 0) return 0;
+    GroupedParams q{};
+    q.g.A = static_cast<const uint16_t*>(A);
+    q.g.B = static_cast<const uint16_t*>(Wfused);
+    q.g.C = dH;
+    q.g.lda = K;
+    q.g.ldb = 2 * N;
+    q.g.ldc = 2 * N;
+    q.g.N = (int)(2 * N);
+    q.g.K = (int)K;
+    q.g.alpha = 1.0f;
+    q.offsets = offsets;
+    q.dY = dY;
+    q.experts = (int)experts;
+    q.rows = (int)M;
+    q.sB = K * 2 * N * 2;
+    return run_rows("grouped_swiglu_bwd", EPI_SWIGLU_BWD, false, dtype, q,
+                    static_cast<hipStream_t>(stream));
+}
+
+int sg_mxfp4_quantize(const void* X, int64_t ldx, int64_t strideX, int64_t batch, int64_t M,
+                      int64_t K, int dtype, void* codes, void* scales, void* values,
+                      void* stream) {
+    if (M > 0 && K > 0 && batch > 0 && !X) return -1;
+    if (ldx < (K > 1 ? K : 1)) return -2;
+    if (strideX < 0) return -3;
+    if (batch < 0 || batch > 65535) return -4;
+    if (M < 0 || M > kMaxDim) return -5;
+    if (K < 0 || K > kMaxDim) return -6;
+    if (dtype < SG_F32 || dtype > SG_BF16) return -7;
+    if (!codes && !scales && !values) return -8;
+    if (!aligned(codes, 4)) return -8;
+    if (!aligned(scales, 4)) return -9;
+    if (batch == 0 || M == 0 || K == 0) return 0;
+    const int64_t blocks = cdiv(M, 32) * mx_tiles_k(K);
+    if (blocks > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
+    const int esz = dtype == SG_F32 ? 4 : 2;
+    MxQuantParams p{};
+    p.X = X;
+    p.codes = static_cast<uint8_t*>(codes);
+    p.scales = static_cast<uint8_t*>(scales);
+    p.values = values;
+    p.ldx = ldx;
+    p.ldv = K;
+    p.sX = strideX * esz;
+    p.sV = M * K * esz;
+    p.M = (int)M;
+    p.K = (int)K;
+    p.vec_x = aligned(X, 16) && ldx * esz % 16 == 0 && p.sX % 16 == 0;
+    p.vec_v = aligned(values, 16) && K * esz % 16 == 0;
+    const dim3 grid((unsigned)blocks, 1, (unsigned)batch);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    describe("mxfp4_quantize %lld tiles", (long long)blocks);
+    if (dtype == SG_F32)
+        hipLaunchKernelGGL(mx_quantize_kernel<DT_F32>, grid, dim3(256), 0, st, p);
+    else if (dtype == SG_F16)
+        hipLaunchKernelGGL(mx_quantize_kernel<DT_F16>, grid, dim3(256), 0, st, p);
+    else
+        hipLaunchKernelGGL(mx_quantize_kernel<DT_BF16>, grid, dim3(256), 0, st, p);
+    return status_of(hipGetLastError());
+}
+
+int sg_mxfp4_dequantize(const void* codes, const void* scales, int64_t batch, int64_t M,
+                        int64_t K, void* X, int64_t ldx, int64_t strideX, int dtype,
+                        void* stream) {
+    const bool any = batch > 0 && M > 0 && K > 0;
+    if (any && (!codes || !aligned(codes, 4))) return -1;
+    if (any && !scales) return -2;
+    if (batch < 0 || batch > 65535) return -3;
+    if (M < 0 || M > kMaxDim) return -4;
+    if (K < 0 || K > kMaxDim) return -5;
+    if (any && !X) return -6;
+    if (ldx < (K > 1 ? K : 1)) return -7;
+    if (strideX < 0 || (batch > 1 && any && strideX < (M - 1) * ldx + K)) return -8;
+    if (dtype < SG_F32 || dtype > SG_BF16) return -9;
+    if (!any) return 0;
+    const int64_t blocks = cdiv(M, 32) * mx_tiles_k(K);
+    if (blocks > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
+    const int esz = dtype == SG_F32 ? 4 : 2;
+    MxQuantParams p{};
+    p.codes = const_cast<uint8_t*>(static_cast<const uint8_t*>(codes));
+    p.scales = const_cast<uint8_t*>(static_cast<const uint8_t*>(scales));
+    p.values = X;
+    p.ldv = ldx;
+    p.sV = strideX * esz;
+    p.M = (int)M;
+    p.K = (int)K;
+    p.vec_v = aligned(X, 16) && ldx * esz % 16 == 0 && p.sV % 16 == 0;
+    const dim3 grid((unsigned)blocks, 1, (unsigned)batch);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    describe("mxfp4_dequantize %lld tiles", (long long)blocks);
+    if (dtype == SG_F32)
+        hipLaunchKernelGGL(mx_dequantize_kernel<DT_F32>, grid, dim3(256), 0, st, p);
+    else if (dtype == SG_F16)
+        hipLaunchKernelGGL(mx_dequantize_kernel<DT_F16>, grid, dim3(256), 0, st, p);
+    else
+        hipLaunchKernelGGL(mx_dequantize_kernel<DT_BF16>, grid, dim3(256), 0, st, p);
+    return status_of(hipGetLastError());
+}
+
+int sg_mxfp4_tile_scales(const void* src, int64_t ld, int64_t stride, int64_t batch, int64_t M,
+                         int64_t blocks, void* dst, void* stream) {
+    const bool any = batch > 0 && M > 0 && blocks > 0;
+    if (any && !src) return -1;
+    if (ld < (blocks > 1 ? blocks : 1)) return -2;
+    if (stride < 0) return -3;
+    if (batch < 0 || batch > 65535) return -4;
+    if (M < 0 || M > kMaxDim) return -5;
+    if (blocks < 0 || blocks > kMaxDim / kMxBlock) return -6;
+    if (any && (!dst || !aligned(dst, 4))) return -7;
+    if (!any) return 0;
+    const int64_t work = cdiv(cdiv(M, 32) * cdiv(blocks, 8) * (kMxTileBytes / 4), 256);
+    const dim3 grid((unsigned)(work < 8192 ? work : 8192), 1, (unsigned)batch);
+    describe("mxfp4_tile_scales");
+    hipLaunchKernelGGL(mx_tile_scales_kernel, grid, dim3(256), 0,
+                       static_cast<hipStream_t>(stream), static_cast<const uint8_t*>(src), ld,
+                       stride, static_cast<uint8_t*>(dst), (int)M, (int)blocks);
+    return status_of(hipGetLastError());
+}
+
+int sg_mxfp4_gemm(int64_t experts, const int32_t* offsets, int64_t M, int64_t N, int64_t K,
+                  float alpha, const void* A, const void* As, const void* B, const void* Bs,
+                  void* C, int64_t ldc, int dtype, void* stream) {
+    if (experts < 1 || experts > kMaxExperts) return -1;
+    if (!offsets && experts != 1) return -2;
+    if (M < 0 || M > kMaxDim) return -3;
+    if (N < 0 || N > kMaxDim) return -4;
+    if (K < 0 || K > kMaxDim) return -5;
+    const bool reads = M > 0 && N > 0 && K > 0 && alpha != 0.0f;
+    if (reads && (!A || !aligned(A, 16))) return -7;
+    if (reads && (!As || !aligned(As, 4))) return -8;
+    if (reads && (!B || !aligned(B, 16))) return -9;
+    if (reads && (!Bs || !aligned(Bs, 4))) return -10;
+    if (M > 0 && N > 0 && !C) return -11;
+    if (ldc < (N > 1 ? N : 1)) return -12;
+    if (dtype < SG_F32 || dtype > SG_BF16) return -13;
+    if (M == 0 || N == 0) return 0;
+    MxParams x{};
+    x.q.g.A = static_cast<const uint16_t*>(A);
+    x.q.g.B = static_cast<const uint16_t*>(B);
+    x.q.g.C = C;
+    x.q.g.lda = x.q.g.ldb = mx_row_bytes(K);
+    x.q.g.ldc = ldc;
+    x.q.g.N = (int)N;
+    x.q.g.K = reads ? (int)mx_blocks(K) : 0;
+    x.q.g.alpha = alpha;
+    x.q.offsets = offsets;
+    x.q.experts = (int)experts;
+    x.q.rows = (int)M;
+    x.q.sB = N * mx_row_bytes(K);
+    x.As = static_cast<const uint8_t*>(As);
+    x.Bs = static_cast<const uint8_t*>(Bs);
+    x.sBs = mx_scale_bytes(N, K);
+    x.tiles_k = (int)mx_tiles_k(K);
+    return run_mx4("mxfp4_gemm", dtype == SG_F32 ? EPI_GEMM_F32 : EPI_GEMM, dtype, x,
+                   static_cast<hipStream_t>(stream));
+}
+
+int sg_mxfp4_swiglu_gemm(int64_t experts, const int32_t* offsets, int64_t M, int64_t N,
+                         int64_t K, const void* A, const void* As, const void* W,
+                         const void* Ws, void* Y, int dtype, void* stream) {
+    if (experts < 1 || experts > kMaxExperts) return -1;
+    if (!offsets && experts != 1) return -2;
+    if (M < 0 || M > kMaxDim) return -3;
+    if (N < 0 || N > kMaxDim / 2) return -4;
+    if (K < 0 || K > kMaxDim) return -5;
+    const bool reads = M > 0 && N > 0 && K > 0;
+    if (reads && (!A || !aligned(A, 16))) return -6;
+    if (reads && (!As || !aligned(As, 4))) return -7;
+    if (reads && (!W || !aligned(W, 16))) return -8;
+    if (reads && (!Ws || !aligned(Ws, 4))) return -9;
+    if (M > 0 && N > 0 && !Y) return -10;
+    if (dtype != SG_F16 && dtype != SG_BF16) return -11;
+    if (M == 0 || N == 0) return 0;
+    MxParams x{};
+    x.q.g.A = static_cast<const uint16_t*>(A);
+    x.q.g.B = static_cast<const uint16_t*>(W);
+    x.q.g.C = Y;
+    x.q.g.lda = x.q.g.ldb = mx_row_bytes(K);
+    x.q.g.ldc = N;
+    x.q.g.N = (int)(2 * N);
+    x.q.g.K = (int)mx_blocks(K);
+    x.q.g.alpha = 1.0f;
+    x.q.g.epi_flags = aligned(Y, 16) && N % 8 == 0 ? EPI_Y16 : 0;
+    x.q.offsets = offsets;
+    x.q.experts = (int)experts;
+    x.q.rows = (int)M;
+    x.q.sB = 2 * N * mx_row_bytes(K);
+    x.As = static_cast<const uint8_t*>(As);
+    x.Bs = static_cast<const uint8_t*>(Ws);
+    x.sBs = mx_scale_bytes(2 * N, K);
+    x.tiles_k = (int)mx_tiles_k(K);
+    return run_mx4("mxfp4_swiglu", EPI_SWIGLU, dtype, x, static_cast<hipStream_t>(stream));
+}
+
+}  // extern "C"

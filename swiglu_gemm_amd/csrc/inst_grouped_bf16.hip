@@ -1,0 +1,5 @@
+// bf16 instantiations of the grouped GEMM launchers.
+#include "launch_grouped.hpp"
+namespace sg {
+template hipError_t launch_grouped<DT_BF16>(int, bool, bool, int, const GroupedParams&, unsigned, hipStream_t);
+}

@@ -1,0 +1,5 @@
+// fp16 instantiations of the grouped GEMM launchers.
+#include "launch_grouped.hpp"
+namespace sg {
+template hipError_t launch_grouped<DT_F16>(int, bool, bool, int, const GroupedParams&, unsigned, hipStream_t);
+}
