@@ -7,8 +7,11 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <cstdlib>
 
 #include "grouped.hpp"
+#include "grouped_dma.hpp"
+#include "configs16.hpp"
 #include "mx4.hpp"
 #include "swiglu_gemm.h"
 
@@ -52,22 +55,69 @@ hipError_t launch_dt(int dtype, int epi, bool ta, bool tb, int cfg, const Groupe
     return launch_grouped<DT_E4M3>(epi, ta, tb, cfg, q, b, st);
 }
 
-// Products over the rows of each expert: chooses the tile and launches.
-int run_rows(const char* what, int epi, bool tb, int dtype, GroupedParams q, hipStream_t st) {
-    const int64_t M = q.rows, N = q.g.N;
-    q.g.group_m = 4;
-    q.g.tiles_n = (int)cdiv(N, 64);
-    describe("%s any 64x64x32", what);
-    return status_of(launch_dt(dtype, epi, false, tb, -1, q,
-                               most_row_tiles(M, q.experts, 64) * q.g.tiles_n, st));
+// SG_FORCE_GROUPED=<id>: that tile for every call it can run (-1: the 64 x 64 tiles).
+bool forced_group(int* cfg) {
+    const char* s = std::getenv("SG_FORCE_GROUPED");
+    if (!s || !*s) return false;
+    *cfg = std::atoi(s);
+    return true;
 }
 
-int run_depth(const char* what, int epi, int dtype, GroupedParams q, hipStream_t st) {
+// Whether tile c can run the problem: 16-byte aligned operands, rows and expert strides,
+// DMA-compatible tiles, and every lane's offset from its tile's base below 2^31 bytes.
+bool group_cfg_ok(const GroupCfg& c, bool ta, bool tb, int esz, const GroupedParams& q) {
+    if ((c.e4m3 != 0) != (esz == 1)) return false;
+    if (!aligned(q.g.A, 16) || !aligned(q.g.B, 16)) return false;
+    if (q.g.lda * esz % 16 != 0 || q.g.ldb * esz % 16 != 0 || q.sB % 16 != 0) return false;
+    const int nw = c.WM * c.WN;
+    if (!dma_tile_ok(!ta, c.BM, c.BK, esz, nw) || !dma_tile_ok(tb, c.BN, c.BK, esz, nw))
+        return false;
+    constexpr int64_t kLim = (int64_t)1 << 31;
+    return ((ta ? c.BK : c.BM) * q.g.lda + 256) * esz < kLim &&
+           ((tb ? c.BN : c.BK) * q.g.ldb + 256) * esz < kLim;
+}
+
+int choose_rows(bool tb, int esz, const GroupedParams& q) {
+    int cfg = -1;
+    if (forced_group(&cfg))
+        return cfg >= 0 && cfg < kNumGroupCfg && group_cfg_ok(kGroupCfg[cfg], false, tb, esz, q)
+                   ? cfg
+                   : -1;
+    const int64_t runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
+    cfg = esz == 1 ? (mean <= 32 ? 5 : mean < 256 ? 6 : 8)
+                   : (mean <= 32 ? 0 : mean < 128 ? 1 : mean < 256 ? 2 : 4);
+    return group_cfg_ok(kGroupCfg[cfg], false, tb, esz, q) ? cfg : -1;
+}
+
+int choose_depth(const GroupedParams& q) {
+    int cfg = -1;
+    if (!forced_group(&cfg)) cfg = q.g.M >= 256 && q.g.N >= 256 ? 4 : 2;
+    return cfg >= 2 && cfg <= 4 && group_cfg_ok(kGroupCfg[cfg], true, false, 2, q) ? cfg : -1;
+}
+
+// Products over the rows of each expert: chooses the tile and launches.
+int run_rows(const char* what, int epi, bool tb, int dtype, GroupedParams q, hipStream_t st) {
+    const int esz = dtype == SG_F8E4M3 ? 1 : 2;
+    const int cfg = q.g.K > 0 ? choose_rows(tb, esz, q) : -1;
+    const int bm = cfg < 0 ? 64 : kGroupCfg[cfg].BM, bn = cfg < 0 ? 64 : kGroupCfg[cfg].BN;
     q.g.group_m = 4;
-    q.g.tiles_m = (int)cdiv(q.g.M, 64);
-    q.g.tiles_n = (int)cdiv(q.g.N, 64);
-    describe("%s any 64x64x32", what);
-    return status_of(launch_dt(dtype, epi, true, false, -1, q,
+    q.g.tiles_n = (int)cdiv(q.g.N, bn);
+    q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0;
+    describe("%s cfg=%d %s", what, cfg, cfg < 0 ? "any 64x64x32" : kGroupCfg[cfg].name);
+    return status_of(launch_dt(dtype, epi, false, tb, cfg, q,
+                               most_row_tiles(q.rows, q.experts, bm) * q.g.tiles_n, st));
+}
+
+// Products that sum over the rows of each expert.
+int run_depth(const char* what, int epi, int dtype, GroupedParams q, hipStream_t st) {
+    const int cfg = q.rows > 0 ? choose_depth(q) : -1;
+    const int bm = cfg < 0 ? 64 : kGroupCfg[cfg].BM, bn = cfg < 0 ? 64 : kGroupCfg[cfg].BN;
+    q.g.group_m = 4;
+    q.g.tiles_m = (int)cdiv(q.g.M, bm);
+    q.g.tiles_n = (int)cdiv(q.g.N, bn);
+    q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0 && q.sC % 8 == 0;
+    describe("%s cfg=%d %s", what, cfg, cfg < 0 ? "any 64x64x32" : kGroupCfg[cfg].name);
+    return status_of(launch_dt(dtype, epi, true, false, cfg, q,
                                (int64_t)q.experts * q.g.tiles_m * q.g.tiles_n, st));
 }
 

@@ -1,0 +1,224 @@
+// grouped_dma.hpp -- the grouped products on the direct-to-LDS tile loop of
+// gemm16_dma.hpp: a work-group finds its item (grouped.hpp) and runs the loop and the
+// epilogue on the expert's own problem.  Operands 16-byte aligned, rows and expert strides
+// 16-byte multiples.
+#pragma once
+
+#include "gemm16_dma.hpp"
+#include "grouped.hpp"
+
+namespace sg {
+
+// C in fp32: C = alpha * acc + beta * C_old.  As epilogue_gemm_rows_beta_lds, with 16-byte
+// pieces of four outputs: one 32-row block of every wave row and CW wave columns at a time
+// pass through LDS, so that C is read and written along its rows.
+template <int FM, int FN, int BM, int BN, int WN, int NT, int LDSB>
+__device__ __forceinline__ void epilogue_f32_rows_lds(const Gemm16Params& p, f32x16 (&acc)[FN][FM],
+                                                      char* smem, int m0, int n0, int rb, int wn,
+                                                      int lane) {
+    constexpr int TN = BN / WN, CW = staged_wave_cols<BM, BN, FM, WN, LDSB, 0>();
+    static_assert(CW > 0, "one wave column of fp32 rows fits the LDS ring");
+    constexpr int TS = CW * TN, ROW = 4 * TS + 16, CPR = TS / 4;
+    constexpr int PB = BM / (32 * FM) * 32 * CPR;
+    const int lm = lane & 31, lq = (lane >> 5) * 4, wr = rb / (32 * FM);
+    const float alpha = p.alpha, beta = p.beta;
+    float* C = reinterpret_cast<float*>(p.C);
+    const bool vec = (reinterpret_cast<uintptr_t>(C) & 15) == 0 && (p.ldc & 3) == 0;
+#pragma unroll
+    for (int tm = 0; tm < FM; ++tm) {
+#pragma unroll
+        for (int h = 0; h < WN / CW; ++h) {
+            __syncthreads();
+            if (wn / CW == h) {
+                char* row = smem + (wr * 32 + lm) * ROW + 4 * (wn % CW) * TN;
+#pragma unroll
+                for (int tn = 0; tn < FN; ++tn)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        *reinterpret_cast<f32x4*>(row + 4 * (tn * 32 + 8 * g + lq)) =
+                            f32x4{alpha * acc[tn][tm][4 * g], alpha * acc[tn][tm][4 * g + 1],
+                                  alpha * acc[tn][tm][4 * g + 2], alpha * acc[tn][tm][4 * g + 3]};
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < PB; i += NT) {
+                const int rr = i / CPR, c = i - rr * CPR;
+                const int m = m0 + (rr >> 5) * (32 * FM) + tm * 32 + (rr & 31);
+                const int n = n0 + h * TS + c * 4;
+                if (m >= p.M || n >= p.N) continue;
+                f32x4 v = *reinterpret_cast<const f32x4*>(smem + rr * ROW + c * 16);
+                float* cp = C + (int64_t)m * p.ldc + n;
+                if (vec && n + 4 <= p.N) {
+                    if (beta != 0.0f) {
+                        const f32x4 old = *reinterpret_cast<const f32x4*>(cp);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(beta, old[e], v[e]);
+                    }
+                    *reinterpret_cast<f32x4*>(cp) = v;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n + e < p.N)
+                            cp[e] = beta != 0.0f ? __builtin_fmaf(beta, cp[e], v[e]) : v[e];
+                }
+            }
+        }
+    }
+}
+
+// The gradient of gate and up from dY, staged the same way: eight interleaved columns (four
+// pairs) a piece meet four values of dY and leave as one 16-byte store.  dy: the expert's
+// first row of dY.
+template <int DT, int FM, int FN, int BM, int BN, int WN, int NT, int LDSB>
+__device__ __forceinline__ void epilogue_swiglu_bwd_lds(const Gemm16Params& p, const uint16_t* dy,
+                                                        f32x16 (&acc)[FN][FM], char* smem, int m0,
+                                                        int n0, int rb, int wn, int lane) {
+    constexpr int TN = BN / WN, CW = staged_wave_cols<BM, BN, FM, WN, LDSB, 0>();
+    static_assert(CW > 0, "one wave column of fp32 rows fits the LDS ring");
+    constexpr int TS = CW * TN, ROW = 4 * TS + 16, CPR = TS / 8;
+    constexpr int PB = BM / (32 * FM) * 32 * CPR;
+    const int lm = lane & 31, lq = (lane >> 5) * 4, wr = rb / (32 * FM);
+    const int nout = p.N >> 1;
+    uint16_t* H = reinterpret_cast<uint16_t*>(p.C);
+    const bool vec = (reinterpret_cast<uintptr_t>(H) & 15) == 0 &&
+                     (reinterpret_cast<uintptr_t>(dy) & 7) == 0 && (nout & 3) == 0;
+#pragma unroll
+    for (int tm = 0; tm < FM; ++tm) {
+#pragma unroll
+        for (int h = 0; h < WN / CW; ++h) {
+            __syncthreads();
+            if (wn / CW == h) {
+                char* row = smem + (wr * 32 + lm) * ROW + 4 * (wn % CW) * TN;
+#pragma unroll
+                for (int tn = 0; tn < FN; ++tn)
+#pragma unroll
+                    for (int g = 0; g < 4; ++g)
+                        *reinterpret_cast<f32x4*>(row + 4 * (tn * 32 + 8 * g + lq)) =
+                            f32x4{acc[tn][tm][4 * g], acc[tn][tm][4 * g + 1],
+                                  acc[tn][tm][4 * g + 2], acc[tn][tm][4 * g + 3]};
+            }
+            __syncthreads();
+            for (int i = threadIdx.x; i < PB; i += NT) {
+                const int rr = i / CPR, c = i - rr * CPR;
+                const int m = m0 + (rr >> 5) * (32 * FM) + tm * 32 + (rr & 31);
+                const int n = n0 + h * TS + c * 8;
+                if (m >= p.M || n >= p.N) continue;
+                const char* src = smem + rr * ROW + c * 32;
+                const f32x4 lo = *reinterpret_cast<const f32x4*>(src);
+                const f32x4 hi = *reinterpret_cast<const f32x4*>(src + 16);
+                const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                const uint16_t* d = dy + (int64_t)m * nout + (n >> 1);
+                uint16_t* out = H + (int64_t)m * p.ldc + n;
+                const bool whole = vec && n + 8 <= p.N;
+                uint16_t dv[4] = {0, 0, 0, 0};
+                if (whole) {
+                    const u32x2 w = *reinterpret_cast<const u32x2*>(d);
+                    dv[0] = (uint16_t)w.x, dv[1] = (uint16_t)(w.x >> 16);
+                    dv[2] = (uint16_t)w.y, dv[3] = (uint16_t)(w.y >> 16);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (n + 2 * j < p.N) dv[j] = d[j];
+                }
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    swiglu_grad(v[2 * j], v[2 * j + 1], to_f32<DT>(dv[j]), o[2 * j], o[2 * j + 1]);
+                if (whole) {
+                    __builtin_nontemporal_store(
+                        u32x4{pack2<DT>(o[0], o[1]), pack2<DT>(o[2], o[3]), pack2<DT>(o[4], o[5]),
+                              pack2<DT>(o[6], o[7])},
+                        reinterpret_cast<u32x4*>(out));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (n + e < p.N) out[e] = from_f32<DT>(o[e]);
+                }
+            }
+        }
+    }
+}
+
+template <int DT, bool TA, bool TB, int EPI, int BM, int BN, int BK, int S, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, 1) grouped_dma_kernel(const GroupedParams q) {
+    using D = DmaShape<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>;
+    __shared__ __attribute__((aligned(1024))) char smem[D::LDS];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    GroupItem it;
+    if constexpr (TA) {
+        if (!find_depth(q, blockIdx.x, it)) return;
+    } else {
+        if (!find_rows<BM>(q, blockIdx.x, lane, it)) return;
+    }
+    const Gemm16Params p = group_problem<TA, D::ESZ, EPI == EPI_GEMM_F32 ? 4 : 2>(q, it);
+    const int m0 = it.tm * BM, n0 = it.tn * BN;
+    const int nkt = p.K / BK, ktail = p.K - nkt * BK;
+
+    typename D::Acc acc;
+#pragma unroll
+    for (int i = 0; i < D::FN; ++i)
+#pragma unroll
+        for (int j = 0; j < D::FM; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+    dma_mainloop<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>(p, smem, m0, n0, 0, nkt, ktail, acc, wave,
+                                                         lane);
+    const int wm = wave % WM, wn = wave / WM;
+    if constexpr (EPI == EPI_GEMM_F32)
+        epilogue_f32_rows_lds<D::FM, D::FN, BM, BN, WN, 64 * WM * WN, D::LDS>(
+            p, acc, smem, m0, n0, wm * D::TM, wn, lane);
+    else if constexpr (EPI == EPI_SWIGLU_BWD)
+        epilogue_swiglu_bwd_lds<D::DT_OUT, D::FM, D::FN, BM, BN, WN, 64 * WM * WN, D::LDS>(
+            p, reinterpret_cast<const uint16_t*>(q.dY) + (int64_t)it.row0 * (p.N >> 1), acc, smem,
+            m0, n0, wm * D::TM, wn, lane);
+    else
+        dma_epilogue<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>(p, acc, smem, m0, n0, wave, lane);
+}
+
+// Tiles of the grouped products: those of the plain ones that suit runs of rows of every
+// length.  Index = configuration id (SG_FORCE_GROUPED=<id> overrides the choice; -1: the
+// kernel for every alignment).
+struct GroupCfg {
+    int e4m3, BM, BN, BK, S, WM, WN;
+    const char* name;
+};
+constexpr GroupCfg kGroupCfg[] = {
+    {0, 32, 128, 64, 4, 1, 4, "32x128x64 s4 1x4w"},
+    {0, 64, 128, 64, 4, 1, 4, "64x128x64 s4 1x4w"},
+    {0, 128, 128, 64, 2, 2, 4, "128x128x64 s2 2x4w"},
+    {0, 128, 256, 64, 3, 2, 4, "128x256x64 s3 2x4w"},
+    {0, 256, 256, 64, 2, 4, 2, "256x256x64 s2 4x2w"},
+    {1, 32, 128, 128, 4, 1, 4, "e4m3 32x128x128 s4 1x4w"},
+    {1, 128, 128, 128, 2, 2, 4, "e4m3 128x128x128 s2 2x4w"},
+    {1, 128, 256, 128, 3, 2, 4, "e4m3 128x256x128 s3 2x4w"},
+    {1, 256, 256, 128, 2, 4, 2, "e4m3 256x256x128 s2 4x2w"},
+};
+constexpr int kNumGroupCfg = sizeof(kGroupCfg) / sizeof(kGroupCfg[0]);
+
+#define SG_GROUPED_16(X)          \
+    X(0, 32, 128, 64, 4, 1, 4)    \
+    X(1, 64, 128, 64, 4, 1, 4)    \
+    X(2, 128, 128, 64, 2, 2, 4)   \
+    X(3, 128, 256, 64, 3, 2, 4)   \
+    X(4, 256, 256, 64, 2, 4, 2)
+// products that sum over the rows: a transposed A's 32- and 64-row tiles are too narrow
+#define SG_GROUPED_DEPTH(X)       \
+    X(2, 128, 128, 64, 2, 2, 4)   \
+    X(3, 128, 256, 64, 3, 2, 4)   \
+    X(4, 256, 256, 64, 2, 4, 2)
+#define SG_GROUPED_8(X)           \
+    X(5, 32, 128, 128, 4, 1, 4)   \
+    X(6, 128, 128, 128, 2, 2, 4)  \
+    X(7, 128, 256, 128, 3, 2, 4)  \
+    X(8, 256, 256, 128, 2, 4, 2)
+
+#define SG_GROUP_ROW(ID, BM_, BN_, BK_, S_, WM_, WN_)                                          \
+    static_assert(kGroupCfg[ID].BM == BM_ && kGroupCfg[ID].BN == BN_ &&                        \
+                      kGroupCfg[ID].BK == BK_ && kGroupCfg[ID].S == S_ &&                      \
+                      kGroupCfg[ID].WM == WM_ && kGroupCfg[ID].WN == WN_,                      \
+                  "grouped row " #ID);
+SG_GROUPED_16(SG_GROUP_ROW)
+SG_GROUPED_DEPTH(SG_GROUP_ROW)
+SG_GROUPED_8(SG_GROUP_ROW)
+#undef SG_GROUP_ROW
+
+}  // namespace sg

@@ -3,14 +3,39 @@
 #pragma once
 
 #include "grouped.hpp"
+#include "grouped_dma.hpp"
 
 namespace sg {
 
 template <int DT, bool TA, bool TB, int EPI>
 hipError_t launch_grouped_epi(int cfg, const GroupedParams& q, unsigned blocks, hipStream_t st) {
-    (void)cfg;
-    hipLaunchKernelGGL((grouped_any_kernel<DT, TA, TB, EPI>), dim3(blocks), dim3(256), 0, st, q);
-    return hipGetLastError();
+    if (cfg < 0) {
+        hipLaunchKernelGGL((grouped_any_kernel<DT, TA, TB, EPI>), dim3(blocks), dim3(256), 0, st,
+                           q);
+        return hipGetLastError();
+    }
+#define SG_GCASE(ID, BM, BN, BK, S, WM, WN)                                                   \
+    case ID:                                                                                  \
+        hipLaunchKernelGGL((grouped_dma_kernel<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>),      \
+                           dim3(blocks), dim3(64 * WM * WN), 0, st, q);                       \
+        return hipGetLastError();
+    if constexpr (DT == DT_E4M3) {
+        switch (cfg) {
+            SG_GROUPED_8(SG_GCASE)
+            default: return hipErrorInvalidValue;
+        }
+    } else if constexpr (TA) {
+        switch (cfg) {
+            SG_GROUPED_DEPTH(SG_GCASE)
+            default: return hipErrorInvalidValue;
+        }
+    } else {
+        switch (cfg) {
+            SG_GROUPED_16(SG_GCASE)
+            default: return hipErrorInvalidValue;
+        }
+    }
+#undef SG_GCASE
 }
 
 template <int DT>

@@ -2,6 +2,8 @@
 length (none, one, odd, longer than a tile), rows that belong to no expert, one expert and
 many, both weight layouts, all operand types, padded and unaligned strides, alpha, beta and
 the experts' scales."""
+import os
+
 import pytest
 
 torch = pytest.importorskip("torch")
@@ -384,3 +386,57 @@ def test_calls_overlap_on_two_streams_and_replay_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(Y, alone[i]) and torch.equal(C, want)
+
+
+# ------------------------------------------------------------------ every tile
+@pytest.fixture
+def force():
+    yield lambda cfg: os.environ.__setitem__("SG_FORCE_GROUPED", str(cfg))
+    os.environ.pop("SG_FORCE_GROUPED", None)
+
+
+def took(cfg):
+    import swiglu_gemm_amd as sg
+    return "cfg=%d " % cfg in sg.last_config()
+
+
+LONG = [1, 0, 257, 64, 130]
+
+
+@pytest.mark.parametrize("cfg", range(5))
+@pytest.mark.parametrize("dtype,trans", [("bf16", "N"), ("f16", "T")])
+def test_every_tile_rows(force, cfg, dtype, trans):
+    """Ragged runs, a K tail, N inside a chunk, C aligned and not, beta."""
+    force(cfg)
+    for N, K, pad, beta in ((328, 200, (0, 0, 0), 0.0), (260, 136, (8, 12 if trans == "N" else 8, 4), 0.5),
+                            (300, 64, (8, 4 if trans == "N" else 8, 3), 0.0),
+                            (512, 512, (0, 0, 0), 0.0)):
+        run_gemm(dtype, trans, LONG, N, K, beta=beta, pad=pad, before=3, behind=5, scaled=True)
+        assert took(cfg)
+    run_swiglu(dtype, LONG, 164, 200, before=3, behind=5)
+    assert took(cfg)
+    run_swiglu(dtype, LONG, 256, 128)
+    run_swiglu(dtype, LONG, 164, 200, bwd=True, before=3, behind=5)
+    assert took(cfg)
+    run_swiglu(dtype, LONG, 256, 128, bwd=True)
+
+
+@pytest.mark.parametrize("cfg", range(5, 9))
+@pytest.mark.parametrize("trans", "NT")
+def test_every_tile_e4m3(force, cfg, trans):
+    force(cfg)
+    for N, K, pad in ((336, 208, (0, 0, 0)), (272, 144, (16, 16, 4))):
+        run_gemm("e4m3", trans, LONG, N, K, pad=pad, before=3, behind=5, scaled=True, beta=0.5)
+        assert took(cfg)
+    run_swiglu("e4m3", LONG, 168, 208, before=3, behind=5, alpha=0.5, scaled=True)
+    assert took(cfg)
+
+
+@pytest.mark.parametrize("cfg", range(2, 5))
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f16", "same")])
+def test_every_tile_depth(force, cfg, dtype, out):
+    force(cfg)
+    for N, K, pad, beta in ((328, 264, (0, 0, 0), 0.0), (260, 300, (4, 4, 4), 0.5),
+                            (512, 512, (0, 0, 0), 0.0)):
+        run_wgrad(dtype, out, LONG, N, K, beta=beta, pad=pad, before=3, behind=5)
+        assert took(cfg)
