@@ -13,6 +13,7 @@
 #include "grouped_dma.hpp"
 #include "configs16.hpp"
 #include "mx4.hpp"
+#include "mx4_dma.hpp"
 #include "swiglu_gemm.h"
 
 using namespace sg;
@@ -121,16 +122,29 @@ int run_depth(const char* what, int epi, int dtype, GroupedParams q, hipStream_t
                                (int64_t)q.experts * q.g.tiles_m * q.g.tiles_n, st));
 }
 
+int choose_mx4(const GroupedParams& q) {
+    if (const char* s = std::getenv("SG_FORCE_MX4")) {
+        const int c = std::atoi(s);
+        if (*s && c >= 0 && c < kNumMxCfg) return c;
+    }
+    const int64_t runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
+    return mean <= 32 ? 0 : mean < 256 ? 1 : 3;
+}
+
 int run_mx4(const char* what, int epi, int dtype, MxParams x, hipStream_t st) {
     GroupedParams& q = x.q;
+    // a lane's offset from its tile's base stays below 2^31 bytes
+    if (256 * q.g.lda + 256 >= (int64_t)1 << 31) return status_of(hipErrorInvalidConfiguration);
+    const int cfg = choose_mx4(q);
+    const MxCfg& c = kMxCfg[cfg];
     q.g.group_m = 4;
-    q.g.tiles_n = (int)cdiv(q.g.N, 128);
-    const int64_t blocks = (q.offsets ? most_row_tiles(q.rows, q.experts, 32) : cdiv(q.rows, 32)) *
-                           q.g.tiles_n;
-    if (blocks > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
-    describe("%s any 32x128", what);
-    return status_of(launch_mx4(epi, dtype == SG_F16 ? DT_F16 : DT_BF16, -1, x, (unsigned)blocks,
-                                st));
+    q.g.tiles_n = (int)cdiv(q.g.N, c.BN);
+    q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0;
+    const int64_t tiles_m = q.offsets ? most_row_tiles(q.rows, q.experts, c.BM) : cdiv(q.rows, c.BM);
+    if (tiles_m * q.g.tiles_n > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
+    describe("%s cfg=%d %s", what, cfg, c.name);
+    return status_of(launch_mx4(epi, dtype == SG_F16 ? DT_F16 : DT_BF16, cfg, x,
+                                (unsigned)(tiles_m * q.g.tiles_n), st));
 }
 
 }  // namespace

@@ -1,13 +1,21 @@
 // The 4-bit product's kernels.
-#include "mx4.hpp"
+#include "mx4_dma.hpp"
 
 namespace sg {
 
 template <int DT_OUT, int EPI>
 static hipError_t launch_mx4_epi(int cfg, const MxParams& x, unsigned blocks, hipStream_t st) {
-    (void)cfg;
-    hipLaunchKernelGGL((mx_any_kernel<DT_OUT, EPI>), dim3(blocks), dim3(256), 0, st, x);
-    return hipGetLastError();
+#define SG_MXCASE(ID, BM, BN, S, WM, WN)                                                       \
+    case ID:                                                                                   \
+        hipLaunchKernelGGL((mx_dma_kernel<DT_OUT, EPI, BM, BN, S, WM, WN>), dim3(blocks),      \
+                           dim3(64 * WM * WN), 0, st, x);                                      \
+        return hipGetLastError();
+    switch (cfg) {
+        SG_MX_CONFIGS(SG_MXCASE)
+        default: break;
+    }
+#undef SG_MXCASE
+    return hipErrorInvalidValue;
 }
 
 hipError_t launch_mx4(int epi, int dt, int cfg, const MxParams& x, unsigned blocks,

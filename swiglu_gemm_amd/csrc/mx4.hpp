@@ -245,46 +245,6 @@ struct MxParams {
     int tiles_k;
 };
 
-// One 32 x 32 accumulator a wave, four waves side by side, fragments straight from memory.
-template <int DT_OUT, int EPI>
-__global__ void __launch_bounds__(256) mx_any_kernel(const MxParams x) {
-    const GroupedParams& q = x.q;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    GroupItem it;
-    if (!find_rows<32>(q, blockIdx.x, lane, it)) return;
-    const Gemm16Params p = group_problem<false, 1, EPI == EPI_GEMM_F32 ? 4 : 2>(q, it);
-    const int m0 = it.tm * 32, n0 = it.tn * 128 + wave * 32;
-    const int nb = p.K, h = lane >> 5;
-    const int ra = min(m0 + (lane & 31), p.M - 1), rb = min(n0 + (lane & 31), p.N - 1);
-    const uint8_t* A = reinterpret_cast<const uint8_t*>(p.A) + ra * p.lda;
-    const uint8_t* B = reinterpret_cast<const uint8_t*>(p.B) + rb * p.ldb;
-    const uint8_t* Bs = x.Bs + it.e * x.sBs;
-    f32x16 acc;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.0f;
-    for (int b0 = 0; b0 < nb; b0 += 2) {
-        const int b = b0 + h;
-        u32x4 fa = {0u, 0u, 0u, 0u}, fb = {0u, 0u, 0u, 0u};
-        int sa = 127, sb = 127;
-        if (b < nb) {
-            fa = *reinterpret_cast<const u32x4*>(A + b * 16);
-            fb = *reinterpret_cast<const u32x4*>(B + b * 16);
-            sa = x.As[mx_scale_at(it.row0 + ra, b, x.tiles_k)];
-            sb = Bs[mx_scale_at(rb, b, x.tiles_k)];
-        }
-        const i32x8 va = {(int)fa.x, (int)fa.y, (int)fa.z, (int)fa.w, 0, 0, 0, 0};
-        const i32x8 vb = {(int)fb.x, (int)fb.y, (int)fb.z, (int)fb.w, 0, 0, 0, 0};
-        acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(vb, va, acc, 4, 4, 0, sb, 0, sa);
-    }
-    const int m = m0 + (lane & 31);
-    if (m >= p.M) return;
-#pragma unroll
-    for (int g = 0; g < 4; ++g) {
-        const float a[4] = {acc[4 * g], acc[4 * g + 1], acc[4 * g + 2], acc[4 * g + 3]};
-        group_store<DT_OUT, EPI, true>(p, nullptr, m, n0 + 8 * g + 4 * h, a);
-    }
-}
-
 // dt: the output type; cfg: the tile.  blocks: the host's upper bound of the items.
 hipError_t launch_mx4(int epi, int dt, int cfg, const MxParams& x, unsigned blocks,
                       hipStream_t st);

@@ -260,3 +260,19 @@ def test_mixture_layer_in_four_bits():
         ref.check(Y[p], w, t)
         s, err = ref.matmul(y[p], wd.t())
         ref.check(Z[p], s, err + ref.half_step(s, torch.float32))
+
+
+@pytest.mark.parametrize("cfg", range(7))
+def test_every_tile(monkeypatch, cfg):
+    """Ragged runs that start inside a tile of scales, rows that end in every block of a K tile,
+    few and many K tiles."""
+    import swiglu_gemm_amd as sg
+    monkeypatch.setenv("SG_FORCE_MX4", str(cfg))
+    sizes = [1, 0, 257, 64, 130]
+    for nb in range(1, 18):
+        run_product(sizes, 160, 32 * nb, spread=1, before=3, behind=5)
+        assert "cfg=%d " % cfg in sg.last_config()
+    run_product(sizes, 520, 2048, "f32", alpha=-0.5)
+    run_product(300, 324, 1312, "f16", spread=0, pad=4)
+    run_product(sizes, 164, 416, swiglu=True, spread=0, before=3, behind=5)
+    run_product(260, 256, 1024, "f16", swiglu=True, spread=0)
