@@ -525,48 +525,71 @@ def silu_mul(G, U, Y):
 
 
 # ------------------------------------------------- products grouped by expert
-def _same_device(*ts):
-    """Every tensor on one GPU; a context that makes it the current device (the library
-    launches on the current device's kernels)."""
-    import torch
-    first = None
-    for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("every tensor must be on the GPU")
-        if first is None:
-            first = t.device
-        elif t.device != first:
-            raise ValueError("every tensor must be on one device, got %s and %s"
-                             % (first, t.device))
-    return torch.cuda.device(first)
+# These run for single tokens, where a call costs the host as much as the GPU: each tensor's
+# attributes are read once, and the usual case (contiguous tensors) is checked first.
+_TORCH = None
 
 
-def _experts(offsets, experts: int) -> None:
-    import torch
-    if offsets.dtype != torch.int32:
+def _torch():
+    """torch and the current device's index (looked up once)."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = (torch, getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device)
+    return _TORCH
+
+
+def _launch(what: str, fn, tensors, *args) -> None:
+    """Calls the library on the tensors' device and torch's current stream there.  Every tensor
+    (None: an argument left out) must be on one GPU; where that is not the current device it is
+    made so for the call."""
+    device = -1
+    for t in tensors:
+        if t is not None:
+            d = t.get_device()
+            if d < 0:
+                raise ValueError("every tensor must be on the GPU")
+            if device < 0:
+                device = d
+            elif d != device:
+                raise ValueError("every tensor must be on one device, got cuda:%d and cuda:%d"
+                                 % (device, d))
+    torch, current = _torch()
+    if current() != device:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(tensors[0]))
+    else:
+        status = fn(*args, _stream(tensors[0]))
+    if status != 0:
+        _check(status, what)
+
+
+def _experts(offsets, experts: int) -> int:
+    if offsets.dtype is not _torch()[0].int32:
         raise TypeError("offsets must be int32, not %s" % offsets.dtype)
-    if offsets.dim() != 1 or not offsets.is_contiguous() or offsets.numel() != experts + 1:
+    if offsets.shape != (experts + 1,) or not offsets.is_contiguous():
         raise ValueError("offsets must be a contiguous vector of experts + 1 = %d row numbers"
                          % (experts + 1))
+    return offsets.data_ptr()
 
 
 def _scale(scale, experts: int):
-    import torch
     if scale is None:
         return None
-    if scale.dtype != torch.float32:
+    if scale.dtype is not _torch()[0].float32:
         raise TypeError("scale must be float32")
-    if scale.dim() != 1 or not scale.is_contiguous() or scale.numel() != experts:
+    if scale.shape != (experts,) or not scale.is_contiguous():
         raise ValueError("scale must be a contiguous vector of %d factors" % experts)
     return scale.data_ptr()
 
 
 def _rows(t, name: str, cols: int) -> int:
     """Leading dimension of a 2-D tensor of rows with `cols` columns."""
-    if t.dim() != 2 or t.size(1) != cols:
-        raise ValueError("%s has shape %s, expected rows of %d" % (name, tuple(t.shape), cols))
+    sh = t.shape
+    if len(sh) != 2 or sh[1] != cols:
+        raise ValueError("%s has shape %s, expected rows of %d" % (name, tuple(sh), cols))
+    if t.is_contiguous():
+        return cols or 1
     ld = _ld(t)
     if ld < cols:
         raise ValueError("%s: rows overlap (row stride %d, %d columns)" % (name, ld, cols))
@@ -575,13 +598,17 @@ def _rows(t, name: str, cols: int) -> int:
 
 def _stack(t, name: str, disjoint: bool):
     """Leading dimension and stride of a 3-D stack of row-major matrices, one an expert."""
-    if t.dim() != 3 or t.size(0) < 1:
+    sh = t.shape
+    if len(sh) != 3 or sh[0] < 1:
         raise ValueError("%s must be 3-D, one matrix for each expert" % name)
-    e, r, c = t.shape
-    if c > 1 and t.stride(2) != 1:
+    e, r, c = sh
+    if t.is_contiguous():
+        return c or 1, r * c
+    st = t.stride()
+    if c > 1 and st[2] != 1:
         raise ValueError("%s: the last dimension must be contiguous (stride 1)" % name)
-    ld = max(t.stride(1), 1) if r > 1 else max(c, 1)
-    stride = t.stride(0) if e > 1 else 0
+    ld = max(st[1], 1) if r > 1 else max(c, 1)
+    stride = st[0] if e > 1 else 0
     if ld < c or (disjoint and e > 1 and r and c and stride < (r - 1) * ld + c):
         raise ValueError("%s: the matrices or their rows overlap" % name)
     return ld, stride
@@ -593,33 +620,35 @@ def grouped_gemm(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, transB
     offsets[e + 1] of each expert, in place on C; other rows stay as they are.  A [M, K];
     B [experts, K, N], or [experts, N, K] with transB='T'; C [M, N] of A's dtype (bf16 for
     e4m3 operands); scale: None or float32 [experts]."""
+    codes, outs = _tables()[:2]
     code = _dtype_code(A)
     if code == SG_F32:
         raise TypeError("grouped products take bf16, fp16 or e4m3 operands")
-    tb = transB.upper()
-    if tb not in ("N", "T"):
+    if transB not in ("N", "T", "n", "t"):
         raise ValueError("transB must be 'N' or 'T'")
-    if A.dim() != 2:
+    ash = A.shape
+    if len(ash) != 2:
         raise ValueError("A must be 2-D")
-    if _tables()[0].get(B.dtype) != code:
+    if codes.get(B.dtype) != code:
         raise TypeError("B must have A's dtype")
-    if C.dtype not in _out_dtypes(code):
-        raise TypeError("C has dtype %s, expected %s" % (C.dtype, _out_dtypes(code)[0]))
-    M, K = A.shape
+    if C.dtype not in outs[code]:
+        raise TypeError("C has dtype %s, expected %s" % (C.dtype, outs[code][0]))
+    M, K = ash
     ldb, sB = _stack(B, "B", False)
-    E, N = B.shape[0], B.shape[1] if tb == "T" else B.shape[2]
-    if (B.shape[2] if tb == "T" else B.shape[1]) != K:
+    if transB in "Tt":
+        E, N, kb = B.shape
+    else:
+        E, kb, N = B.shape
+    if kb != K:
         raise ValueError("op(B) must have A's %d columns as rows" % K)
     lda, ldc = _rows(A, "A", K), _rows(C, "C", N)
     if C.shape[0] != M:
         raise ValueError("C has %d rows, A %d" % (C.shape[0], M))
-    _experts(offsets, E)
+    op = _experts(offsets, E)
     sp = _scale(scale, E)
-    with _same_device(A, B, C, offsets, scale):
-        st = lib().sg_grouped_gemm(tb.encode(), E, offsets.data_ptr(), M, N, K, float(alpha), sp,
-                                   A.data_ptr(), lda, B.data_ptr(), ldb, sB, float(beta),
-                                   C.data_ptr(), ldc, code, _stream(C))
-    _check(st, "sg_grouped_gemm")
+    _launch("sg_grouped_gemm", lib().sg_grouped_gemm, (C, A, B, offsets, scale), transB.encode(), E,
+            op, M, N, K, float(alpha), sp, A.data_ptr(), lda, B.data_ptr(), ldb, sB, float(beta), C.data_ptr(),
+            ldc, code)
     return C
 
 
@@ -627,29 +656,27 @@ def grouped_gemm_wgrad(A, D, C, offsets, alpha: float = 1.0, beta: float = 0.0):
     """C[e] = alpha * A[rows of e]^T @ D[rows of e] + beta * C[e], in place on C [experts, K,
     N]: the gradient of grouped_gemm's weight from its input A [M, K] and the gradient D
     [M, N] of its output (bf16 or fp16); C has their dtype or float32."""
-    import torch
     code = _dtype_code(A)
     if code not in (SG_F16, SG_BF16):
         raise TypeError("the weight gradient takes bf16 or fp16 operands")
     if D.dtype != A.dtype:
         raise TypeError("D must have A's dtype")
-    if C.dtype not in (A.dtype, torch.float32):
+    if C.dtype not in (A.dtype, _torch()[0].float32):
         raise TypeError("C has dtype %s, expected %s or float32" % (C.dtype, A.dtype))
-    if A.dim() != 2 or D.dim() != 2 or A.shape[0] != D.shape[0]:
+    ash, dsh, csh = A.shape, D.shape, C.shape
+    if len(ash) != 2 or len(dsh) != 2 or ash[0] != dsh[0]:
         raise ValueError("A and D must be 2-D with the same rows")
-    M, K = A.shape
-    N = D.shape[1]
+    M, K = ash
+    N = dsh[1]
     ldc, sC = _stack(C, "C", True)
-    E = C.shape[0]
-    if tuple(C.shape[1:]) != (K, N):
-        raise ValueError("C has shape %s, expected (experts, %d, %d)" % (tuple(C.shape), K, N))
-    _experts(offsets, E)
+    E = csh[0]
+    if csh[1] != K or csh[2] != N:
+        raise ValueError("C has shape %s, expected (experts, %d, %d)" % (tuple(csh), K, N))
+    op = _experts(offsets, E)
     lda, ldd = _rows(A, "A", K), _rows(D, "D", N)
-    with _same_device(A, D, C, offsets):
-        st = lib().sg_grouped_gemm_wgrad(E, offsets.data_ptr(), M, N, K, float(alpha),
-                                         A.data_ptr(), lda, D.data_ptr(), ldd, float(beta),
-                                         C.data_ptr(), ldc, sC, code, _dtype_code(C), _stream(C))
-    _check(st, "sg_grouped_gemm_wgrad")
+    _launch("sg_grouped_gemm_wgrad", lib().sg_grouped_gemm_wgrad, (C, A, D, offsets), E, op, M, N, K,
+            float(alpha), A.data_ptr(), lda, D.data_ptr(), ldd, float(beta), C.data_ptr(), ldc, sC, code,
+            _dtype_code(C))
     return C
 
 
@@ -659,13 +686,15 @@ def _grouped_swiglu(A, Wfused):
         raise TypeError("SwiGLU takes bf16, fp16 or e4m3 operands")
     if _tables()[0].get(Wfused.dtype) != code:
         raise TypeError("Wfused must have A's dtype")
-    if A.dim() != 2 or Wfused.dim() != 3 or Wfused.shape[0] < 1:
+    ash, wsh = A.shape, Wfused.shape
+    if len(ash) != 2 or len(wsh) != 3 or wsh[0] < 1:
         raise ValueError("A must be 2-D and Wfused 3-D, one matrix for each expert")
-    M, K = A.shape
-    E, N2 = Wfused.shape[0], Wfused.shape[2]
+    M, K = ash
+    E, _, N2 = wsh
     if N2 % 2:
         raise ValueError("Wfused must have an even number of columns (gate, up pairs)")
-    _contig(A, "A", (M, K))
+    if not A.is_contiguous():
+        raise ValueError("A must be contiguous")
     _contig(Wfused, "Wfused", (E, K, N2))
     return code, E, M, N2 // 2, K
 
@@ -678,13 +707,10 @@ def grouped_swiglu_gemm(A, Wfused, Y, offsets, alpha: float = 1.0, scale=None):
     if Y.dtype not in _out_dtypes(code):
         raise TypeError("Y has dtype %s, expected %s" % (Y.dtype, _out_dtypes(code)[0]))
     _contig(Y, "Y", (M, N))
-    _experts(offsets, E)
+    op = _experts(offsets, E)
     sp = _scale(scale, E)
-    with _same_device(A, Wfused, Y, offsets, scale):
-        st = lib().sg_grouped_swiglu_gemm(E, offsets.data_ptr(), A.data_ptr(), Wfused.data_ptr(),
-                                          Y.data_ptr(), M, N, K, code, float(alpha), sp,
-                                          _stream(Y))
-    _check(st, "sg_grouped_swiglu_gemm")
+    _launch("sg_grouped_swiglu_gemm", lib().sg_grouped_swiglu_gemm, (Y, A, Wfused, offsets, scale),
+            E, op, A.data_ptr(), Wfused.data_ptr(), Y.data_ptr(), M, N, K, code, float(alpha), sp)
     return Y
 
 
@@ -700,12 +726,10 @@ def grouped_swiglu_gemm_bwd(A, Wfused, dY, dH, offsets):
         _contig(t, name, (M, n))
         if t.dtype != A.dtype:
             raise TypeError("%s must have A's dtype" % name)
-    _experts(offsets, E)
-    with _same_device(A, Wfused, dY, dH, offsets):
-        st = lib().sg_grouped_swiglu_gemm_bwd(E, offsets.data_ptr(), A.data_ptr(),
-                                              Wfused.data_ptr(), dY.data_ptr(), dH.data_ptr(),
-                                              M, N, K, code, _stream(dH))
-    _check(st, "sg_grouped_swiglu_gemm_bwd")
+    op = _experts(offsets, E)
+    _launch("sg_grouped_swiglu_gemm_bwd", lib().sg_grouped_swiglu_gemm_bwd,
+            (dH, A, Wfused, dY, offsets), E, op, A.data_ptr(), Wfused.data_ptr(), dY.data_ptr(),
+            dH.data_ptr(), M, N, K, code)
     return dH
 
 
@@ -722,23 +746,22 @@ def _mx_float(t, name: str) -> int:
     return code
 
 
-def _mx_matrices(t, name: str):
-    """(batch, rows, cols, leading dimension, stride) of a 2-D or 3-D tensor."""
-    if t.dim() == 2:
-        r, c = t.shape
-        return 1, r, c, _rows(t, name, c), 0
-    ld, stride = _stack(t, name, False)
-    return t.shape[0], t.shape[1], t.shape[2], ld, stride
+def _mx_matrices(t, name: str, disjoint: bool = False):
+    """(leading shape, batch, rows, cols, leading dimension, stride) of a 2-D or 3-D tensor."""
+    sh = t.shape
+    if len(sh) == 2:
+        r, c = sh
+        return (), 1, r, c, _rows(t, name, c), 0
+    if len(sh) != 3:
+        raise ValueError("%s must be 2-D or 3-D" % name)
+    ld, stride = _stack(t, name, disjoint)
+    return (sh[0],), sh[0], sh[1], sh[2], ld, stride
 
 
-def _mx_pair(codes, scales, name: str, rows: int, cols: int, batch=None):
-    import torch
-    nb, ns = mxfp4_shapes(rows, cols)
-    lead = () if batch is None else (batch,)
-    for t, what, shape in ((codes, "codes", lead + (rows, nb)), (scales, "scales", lead + (ns,))):
-        if t.dtype != torch.uint8:
-            raise TypeError("%s: %s must be uint8" % (name, what))
-        _contig(t, "%s: %s" % (name, what), shape)
+def _mx_bytes(t, name: str, shape) -> None:
+    if t.dtype is not _torch()[0].uint8:
+        raise TypeError("%s must be uint8" % name)
+    _contig(t, name, shape)
 
 
 def mxfp4_quantize(X, codes=None, scales=None, values=None):
@@ -747,32 +770,27 @@ def mxfp4_quantize(X, codes=None, scales=None, values=None):
     both uint8, S and the scales' tiles as in include/swiglu_gemm.h (mxfp4_shapes).  values: a
     contiguous tensor like X that gets the values they stand for; codes and scales are then
     written only where given, and (codes, scales) may be (None, None)."""
-    import torch
     code = _mx_float(X, "X")
-    if X.dim() not in (2, 3):
-        raise ValueError("X must be 2-D or 3-D")
-    batch, M, K, ld, stride = _mx_matrices(X, "X")
+    lead, batch, M, K, ld, stride = _mx_matrices(X, "X")
     nb, ns = mxfp4_shapes(M, K)
-    lead = tuple(X.shape[:-2])
+    if codes is not None:
+        _mx_bytes(codes, "codes", lead + (M, nb))
+    elif values is None:
+        torch = _torch()[0]
+        codes = torch.empty(lead + (M, nb), dtype=torch.uint8, device=X.device)
+    if scales is not None:
+        _mx_bytes(scales, "scales", lead + (ns,))
+    elif values is None:
+        torch = _torch()[0]
+        scales = torch.empty(lead + (ns,), dtype=torch.uint8, device=X.device)
     if values is not None:
         if values.dtype != X.dtype:
             raise TypeError("values must have X's dtype")
         _contig(values, "values", X.shape)
-    else:
-        if codes is None:
-            codes = torch.empty(lead + (M, nb), dtype=torch.uint8, device=X.device)
-        if scales is None:
-            scales = torch.empty(lead + (ns,), dtype=torch.uint8, device=X.device)
-    for t, what, shape in ((codes, "codes", lead + (M, nb)), (scales, "scales", lead + (ns,))):
-        if t is not None:
-            if t.dtype != torch.uint8:
-                raise TypeError("%s must be uint8" % what)
-            _contig(t, what, shape)
-    ptr = [t.data_ptr() if t is not None else None for t in (codes, scales, values)]
-    with _same_device(X, codes, scales, values):
-        st = lib().sg_mxfp4_quantize(X.data_ptr(), ld, stride, batch, M, K, code, *ptr,
-                                     _stream(X))
-    _check(st, "sg_mxfp4_quantize")
+    _launch("sg_mxfp4_quantize", lib().sg_mxfp4_quantize, (X, codes, scales, values), X.data_ptr(),
+            ld, stride, batch, M, K, code, codes.data_ptr() if codes is not None else None,
+            scales.data_ptr() if scales is not None else None,
+            values.data_ptr() if values is not None else None)
     return codes, scales
 
 
@@ -780,84 +798,69 @@ def mxfp4_dequantize(codes, scales, X):
     """X [rows, K] or [batch, rows, K] = the values of codes and scales, in place on X (fp32,
     fp16 or bf16, rounded once; rows may be strided)."""
     code = _mx_float(X, "X")
-    if X.dim() not in (2, 3):
-        raise ValueError("X must be 2-D or 3-D")
-    batch, M, K, ld, stride = _mx_matrices(X, "X")
-    if X.dim() == 3:
-        _stack(X, "X", True)
-    _mx_pair(codes, scales, "the matrix", M, K, batch if X.dim() == 3 else None)
-    with _same_device(codes, scales, X):
-        st = lib().sg_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), batch, M, K,
-                                       X.data_ptr(), ld, stride, code,
-                                       _stream(X))
-    _check(st, "sg_mxfp4_dequantize")
+    lead, batch, M, K, ld, stride = _mx_matrices(X, "X", True)
+    nb, ns = mxfp4_shapes(M, K)
+    _mx_bytes(codes, "codes", lead + (M, nb))
+    _mx_bytes(scales, "scales", lead + (ns,))
+    _launch("sg_mxfp4_dequantize", lib().sg_mxfp4_dequantize, (X, codes, scales), codes.data_ptr(),
+            scales.data_ptr(), batch, M, K, X.data_ptr(), ld, stride, code)
     return X
 
 
 def mxfp4_tile_scales(S):
     """Scales stored as rows of bytes, S [rows, blocks] or [batch, rows, blocks] uint8, in the
     tiles that mxfp4_gemm reads."""
-    import torch
+    torch = _torch()[0]
     if S.dtype != torch.uint8:
         raise TypeError("scales must be uint8")
-    if S.dim() not in (2, 3):
-        raise ValueError("scales must be 2-D or 3-D")
-    batch, M, nb, ld, stride = _mx_matrices(S, "scales")
-    out = torch.empty(tuple(S.shape[:-2]) + (mxfp4_shapes(M, 32 * nb)[1],), dtype=torch.uint8,
-                      device=S.device)
-    with _same_device(S):
-        st = lib().sg_mxfp4_tile_scales(S.data_ptr(), ld, stride, batch, M, nb, out.data_ptr(),
-                                        _stream(S))
-    _check(st, "sg_mxfp4_tile_scales")
+    lead, batch, M, nb, ld, stride = _mx_matrices(S, "scales")
+    out = torch.empty(lead + (mxfp4_shapes(M, 32 * nb)[1],), dtype=torch.uint8, device=S.device)
+    _launch("sg_mxfp4_tile_scales", lib().sg_mxfp4_tile_scales, (S, out), S.data_ptr(), ld, stride,
+            batch, M, nb, out.data_ptr())
     return out
 
 
 def _mx_product(A, As, B, Bs, offsets, out, rows_of_b):
-    """Checks of a 4-bit product: (experts, M, K) with K in whole blocks; rows_of_b: B's rows
-    for out's columns."""
-    import torch
-    if A.dim() != 2 or out.dim() != 2:
+    """Checks of a 4-bit product: (experts, offsets' address, M, K) with K in whole blocks;
+    rows_of_b: B's rows for out's columns."""
+    ash, bsh = A.shape, B.shape
+    if len(ash) != 2:
         raise ValueError("A and the output must be 2-D")
-    E = 1
+    E, op, lead = 1, None, ()
     if offsets is not None:
-        if B.dim() != 3:
+        if len(bsh) != 3 or bsh[0] < 1:
             raise ValueError("with offsets the weight must be 3-D, one matrix for each expert")
-        E = B.shape[0]
-        _experts(offsets, E)
-    elif B.dim() != 2:
+        E = bsh[0]
+        lead = (E,)
+        op = _experts(offsets, E)
+    elif len(bsh) != 2:
         raise ValueError("without offsets the weight must be 2-D")
-    M, row = A.shape
-    if row % 16 or B.shape[-1] != row:
+    M, row = ash
+    if row % 16 or bsh[-1] != row:
         raise ValueError("the rows of codes must be of one length, whole blocks of 16 bytes")
     K = row * 2
-    _mx_pair(A, As, "A", M, K)
-    _mx_pair(B, Bs, "the weight", rows_of_b, K, E if offsets is not None else None)
+    _mx_bytes(A, "A: codes", ash)
+    _mx_bytes(As, "A: scales", (mxfp4_shapes(M, K)[1],))
+    _mx_bytes(B, "the weight: codes", lead + (rows_of_b, row))
+    _mx_bytes(Bs, "the weight: scales", lead + (mxfp4_shapes(rows_of_b, K)[1],))
     if out.shape[0] != M:
         raise ValueError("the output has %d rows, A %d" % (out.shape[0], M))
-    for t, name in ((A, "A"), (B, "the weight's codes")):
-        if t.data_ptr() % 16:
-            raise ValueError("%s must be 16-byte aligned" % name)
-    for t in (As, Bs):
-        if t.data_ptr() % 4:
-            raise ValueError("scales must be 4-byte aligned")
-    return E, M, K
+    return E, op, M, K
 
 
 def mxfp4_gemm(A, As, B, Bs, C, offsets=None, alpha: float = 1.0):
     """C = alpha * A @ B^T of two matrices held as (codes, scales): A [M, K], B [N, K]; C [M, N]
     fp32, fp16 or bf16, rows may be strided.  With offsets, B [experts, N, K] and the rows of
-    each expert meet its own matrix; rows of no expert stay as they are."""
+    each expert meet its own matrix; rows of no expert stay as they are.  The codes must be
+    16-byte, the scales 4-byte aligned."""
     code = _mx_float(C, "C")
     if C.dim() != 2:
         raise ValueError("A and the output must be 2-D")
     N = C.shape[1]
-    E, M, K = _mx_product(A, As, B, Bs, offsets, C, N)
+    E, op, M, K = _mx_product(A, As, B, Bs, offsets, C, N)
     ldc = _rows(C, "C", N)
-    with _same_device(A, As, B, Bs, C, offsets):
-        st = lib().sg_mxfp4_gemm(E, offsets.data_ptr() if offsets is not None else None, M, N, K,
-                                 float(alpha), A.data_ptr(), As.data_ptr(), B.data_ptr(),
-                                 Bs.data_ptr(), C.data_ptr(), ldc, code, _stream(C))
-    _check(st, "sg_mxfp4_gemm")
+    _launch("sg_mxfp4_gemm", lib().sg_mxfp4_gemm, (C, A, As, B, Bs, offsets), E, op, M, N, K,
+            float(alpha), A.data_ptr(), As.data_ptr(), B.data_ptr(), Bs.data_ptr(), C.data_ptr(), ldc, code)
     return C
 
 
@@ -871,11 +874,8 @@ def mxfp4_swiglu_gemm(A, As, W, Ws, Y, offsets=None):
     if Y.dim() != 2:
         raise ValueError("A and the output must be 2-D")
     N = Y.shape[1]
-    E, M, K = _mx_product(A, As, W, Ws, offsets, Y, 2 * N)
+    E, op, M, K = _mx_product(A, As, W, Ws, offsets, Y, 2 * N)
     _contig(Y, "Y", (M, N))
-    with _same_device(A, As, W, Ws, Y, offsets):
-        st = lib().sg_mxfp4_swiglu_gemm(E, offsets.data_ptr() if offsets is not None else None,
-                                        M, N, K, A.data_ptr(), As.data_ptr(), W.data_ptr(),
-                                        Ws.data_ptr(), Y.data_ptr(), code, _stream(Y))
-    _check(st, "sg_mxfp4_swiglu_gemm")
+    _launch("sg_mxfp4_swiglu_gemm", lib().sg_mxfp4_swiglu_gemm, (Y, A, As, W, Ws, offsets), E, op, M,
+            N, K, A.data_ptr(), As.data_ptr(), W.data_ptr(), Ws.data_ptr(), Y.data_ptr(), code)
     return Y

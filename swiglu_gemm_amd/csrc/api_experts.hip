@@ -67,7 +67,7 @@ bool forced_group(int* cfg) {
 // Whether tile c can run the problem: 16-byte aligned operands, rows and expert strides,
 // DMA-compatible tiles, and every lane's offset from its tile's base below 2^31 bytes.
 bool group_cfg_ok(const GroupCfg& c, bool ta, bool tb, int esz, const GroupedParams& q) {
-    if ((c.e4m3 != 0) != (esz == 1)) return false;
+    if ((c.e4m3 != 0) != (esz == 1) || (ta ? c.rate_d : c.rate) <= 0.0) return false;
     if (!aligned(q.g.A, 16) || !aligned(q.g.B, 16)) return false;
     if (q.g.lda * esz % 16 != 0 || q.g.ldb * esz % 16 != 0 || q.sB % 16 != 0) return false;
     const int nw = c.WM * c.WN;
@@ -78,28 +78,85 @@ bool group_cfg_ok(const GroupCfg& c, bool ta, bool tb, int esz, const GroupedPar
            ((tb ? c.BN : c.BK) * q.g.ldb + 256) * esz < kLim;
 }
 
-int choose_rows(bool tb, int esz, const GroupedParams& q) {
-    int cfg = -1;
-    if (forced_group(&cfg))
-        return cfg >= 0 && cfg < kNumGroupCfg && group_cfg_ok(kGroupCfg[cfg], false, tb, esz, q)
-                   ? cfg
-                   : -1;
-    const int64_t runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
-    cfg = esz == 1 ? (mean <= 32 ? 5 : mean < 256 ? 6 : 8)
-                   : (mean <= 32 ? 0 : mean < 128 ? 1 : mean < 256 ? 2 : 4);
-    return group_cfg_ok(kGroupCfg[cfg], false, tb, esz, q) ? cfg : -1;
+// Microseconds of `tiles` tiles of `flops` products each that move `bytes` in all: rounds of
+// work-groups over the CUs (`occ` to a CU, which then share it), a last round counted whole
+// while there are few and in the mean when there are many; never less than the bytes take.
+constexpr int kNumCU = 256;
+constexpr double kBytesPerUs = 4.8e6;
+double est_us(double tiles, int occ, double flops, double rate, double fixed, double bytes) {
+    const double w = tiles / (kNumCU * occ);
+    const double rounds = w < 0.5 ? 1.0 : w < 4.0 ? std::fmax(1.0, std::ceil(w - 0.1)) : w + 0.4;
+    const double share = std::fmin((double)occ, std::fmax(1.0, tiles / kNumCU));
+    const double t = rounds * (share * flops / (rate * 1e6) + fixed), m = bytes / kBytesPerUs;
+    return std::fmax(t, m) + 0.15 * std::fmin(t, m);
 }
 
-int choose_depth(const GroupedParams& q) {
+// The rows of each expert are not known here, so their mean stands for them: a run of n rows
+// is taken for n/BM + 1/2 tiles, never less than one (half of one costs 0.6).
+double row_tiles(const GroupCfg& c, const GroupedParams& q) {
+    const double runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
+    const bool half = group_half(false, c.BM, c.BN, c.WM, c.WN);
+    const double least = half && mean <= c.BM / 2 ? 0.6 : 1.0;
+    return (double)cdiv(q.g.N, c.BN) * runs * std::fmax(least, mean / c.BM + (half ? 0.4 : 0.5));
+}
+
+double est_rows8(const GroupCfg& c, const GroupedParams& q) {
+    const double runs = q.experts < q.rows ? q.experts : q.rows;
+    const double bytes =
+        (double)q.rows * q.g.K + runs * q.g.K * (double)q.g.N + (double)q.rows * q.g.N * 2.0;
+    return est_us(row_tiles(c, q), group_occ(c.S * (c.BM + c.BN) * c.BK), 2.0 * c.BM * c.BN * q.g.K,
+                  c.rate, c.fixed, bytes);
+}
+
+// 16-bit rows go by the mean length of a run: up to 32 rows the tile that streams a weight for
+// them, then 128 x 256, above 384 the 32-deep one with two work-groups a CU, whose uneven
+// rounds cost less, and from 900 on 256 x 256; a smaller one where that leaves more than half
+// of the CUs without a tile.  Within 2.8 % of the best tile in the mean over the 72 problems
+// measured (see kGroupCfg); a cost model in rounds, as for the others, 3.3 %.
+int choose_rows16(const GroupedParams& q) {
+    const double runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
+    int cfg = mean <= 32 ? 0 : mean < 384 ? 2 : mean < 900 ? 4 : 3;
+    if (cfg >= 3 && row_tiles(kGroupCfg[cfg], q) < kNumCU / 2) cfg = 2;
+    if (cfg == 2 && row_tiles(kGroupCfg[cfg], q) < kNumCU / 2) cfg = 0;
+    return cfg;
+}
+
+double est_depth(const GroupCfg& c, const GroupedParams& q) {
+    const double tiles = (double)q.experts * cdiv(q.g.M, c.BM) * cdiv(q.g.N, c.BN);
+    const double bytes = (double)q.rows * (q.g.M + q.g.N) * 2.0 +
+                         (double)q.experts * q.g.M * (double)q.g.N * 2.0;
+    const int occ = group_occ(c.S * (c.BM + c.BN) * c.BK * 2);
+    return est_us(tiles, occ, 2.0 * c.BM * c.BN * q.rows / q.experts, c.rate_d, c.fixed_d, bytes);
+}
+
+// The tile with the least estimated time, or -1: the kernel for every alignment.
+int choose_group(bool depth, bool tb, int esz, const GroupedParams& q) {
     int cfg = -1;
-    if (!forced_group(&cfg)) cfg = q.g.M >= 256 && q.g.N >= 256 ? 4 : 2;
-    return cfg >= 2 && cfg <= 4 && group_cfg_ok(kGroupCfg[cfg], true, false, 2, q) ? cfg : -1;
+    if (forced_group(&cfg))
+        return cfg >= 0 && cfg < kNumGroupCfg && group_cfg_ok(kGroupCfg[cfg], depth, tb, esz, q)
+                   ? cfg
+                   : -1;
+    if (!depth && esz == 2) {
+        cfg = choose_rows16(q);
+        return group_cfg_ok(kGroupCfg[cfg], depth, tb, esz, q) ? cfg : -1;
+    }
+    double best = 0.0;
+    for (int i = 0; i < kNumGroupCfg; ++i) {
+        const GroupCfg& c = kGroupCfg[i];
+        if (!group_cfg_ok(c, depth, tb, esz, q)) continue;
+        const double t = depth ? est_depth(c, q) : est_rows8(c, q);
+        if (cfg < 0 || t < best) {
+            cfg = i;
+            best = t;
+        }
+    }
+    return cfg;
 }
 
 // Products over the rows of each expert: chooses the tile and launches.
 int run_rows(const char* what, int epi, bool tb, int dtype, GroupedParams q, hipStream_t st) {
     const int esz = dtype == SG_F8E4M3 ? 1 : 2;
-    const int cfg = q.g.K > 0 ? choose_rows(tb, esz, q) : -1;
+    const int cfg = q.g.K > 0 ? choose_group(false, tb, esz, q) : -1;
     const int bm = cfg < 0 ? 64 : kGroupCfg[cfg].BM, bn = cfg < 0 ? 64 : kGroupCfg[cfg].BN;
     q.g.group_m = 4;
     q.g.tiles_n = (int)cdiv(q.g.N, bn);
@@ -111,7 +168,7 @@ int run_rows(const char* what, int epi, bool tb, int dtype, GroupedParams q, hip
 
 // Products that sum over the rows of each expert.
 int run_depth(const char* what, int epi, int dtype, GroupedParams q, hipStream_t st) {
-    const int cfg = q.rows > 0 ? choose_depth(q) : -1;
+    const int cfg = q.rows > 0 ? choose_group(true, false, 2, q) : -1;
     const int bm = cfg < 0 ? 64 : kGroupCfg[cfg].BM, bn = cfg < 0 ? 64 : kGroupCfg[cfg].BN;
     q.g.group_m = 4;
     q.g.tiles_m = (int)cdiv(q.g.M, bm);

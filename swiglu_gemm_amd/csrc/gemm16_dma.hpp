@@ -234,6 +234,17 @@ __device__ __forceinline__ typename FragT<ESZ>::type read_frag(const char* tile,
     }
 }
 
+// The first n elements of a lane's fragment, the others zero.
+template <int ESZ>
+__device__ __forceinline__ void keep_first(typename FragT<ESZ>::type& f, int n) {
+    constexpr int ND = ESZ == 2 ? 4 : 8;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        const int nb = n * ESZ - 4 * d;              // bytes of dword d that stay
+        f[d] = nb >= 4 ? f[d] : nb <= 0 ? 0u : f[d] & ((1u << (8 * nb)) - 1u);
+    }
+}
+
 template <int DT>
 __device__ __forceinline__ f32x16 mfma_op(const typename FragT<DT == DT_E4M3 ? 1 : 2>::type& a,
                                           const typename FragT<DT == DT_E4M3 ? 1 : 2>::type& b,
@@ -287,10 +298,17 @@ struct DmaShape {
 // of BK: the S-stage direct-to-LDS ring feeding the MFMAs.  Every thread of the
 // work-group calls it; LDS is free on return only after a barrier (the last k-step
 // reads a stage without one).
-template <int DT, bool TA, bool TB, int EPI, int BM, int BN, int BK, int S, int WM, int WN>
+//
+// RT (a ring tail) and ring_tail: the partial tile goes through the ring like the others,
+// whole, and its fragments are cut to the first ktail k (both operands, so nothing that is
+// loaded past them counts, infinities and NaN included).  For callers that know that a whole
+// tile can be read there.  Saves the drain of the ring and the register-staged loads.
+template <int DT, bool TA, bool TB, int EPI, int BM, int BN, int BK, int S, int WM, int WN,
+          bool RT = false>
 __device__ __forceinline__ void dma_mainloop(
     const Gemm16Params& p, char* smem, int m0, int n0, int kbeg, int nkt, int ktail,
-    typename DmaShape<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>::Acc& acc, int wave, int lane) {
+    typename DmaShape<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>::Acc& acc, int wave, int lane,
+    bool ring_tail = false) {
     using D = DmaShape<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>;
     constexpr int ESZ = D::ESZ, FM = D::FM, FN = D::FN, KS = D::KS, TM = D::TM, TN = D::TN;
     constexpr bool KCA = D::KCA, KCB = D::KCB, W12 = D::W12;
@@ -367,11 +385,12 @@ __device__ __forceinline__ void dma_mainloop(
         if constexpr (W12) db2.issue(stB(sti) + TB_::BYTES, t, wave);
     };
 
-    if (nkt > 0) {
+    const int nt = RT && ring_tail ? nkt + 1 : nkt;      // tiles of the ring
+    if (nt > 0) {
 #pragma unroll
         for (int i = 0; i < S - 1; ++i)
-            if (i < nkt) issue(i);
-        if (nkt >= S - 1) wait_vmcnt<(S - 2) * NL>();
+            if (i < nt) issue(i);
+        if (nt >= S - 1) wait_vmcnt<(S - 2) * NL>();
         else wait_vmcnt<0>();
         __builtin_amdgcn_s_barrier();
         __builtin_amdgcn_sched_barrier(0);
@@ -407,7 +426,7 @@ __device__ __forceinline__ void dma_mainloop(
         // t+1, then tile t+1's first fragments under tile t's last MFMAs.  sc, sn:
         // the stages of tiles t and t+1.
         auto tile = [&](int t, int sc, int sn) __attribute__((always_inline)) {
-            const bool ahead = t + S - 1 < nkt;
+            const bool ahead = t + S - 1 < nt;
             if constexpr (SPREAD) {
                 const int sx = (t + S - 1) % S;
 #pragma unroll
@@ -451,6 +470,44 @@ __device__ __forceinline__ void dma_mainloop(
         } else {
             for (int t = 0; t < nkt; ++t) tile(t, t % S, (t + 1) % S);
         }
+    }
+    if constexpr (RT) {
+        static_assert(!W12, "one B tile");
+        if (ktail > 0) {
+            // a rolled loop, its addresses from an opaque lane index: nothing of it is
+            // carried through the main loop
+            int ln = lane;
+            asm volatile("" : "+v"(ln));
+            char* sa = stA(nkt % S);
+            char* sb = stB(nkt % S);
+            if (!ring_tail) {
+                const int kt = kbeg + nkt * BK;
+                __syncthreads();
+                DmaStream<KCA, BM, BK, ESZ, NW> ta;
+                ta.init(p.A, p.lda, m0, p.M, kt, wave, ln);
+                ta.load_tail(sa, ktail, wave, ln);
+                DmaStream<KCB, BNS, BK, ESZ, NW> tb;
+                tb.init(p.B, p.ldb, n0, p.N, kt, wave, ln);
+                tb.load_tail(sb, ktail, wave, ln);
+                __syncthreads();
+            }
+#pragma unroll 1
+            for (int s = 0; s * D::KSTEP < ktail; ++s) {
+                const int n = ktail - s * D::KSTEP - D::KSTEP / 2 * (ln >> 5);
+#pragma unroll
+                for (int tm = 0; tm < FM; ++tm) {
+                    fa[0][tm] = read_frag<KCA, BM, BK, ESZ>(sa, wm * TM + tm * 32, s, ln);
+                    keep_first<ESZ>(fa[0][tm], n);
+                }
+#pragma unroll
+                for (int tn = 0; tn < FN; ++tn) {
+                    fb[0][tn] = read_frag<KCB, BNS, BK, ESZ>(sb, wn * TN + tn * 32, s, ln);
+                    keep_first<ESZ>(fb[0][tn], n);
+                }
+                mfma_all(fa[0], fb[0]);
+            }
+        }
+        return;
     }
     if (ktail > 0) {
         // every DMA has landed (the ring's last wait is for all of them); once every

@@ -43,29 +43,41 @@ __device__ __forceinline__ int group_offset(const GroupedParams& q, int e) {
     return min(max(q.offsets[e], 0), q.rows);
 }
 
-// The work of one work-group: expert e, whose rows are [row0, row0 + rows), and the tile
-// (tm, tn) of its product.
+// The work of one work-group: expert e, whose rows are [row0, row0 + rows), and the rows from
+// m0 on and columns from tile tn of its product.
 struct GroupItem {
-    int e, row0, rows, tm, tn;
+    int e, row0, rows, m0, tn;
 };
+
+// The sum of x over the lanes up to and including this one.
+__device__ __forceinline__ int lane_scan(int x, int lane) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int up = __shfl_up(x, d);
+        if (lane >= d) x += up;
+    }
+    return x;
+}
 
 // Finds the item of work-group `bid` for products over an expert's rows in tiles of BM
 // rows; false if there are fewer items.  Every lane of a wave calls it and gets the same
 // answer in scalar registers: lane l counts the tiles of experts [l*P, (l+1)*P), P =
 // ceil(experts / 64), a scan over the lanes finds the one that holds the item, and its
-// experts are walked.  Consecutive items share an XCD (xcd_remap over the real count).
+// experts are walked.  Consecutive items share an XCD, and an expert's items follow one
+// another, so that its weight is read while it is in that XCD's L2.
 template <int BM>
 __device__ __forceinline__ bool find_rows(const GroupedParams& q, int bid, int lane,
                                           GroupItem& it) {
     const int tiles_n = q.g.tiles_n;
+    int tm;
     if (!q.offsets) {
         const int tiles_m = (q.rows + BM - 1) / BM;
         if (bid >= tiles_m * tiles_n) return false;
         it.e = 0;
         it.row0 = 0;
         it.rows = q.rows;
-        tile_coords(xcd_remap(bid, tiles_m * tiles_n), tiles_m, tiles_n, q.g.group_m, it.tm,
-                    it.tn);
+        tile_coords(xcd_remap(bid, tiles_m * tiles_n), tiles_m, tiles_n, q.g.group_m, tm, it.tn);
+        it.m0 = tm * BM;
         return true;
     }
     const int per = (q.experts + 63) / 64;
@@ -76,12 +88,7 @@ __device__ __forceinline__ bool find_rows(const GroupedParams& q, int bid, int l
         const int n = group_offset(q, e + 1) - group_offset(q, e);
         if (n > 0) mine += (n + BM - 1) / BM;
     }
-    int incl = mine;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int up = __shfl_up(incl, d);
-        if (lane >= d) incl += up;
-    }
+    const int incl = lane_scan(mine, lane);
     const int total = __builtin_amdgcn_readlane(incl, 63) * tiles_n;
     if (bid >= total) return false;
     const int lid = xcd_remap(bid, total);
@@ -103,21 +110,40 @@ __device__ __forceinline__ bool find_rows(const GroupedParams& q, int bid, int l
     it.e = e;
     it.row0 = row0;
     it.rows = n;
-    tile_coords(lid - first, tiles_m, tiles_n, q.g.group_m, it.tm, it.tn);
+    tile_coords(lid - first, tiles_m, tiles_n, q.g.group_m, tm, it.tn);
+    it.m0 = tm * BM;
     return true;
 }
 
 // The same for products that sum over an expert's rows: tiles_m x tiles_n tiles of C for
-// every expert, whatever its rows.
-__device__ __forceinline__ bool find_depth(const GroupedParams& q, int bid, GroupItem& it) {
+// every expert, whatever its rows.  An item's work goes with its expert's rows, so each
+// expert's tiles are dealt to all XCDs (a compact block of them to each), and the experts
+// come in order of their rows, the longest first, so that short items end the launch.  (Up to
+// 64 experts, one a lane; more come in their own order.)
+template <int BM>
+__device__ __forceinline__ bool find_depth(const GroupedParams& q, int bid, int lane,
+                                           GroupItem& it) {
     const int per = q.g.tiles_m * q.g.tiles_n;
     if (bid >= per * q.experts) return false;
-    const int lid = xcd_remap(bid, per * q.experts);
-    it.e = lid / per;
+    const int place = bid / per;
+    it.e = place;
+    if (q.experts <= 64) {
+        const int e = min(lane, q.experts - 1);
+        const int rows = lane < q.experts ? group_offset(q, e + 1) - group_offset(q, e) : -1;
+        int before = 0;
+        for (int j = 0; j < q.experts; ++j) {
+            const int other = __builtin_amdgcn_readlane(rows, j);
+            before += other > rows || (other == rows && j < lane);
+        }
+        it.e = __builtin_ctzll(__ballot(lane < q.experts && before == place));
+    }
     it.row0 = __builtin_amdgcn_readfirstlane(group_offset(q, it.e));
     const int n = __builtin_amdgcn_readfirstlane(group_offset(q, it.e + 1)) - it.row0;
     it.rows = n > 0 ? n : 0;
-    tile_coords(lid - it.e * per, q.g.tiles_m, q.g.tiles_n, q.g.group_m, it.tm, it.tn);
+    int tm;
+    tile_coords(xcd_remap(bid - place * per, per), q.g.tiles_m, q.g.tiles_n, q.g.group_m, tm,
+                it.tn);
+    it.m0 = tm * BM;
     return true;
 }
 
@@ -211,12 +237,12 @@ __global__ void __launch_bounds__(256) grouped_any_kernel(const GroupedParams q)
     const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63;
     GroupItem it;
     if constexpr (TA) {
-        if (!find_depth(q, blockIdx.x, it)) return;
+        if (!find_depth<T>(q, blockIdx.x, lane, it)) return;
     } else {
         if (!find_rows<T>(q, blockIdx.x, lane, it)) return;
     }
     const Gemm16Params p = group_problem<TA, ESZ, CSZ>(q, it);
-    const int m0 = it.tm * T, n0 = it.tn * T;
+    const int m0 = it.m0, n0 = it.tn * T;
     f32x16 acc;
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.0f;

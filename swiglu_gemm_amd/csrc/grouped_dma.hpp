@@ -138,21 +138,32 @@ __device__ __forceinline__ void epilogue_swiglu_bwd_lds(const Gemm16Params& p, c
     }
 }
 
-template <int DT, bool TA, bool TB, int EPI, int BM, int BN, int BK, int S, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN, 1) grouped_dma_kernel(const GroupedParams q) {
-    using D = DmaShape<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>;
-    __shared__ __attribute__((aligned(1024))) char smem[D::LDS];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    GroupItem it;
+// Whether the partial K tile at the end of a tile's loop may be read whole: every row of
+// op(A) and op(B) it touches, to the end of the K tile, lies in front of the operands' ends
+// (the bytes past K are the next row's, the next expert's, or padding).
+template <bool TA, bool TB, int BM, int BN, int BK, int ESZ>
+__device__ __forceinline__ bool tail_readable(const GroupedParams& q, const GroupItem& it,
+                                              const Gemm16Params& p, int m0, int n0, int nkt) {
     if constexpr (TA) {
-        if (!find_depth(q, blockIdx.x, it)) return;
+        // k are rows of A and D; past the expert's rows come the next expert's
+        return it.row0 + (nkt + 1) * BK <= q.rows;
     } else {
-        if (!find_rows<BM>(q, blockIdx.x, lane, it)) return;
+        // A: k run along a row, so past K comes the next row, if there is one
+        const bool a_in = it.row0 + min(m0 + BM, p.M) < q.rows && (nkt + 1) * BK <= q.g.lda + p.K;
+        const bool more = it.e + 1 < q.experts && q.sB >= (int64_t)(TB ? p.N : p.K) * p.ldb * ESZ;
+        const bool b_in = TB ? (more || min(n0 + BN, p.N) < p.N) && (nkt + 1) * BK <= p.ldb + p.K
+                             : more && (nkt + 1) * BK - p.K <= p.K;
+        return a_in && b_in;
     }
-    const Gemm16Params p = group_problem<TA, D::ESZ, EPI == EPI_GEMM_F32 ? 4 : 2>(q, it);
-    const int m0 = it.tm * BM, n0 = it.tn * BN;
-    const int nkt = p.K / BK, ktail = p.K - nkt * BK;
+}
 
+template <int DT, bool TA, bool TB, int EPI, int BM, int BN, int BK, int S, int WM, int WN>
+__device__ __forceinline__ void grouped_tile(const GroupedParams& q, const GroupItem& it,
+                                             const Gemm16Params& p, char* smem, int wave,
+                                             int lane) {
+    using D = DmaShape<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>;
+    const int m0 = it.m0, n0 = it.tn * BN;
+    const int nkt = p.K / BK, ktail = p.K - nkt * BK;
     typename D::Acc acc;
 #pragma unroll
     for (int i = 0; i < D::FN; ++i)
@@ -160,8 +171,10 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) grouped_dma_kernel(const Grou
         for (int j = 0; j < D::FM; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    dma_mainloop<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>(p, smem, m0, n0, 0, nkt, ktail, acc, wave,
-                                                         lane);
+    const bool ring_tail =
+        ktail > 0 && tail_readable<TA, TB, BM, BN, BK, D::ESZ>(q, it, p, m0, n0, nkt);
+    dma_mainloop<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN, true>(p, smem, m0, n0, 0, nkt, ktail, acc,
+                                                               wave, lane, ring_tail);
     const int wm = wave % WM, wn = wave / WM;
     if constexpr (EPI == EPI_GEMM_F32)
         epilogue_f32_rows_lds<D::FM, D::FN, BM, BN, WN, 64 * WM * WN, D::LDS>(
@@ -174,51 +187,102 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) grouped_dma_kernel(const Grou
         dma_epilogue<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>(p, acc, smem, m0, n0, wave, lane);
 }
 
-// Tiles of the grouped products: those of the plain ones that suit runs of rows of every
-// length.  Index = configuration id (SG_FORCE_GROUPED=<id> overrides the choice; -1: the
-// kernel for every alignment).
+// Two work-groups a CU where the ring takes at most half of its LDS.
+constexpr int group_occ(int lds) { return lds <= 80 * 1024 ? 2 : 1; }
+
+// Tiles that run an expert's last rows on half of their height where that holds them (same
+// columns, same number of waves; measured 0.6 of the time of a whole one): the ones of 128
+// rows or more that products over rows take for long runs.
+constexpr bool group_half(bool ta, int bm, int bn, int wm, int wn) {
+    return !ta && ((bm == 256 && wm * wn == 8) || (bm == 128 && bn == 256 && wm * wn == 4));
+}
+
+template <int DT, bool TA, bool TB, int EPI, int BM, int BN, int BK, int S, int WM, int WN>
+__global__ void __launch_bounds__(
+    64 * WM * WN, group_occ(DmaShape<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>::LDS))
+    grouped_dma_kernel(const GroupedParams q) {
+    using D = DmaShape<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>;
+    constexpr bool HALF = group_half(TA, BM, BN, WM, WN);
+    constexpr int S2 = BM == 256 ? 3 : S, WM2 = BM == 256 ? 2 : 1, WN2 = 4;
+    constexpr int LDS_HALF = HALF ? S2 * (BM / 2 + BN) * BK * D::ESZ : 0;
+    __shared__ __attribute__((aligned(1024))) char smem[LDS_HALF > D::LDS ? LDS_HALF : D::LDS];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    GroupItem it;
+    if constexpr (TA) {
+        if (!find_depth<BM>(q, blockIdx.x, lane, it)) return;
+    } else {
+        if (!find_rows<BM>(q, blockIdx.x, lane, it)) return;
+    }
+    const Gemm16Params p = group_problem<TA, D::ESZ, EPI == EPI_GEMM_F32 ? 4 : 2>(q, it);
+    if constexpr (HALF) {
+        if (it.rows - it.m0 <= BM / 2) {
+            grouped_tile<DT, TA, TB, EPI, BM / 2, BN, BK, S2, WM2, WN2>(q, it, p, smem, wave, lane);
+            return;
+        }
+    }
+    grouped_tile<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN>(q, it, p, smem, wave, lane);
+}
+
+// Tiles of the grouped products.  Index = configuration id (SG_FORCE_GROUPED=<id> overrides
+// the choice; -1: the kernel for every alignment).  rate and fixed are the cost model's: TFLOP/s
+// of a CU and the time a tile costs beside its products (_d: products that sum over rows; 0:
+// not for these; 1 for 16-bit rows, which go by the mean length of a run instead).  They were fitted to
+// every tile forced on 51 problems (1 to 64 experts, 1 to 4096 rows each): the model's choice
+// is 0.4 % above the best tile in the mean for weight gradients, 1.5 % for e4m3 (both
+// layouts' products and SwiGLU).
+//
+// What the tiles are for (MI355X, bf16, weights cold): 32 x 128, which streams a weight for a
+// few rows: 64 experts of 4 rows, 2048 x 1536: 71 us, 81-84 us on the others.  128 x 256 with
+// a 32-deep ring, two work-groups a CU that fill each other's gaps: 32 uneven experts of 512
+// rows in the mean, 2048 x 2048: 158 us against 190 us for 256 x 256 (one work-group a CU,
+// whole rounds of long tiles) and 172 us for the 64-deep 128 x 256; 256 x 256 where experts
+// are long: 4096 rows of one 64 us against 67 us, 70 us.
 struct GroupCfg {
     int e4m3, BM, BN, BK, S, WM, WN;
+    double rate, fixed, rate_d, fixed_d;
     const char* name;
 };
 constexpr GroupCfg kGroupCfg[] = {
-    {0, 32, 128, 64, 4, 1, 4, "32x128x64 s4 1x4w"},
-    {0, 64, 128, 64, 4, 1, 4, "64x128x64 s4 1x4w"},
-    {0, 128, 128, 64, 2, 2, 4, "128x128x64 s2 2x4w"},
-    {0, 128, 256, 64, 3, 2, 4, "128x256x64 s3 2x4w"},
-    {0, 256, 256, 64, 2, 4, 2, "256x256x64 s2 4x2w"},
-    {1, 32, 128, 128, 4, 1, 4, "e4m3 32x128x128 s4 1x4w"},
-    {1, 128, 128, 128, 2, 2, 4, "e4m3 128x128x128 s2 2x4w"},
-    {1, 128, 256, 128, 3, 2, 4, "e4m3 128x256x128 s3 2x4w"},
-    {1, 256, 256, 128, 2, 4, 2, "e4m3 256x256x128 s2 4x2w"},
+    {0, 32, 128, 64, 4, 1, 4, 1.0, 0.0, 0.0, 0.0, "32x128x64 s4 1x4w"},
+    {0, 128, 128, 64, 2, 2, 4, 0.0, 0.0, 4.5, 4.22, "128x128x64 s2 2x4w"},
+    {0, 128, 256, 64, 3, 2, 4, 1.0, 0.0, 0.0, 0.0, "128x256x64 s3 2x4w"},
+    {0, 256, 256, 64, 2, 4, 2, 1.0, 0.0, 4.14, 5.4, "256x256x64 s2 4x2w"},
+    {0, 128, 256, 32, 3, 2, 2, 1.0, 0.0, 2.86, 0.93, "128x256x32 s3 2x2w"},
+    {1, 32, 128, 128, 4, 1, 4, 3.64, 4.18, 0.0, 0.0, "e4m3 32x128x128 s4 1x4w"},
+    {1, 128, 128, 128, 2, 2, 4, 7.41, 0.87, 0.0, 0.0, "e4m3 128x128x128 s2 2x4w"},
+    {1, 128, 256, 128, 3, 2, 4, 9.76, 4.73, 0.0, 0.0, "e4m3 128x256x128 s3 2x4w"},
+    {1, 256, 256, 128, 2, 4, 2, 11.42, 3.43, 0.0, 0.0, "e4m3 256x256x128 s2 4x2w"},
 };
 constexpr int kNumGroupCfg = sizeof(kGroupCfg) / sizeof(kGroupCfg[0]);
 
 #define SG_GROUPED_16(X)          \
     X(0, 32, 128, 64, 4, 1, 4)    \
-    X(1, 64, 128, 64, 4, 1, 4)    \
-    X(2, 128, 128, 64, 2, 2, 4)   \
-    X(3, 128, 256, 64, 3, 2, 4)   \
-    X(4, 256, 256, 64, 2, 4, 2)
-// products that sum over the rows: a transposed A's 32- and 64-row tiles are too narrow
+    X(2, 128, 256, 64, 3, 2, 4)   \
+    X(3, 256, 256, 64, 2, 4, 2)   \
+    X(4, 128, 256, 32, 3, 2, 2)
 #define SG_GROUPED_DEPTH(X)       \
-    X(2, 128, 128, 64, 2, 2, 4)   \
-    X(3, 128, 256, 64, 3, 2, 4)   \
-    X(4, 256, 256, 64, 2, 4, 2)
+    X(1, 128, 128, 64, 2, 2, 4)   \
+    X(3, 256, 256, 64, 2, 4, 2)   \
+    X(4, 128, 256, 32, 3, 2, 2)
 #define SG_GROUPED_8(X)           \
     X(5, 32, 128, 128, 4, 1, 4)   \
     X(6, 128, 128, 128, 2, 2, 4)  \
     X(7, 128, 256, 128, 3, 2, 4)  \
     X(8, 256, 256, 128, 2, 4, 2)
 
-#define SG_GROUP_ROW(ID, BM_, BN_, BK_, S_, WM_, WN_)                                          \
-    static_assert(kGroupCfg[ID].BM == BM_ && kGroupCfg[ID].BN == BN_ &&                        \
-                      kGroupCfg[ID].BK == BK_ && kGroupCfg[ID].S == S_ &&                      \
-                      kGroupCfg[ID].WM == WM_ && kGroupCfg[ID].WN == WN_,                      \
-                  "grouped row " #ID);
+constexpr bool group_row(int id, bool depth, int bm, int bn, int bk, int s, int wm, int wn) {
+    const GroupCfg& c = kGroupCfg[id];
+    return c.BM == bm && c.BN == bn && c.BK == bk && c.S == s && c.WM == wm && c.WN == wn &&
+           (depth ? c.rate_d : c.rate) > 0.0;
+}
+#define SG_GROUP_ROW(ID, BM, BN, BK, S, WM, WN) \
+    static_assert(group_row(ID, false, BM, BN, BK, S, WM, WN), "grouped row " #ID);
+#define SG_GROUP_ROW_D(ID, BM, BN, BK, S, WM, WN) \
+    static_assert(group_row(ID, true, BM, BN, BK, S, WM, WN), "grouped row " #ID);
 SG_GROUPED_16(SG_GROUP_ROW)
-SG_GROUPED_DEPTH(SG_GROUP_ROW)
 SG_GROUPED_8(SG_GROUP_ROW)
+SG_GROUPED_DEPTH(SG_GROUP_ROW_D)
 #undef SG_GROUP_ROW
+#undef SG_GROUP_ROW_D
 
 }  // namespace sg

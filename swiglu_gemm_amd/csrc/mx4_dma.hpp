@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_dma_kernel(const MxParams 
     GroupItem it;
     if (!find_rows<BM>(x.q, blockIdx.x, lane, it)) return;
     const Gemm16Params p = group_problem<false, 1, EPI == EPI_GEMM_F32 ? 4 : 2>(x.q, it);
-    const int m0 = it.tm * BM, n0 = it.tn * BN;
+    const int m0 = it.m0, n0 = it.tn * BN;
     typename D::Acc acc;
 #pragma unroll
     for (int i = 0; i < D::FN; ++i)
