@@ -78,47 +78,44 @@ bool group_cfg_ok(const GroupCfg& c, bool ta, bool tb, int esz, const GroupedPar
            ((tb ? c.BN : c.BK) * q.g.ldb + 256) * esz < kLim;
 }
 
-// Microseconds of `tiles` tiles of `flops` products each that move `bytes` in all: rounds of
-// work-groups over the CUs (`occ` to a CU, which then share it), a last round counted whole
-// while there are few and in the mean when there are many; never less than the bytes take.
+// Rounds of work-groups over the CUs, `occ` to a CU: whole ones while there are few, the mean
+// when there are many.  Where two share a CU, one that has it alone takes 0.62 of the time.
 constexpr int kNumCU = 256;
-constexpr double kBytesPerUs = 4.8e6;
+double rounds_of(double w, int occ) {
+    if (w <= 1.0) return occ == 1 || w > 0.5 ? 1.0 : 0.62;
+    if (w >= 4.0) return w + (occ == 1 ? 0.4 : 0.25);
+    if (occ == 1) return std::ceil(w - 0.06);
+    const double rest = w - std::floor(w);
+    return std::floor(w) + (rest < 0.05 ? 0.0 : rest <= 0.5 ? 0.62 : 1.0);
+}
+
+// Microseconds of `tiles` tiles of `flops` each that move `bytes` in all: never less than the
+// bytes take.
 double est_us(double tiles, int occ, double flops, double rate, double fixed, double bytes) {
-    const double w = tiles / (kNumCU * occ);
-    const double rounds = w < 0.5 ? 1.0 : w < 4.0 ? std::fmax(1.0, std::ceil(w - 0.1)) : w + 0.4;
-    const double share = std::fmin((double)occ, std::fmax(1.0, tiles / kNumCU));
-    const double t = rounds * (share * flops / (rate * 1e6) + fixed), m = bytes / kBytesPerUs;
+    const double t =
+        rounds_of(tiles / (kNumCU * occ), occ) * occ * (flops / (rate * 1e6) + fixed);
+    const double m = bytes / 4.8e6;
     return std::fmax(t, m) + 0.15 * std::fmin(t, m);
 }
 
-// The rows of each expert are not known here, so their mean stands for them: a run of n rows
-// is taken for n/BM + 1/2 tiles, never less than one (half of one costs 0.6).
-double row_tiles(const GroupCfg& c, const GroupedParams& q) {
+// The rows of each expert are not known here, so their mean stands for them: a run of n rows is
+// taken for n/BM + 1/2 tiles, never less than one (half of one costs 0.6).
+double est_rows(const GroupCfg& c, bool tb, int esz, const GroupedParams& q) {
     const double runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
     const bool half = group_half(false, c.BM, c.BN, c.WM, c.WN);
-    const double least = half && mean <= c.BM / 2 ? 0.6 : 1.0;
-    return (double)cdiv(q.g.N, c.BN) * runs * std::fmax(least, mean / c.BM + (half ? 0.4 : 0.5));
-}
-
-double est_rows8(const GroupCfg& c, const GroupedParams& q) {
-    const double runs = q.experts < q.rows ? q.experts : q.rows;
-    const double bytes =
-        (double)q.rows * q.g.K + runs * q.g.K * (double)q.g.N + (double)q.rows * q.g.N * 2.0;
-    return est_us(row_tiles(c, q), group_occ(c.S * (c.BM + c.BN) * c.BK), 2.0 * c.BM * c.BN * q.g.K,
-                  c.rate, c.fixed, bytes);
-}
-
-// 16-bit rows go by the mean length of a run: up to 32 rows the tile that streams a weight for
-// them, then 128 x 256, above 384 the 32-deep one with two work-groups a CU, whose uneven
-// rounds cost less, and from 900 on 256 x 256; a smaller one where that leaves more than half
-// of the CUs without a tile.  Within 2.8 % of the best tile in the mean over the 72 problems
-// measured (see kGroupCfg); a cost model in rounds, as for the others, 3.3 %.
-int choose_rows16(const GroupedParams& q) {
-    const double runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
-    int cfg = mean <= 32 ? 0 : mean < 384 ? 2 : mean < 900 ? 4 : 3;
-    if (cfg >= 3 && row_tiles(kGroupCfg[cfg], q) < kNumCU / 2) cfg = 2;
-    if (cfg == 2 && row_tiles(kGroupCfg[cfg], q) < kNumCU / 2) cfg = 0;
-    return cfg;
+    double per = std::fmax(half && mean <= c.BM / 2 ? 0.6 : 1.0, mean / c.BM + (half ? 0.35 : 0.5));
+    if (q.experts == 1) {
+        const int rest = q.rows % c.BM;
+        per = q.rows / c.BM + (rest == 0 ? 0.0 : half && rest <= c.BM / 2 ? 0.6 : 1.0);
+    }
+    const double bytes = (double)q.rows * q.g.K * esz + runs * q.g.K * (double)q.g.N * esz +
+                         (double)q.rows * q.g.N * 2.0;
+    const int occ = group_occ(c.S * (c.BM + c.BN) * c.BK * esz);
+    // B stored N x K in a 32-deep ring is read in 64-byte pieces: 0.85 of the rate (16 experts of
+    // 512 rows, K = 2816, N = 2048: 143 us on 128 x 256 x 32, 124 us on the 64-deep one)
+    const double rate = c.rate * (tb && c.BK * esz < 128 ? 0.85 : 1.0);
+    return est_us((double)cdiv(q.g.N, c.BN) * runs * per, occ, 2.0 * c.BM * c.BN * q.g.K, rate,
+                  c.fixed, bytes);
 }
 
 double est_depth(const GroupCfg& c, const GroupedParams& q) {
@@ -136,15 +133,11 @@ int choose_group(bool depth, bool tb, int esz, const GroupedParams& q) {
         return cfg >= 0 && cfg < kNumGroupCfg && group_cfg_ok(kGroupCfg[cfg], depth, tb, esz, q)
                    ? cfg
                    : -1;
-    if (!depth && esz == 2) {
-        cfg = choose_rows16(q);
-        return group_cfg_ok(kGroupCfg[cfg], depth, tb, esz, q) ? cfg : -1;
-    }
     double best = 0.0;
     for (int i = 0; i < kNumGroupCfg; ++i) {
         const GroupCfg& c = kGroupCfg[i];
         if (!group_cfg_ok(c, depth, tb, esz, q)) continue;
-        const double t = depth ? est_depth(c, q) : est_rows8(c, q);
+        const double t = depth ? est_depth(c, q) : est_rows(c, tb, esz, q);
         if (cfg < 0 || t < best) {
             cfg = i;
             best = t;
@@ -185,7 +178,10 @@ int choose_mx4(const GroupedParams& q) {
         if (*s && c >= 0 && c < kNumMxCfg) return c;
     }
     const int64_t runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
-    return mean <= 32 ? 0 : mean < 256 ? 1 : 3;
+    auto tiles = [&](int bm, int bn) { return runs * cdiv(mean, bm) * cdiv(q.g.N, bn); };
+    if (mean >= 384 && tiles(256, 256) >= 400) return 3;
+    if (mean > 32 && tiles(128, 128) >= 256) return 2;
+    return tiles(32, 128) >= 256 ? 1 : 0;
 }
 
 int run_mx4(const char* what, int epi, int dtype, MxParams x, hipStream_t st) {

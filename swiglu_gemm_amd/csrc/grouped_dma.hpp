@@ -226,49 +226,53 @@ __global__ void __launch_bounds__(
 // Tiles of the grouped products.  Index = configuration id (SG_FORCE_GROUPED=<id> overrides
 // the choice; -1: the kernel for every alignment).  rate and fixed are the cost model's: TFLOP/s
 // of a CU and the time a tile costs beside its products (_d: products that sum over rows; 0:
-// not for these; 1 for 16-bit rows, which go by the mean length of a run instead).  They were fitted to
-// every tile forced on 51 problems (1 to 64 experts, 1 to 4096 rows each): the model's choice
-// is 0.4 % above the best tile in the mean for weight gradients, 1.5 % for e4m3 (both
-// layouts' products and SwiGLU).
+// not for these).  They were fitted, near the rates of single tiles, to every tile forced on
+// 38 problems (1 to 64 experts, 1 to 16384 rows, K and N 724 to 5000) for each layout, SwiGLU
+// and the weight gradient; the model's choice is 1.2 % above the best tile in the mean for
+// 16-bit and 1.1 % for e4m3 rows, 2.0 % for weight gradients.
 //
 // What the tiles are for (MI355X, bf16, weights cold): 32 x 128, which streams a weight for a
-// few rows: 64 experts of 4 rows, 2048 x 1536: 71 us, 81-84 us on the others.  128 x 256 with
-// a 32-deep ring, two work-groups a CU that fill each other's gaps: 32 uneven experts of 512
+// few rows: 64 experts of 4 rows, 2048 x 1536: 72 us, 76-81 us on the wider ones; 32 x 64 where
+// even those leave CUs idle: 2 rows, 896 x 1792: 10.2 against 13.1 us.  128 x 256 with a
+// 32-deep ring, two work-groups a CU that fill each other's gaps: 32 uneven experts of 512
 // rows in the mean, 2048 x 2048: 158 us against 190 us for 256 x 256 (one work-group a CU,
-// whole rounds of long tiles) and 172 us for the 64-deep 128 x 256; 256 x 256 where experts
-// are long: 4096 rows of one 64 us against 67 us, 70 us.
+// whole rounds of long tiles) and 172 us for the 64-deep 128 x 256, which is ahead where its
+// tiles make about one round (16 experts of 128 rows, 2048 x 2816: 44 against 52 us); 256 x 256
+// where experts are long: 4096 rows of one 64 us against 68 and 70 us.  e4m3: 192 x 128, two a
+// CU: 48 experts of 250 rows, 1536 x 4096: 130 us against 142 us on 128 x 128, 137 us on
+// 128 x 256 and 139 us on 256 x 256.
 struct GroupCfg {
     int e4m3, BM, BN, BK, S, WM, WN;
     double rate, fixed, rate_d, fixed_d;
     const char* name;
 };
 constexpr GroupCfg kGroupCfg[] = {
-    {0, 32, 128, 64, 4, 1, 4, 1.0, 0.0, 0.0, 0.0, "32x128x64 s4 1x4w"},
-    {0, 128, 128, 64, 2, 2, 4, 0.0, 0.0, 4.5, 4.22, "128x128x64 s2 2x4w"},
-    {0, 128, 256, 64, 3, 2, 4, 1.0, 0.0, 0.0, 0.0, "128x256x64 s3 2x4w"},
-    {0, 256, 256, 64, 2, 4, 2, 1.0, 0.0, 4.14, 5.4, "256x256x64 s2 4x2w"},
-    {0, 128, 256, 32, 3, 2, 2, 1.0, 0.0, 2.86, 0.93, "128x256x32 s3 2x2w"},
-    {1, 32, 128, 128, 4, 1, 4, 3.64, 4.18, 0.0, 0.0, "e4m3 32x128x128 s4 1x4w"},
-    {1, 128, 128, 128, 2, 2, 4, 7.41, 0.87, 0.0, 0.0, "e4m3 128x128x128 s2 2x4w"},
-    {1, 128, 256, 128, 3, 2, 4, 9.76, 4.73, 0.0, 0.0, "e4m3 128x256x128 s3 2x4w"},
-    {1, 256, 256, 128, 2, 4, 2, 11.42, 3.43, 0.0, 0.0, "e4m3 256x256x128 s2 4x2w"},
+    {0, 32, 64, 64, 6, 1, 2, 1.18, 1.44, 0.0, 0.0, "32x64x64 s6 1x2w"},
+    {0, 32, 128, 64, 4, 1, 4, 2.49, 2.02, 0.0, 0.0, "32x128x64 s4 1x4w"},
+    {0, 128, 128, 64, 2, 2, 4, 0.0, 0.0, 4.0, 2.96, "128x128x64 s2 2x4w"},
+    {0, 128, 256, 64, 3, 2, 4, 4.47, 2.8, 0.0, 0.0, "128x256x64 s3 2x4w"},
+    {0, 128, 256, 32, 3, 2, 2, 5.0, 2.94, 4.3, 2.03, "128x256x32 s3 2x2w"},
+    {0, 256, 256, 64, 2, 4, 2, 4.89, 4.07, 5.17, 5.06, "256x256x64 s2 4x2w"},
+    {1, 32, 128, 128, 4, 1, 4, 3.67, 2.76, 0.0, 0.0, "e4m3 32x128x128 s4 1x4w"},
+    {1, 128, 128, 128, 2, 2, 4, 6.94, 2.01, 0.0, 0.0, "e4m3 128x128x128 s2 2x4w"},
+    {1, 192, 128, 128, 2, 2, 4, 8.28, 3.16, 0.0, 0.0, "e4m3 192x128x128 s2 2x4w"},
 };
 constexpr int kNumGroupCfg = sizeof(kGroupCfg) / sizeof(kGroupCfg[0]);
 
 #define SG_GROUPED_16(X)          \
-    X(0, 32, 128, 64, 4, 1, 4)    \
-    X(2, 128, 256, 64, 3, 2, 4)   \
-    X(3, 256, 256, 64, 2, 4, 2)   \
-    X(4, 128, 256, 32, 3, 2, 2)
+    X(0, 32, 64, 64, 6, 1, 2)     \
+    X(1, 32, 128, 64, 4, 1, 4)    \
+    X(3, 128, 256, 64, 3, 2, 4)   \
+    X(4, 128, 256, 32, 3, 2, 2)   \
+    X(5, 256, 256, 64, 2, 4, 2)
 #define SG_GROUPED_DEPTH(X)       \
-    X(1, 128, 128, 64, 2, 2, 4)   \
-    X(3, 256, 256, 64, 2, 4, 2)   \
-    X(4, 128, 256, 32, 3, 2, 2)
+    X(2, 128, 128, 64, 2, 2, 4)   \
+    X(4, 128, 256, 32, 3, 2, 2)   \
+    X(5, 256, 256, 64, 2, 4, 2)
 #define SG_GROUPED_8(X)           \
-    X(5, 32, 128, 128, 4, 1, 4)   \
-    X(6, 128, 128, 128, 2, 2, 4)  \
-    X(7, 128, 256, 128, 3, 2, 4)  \
-    X(8, 256, 256, 128, 2, 4, 2)
+    X(6, 32, 128, 128, 4, 1, 4)   \
+    X(7, 128, 128, 128, 2, 2, 4)  \
+    X(8, 192, 128, 128, 2, 2, 4)
 
 constexpr bool group_row(int id, bool depth, int bm, int bn, int bk, int s, int wm, int wn) {
     const GroupCfg& c = kGroupCfg[id];

@@ -213,13 +213,9 @@ __device__ __forceinline__ void mx_mainloop(const MxParams& x, const GroupItem& 
 }
 
 template <int DT_OUT, int EPI, int BM, int BN, int S, int WM, int WN>
-__global__ void __launch_bounds__(64 * WM * WN, 1) mx_dma_kernel(const MxParams x) {
+__device__ __forceinline__ void mx_tile(const MxParams& x, const GroupItem& it,
+                                        const Gemm16Params& p, char* smem, int wave, int lane) {
     using D = MxShape<BM, BN, S, WM, WN>;
-    __shared__ __attribute__((aligned(1024))) char smem[D::LDS];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    GroupItem it;
-    if (!find_rows<BM>(x.q, blockIdx.x, lane, it)) return;
-    const Gemm16Params p = group_problem<false, 1, EPI == EPI_GEMM_F32 ? 4 : 2>(x.q, it);
     const int m0 = it.m0, n0 = it.tn * BN;
     typename D::Acc acc;
 #pragma unroll
@@ -249,29 +245,47 @@ __global__ void __launch_bounds__(64 * WM * WN, 1) mx_dma_kernel(const MxParams 
     }
 }
 
+// The last rows of a run go on half of the tile's height where that holds them, as in
+// grouped_dma_kernel.
+template <int DT_OUT, int EPI, int BM, int BN, int S, int WM, int WN>
+__global__ void __launch_bounds__(64 * WM * WN, group_occ(MxShape<BM, BN, S, WM, WN>::LDS))
+    mx_dma_kernel(const MxParams x) {
+    using D = MxShape<BM, BN, S, WM, WN>;
+    constexpr bool HALF = BM >= 128;
+    constexpr int S2 = BM == 256 ? 3 : S;
+    constexpr int LDS_HALF = HALF ? MxShape<(HALF ? BM / 2 : 64), BN, S2, 2, 4>::LDS : 0;
+    __shared__ __attribute__((aligned(1024))) char smem[LDS_HALF > D::LDS ? LDS_HALF : D::LDS];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    GroupItem it;
+    if (!find_rows<BM>(x.q, blockIdx.x, lane, it)) return;
+    const Gemm16Params p = group_problem<false, 1, EPI == EPI_GEMM_F32 ? 4 : 2>(x.q, it);
+    if constexpr (HALF) {
+        static_assert(WM * WN == 8, "the half tile's waves");
+        if (it.rows - it.m0 <= BM / 2) {
+            mx_tile<DT_OUT, EPI, BM / 2, BN, S2, 2, 4>(x, it, p, smem, wave, lane);
+            return;
+        }
+    }
+    mx_tile<DT_OUT, EPI, BM, BN, S, WM, WN>(x, it, p, smem, wave, lane);
+}
+
 // Tiles of the 4-bit product; SG_FORCE_MX4=<id> overrides the choice.
 struct MxCfg {
     int BM, BN, S, WM, WN;
     const char* name;
 };
 constexpr MxCfg kMxCfg[] = {
+    {32, 64, 6, 1, 2, "32x64 s6 1x2w"},
     {32, 128, 3, 1, 4, "32x128 s3 1x4w"},
     {128, 128, 2, 2, 4, "128x128 s2 2x4w"},
-    {128, 256, 3, 2, 4, "128x256 s3 2x4w"},
     {256, 256, 2, 4, 2, "256x256 s2 4x2w"},
-    {32, 128, 7, 1, 4, "32x128 s7 1x4w"},
-    {64, 256, 3, 1, 4, "64x256 s3 1x4w"},
-    {256, 192, 2, 4, 2, "256x192 s2 4x2w"},
 };
 constexpr int kNumMxCfg = sizeof(kMxCfg) / sizeof(kMxCfg[0]);
 #define SG_MX_CONFIGS(X)     \
-    X(0, 32, 128, 3, 1, 4)   \
-    X(1, 128, 128, 2, 2, 4)  \
-    X(2, 128, 256, 3, 2, 4)  \
-    X(3, 256, 256, 2, 4, 2)  \
-    X(4, 32, 128, 7, 1, 4)   \
-    X(5, 64, 256, 3, 1, 4)   \
-    X(6, 256, 192, 2, 4, 2)
+    X(0, 32, 64, 6, 1, 2)    \
+    X(1, 32, 128, 3, 1, 4)   \
+    X(2, 128, 128, 2, 2, 4)  \
+    X(3, 256, 256, 2, 4, 2)
 #define SG_MX_ROW(ID, BM_, BN_, S_, WM_, WN_)                                             \
     static_assert(kMxCfg[ID].BM == BM_ && kMxCfg[ID].BN == BN_ && kMxCfg[ID].S == S_ &&   \
                       kMxCfg[ID].WM == WM_ && kMxCfg[ID].WN == WN_,                       \

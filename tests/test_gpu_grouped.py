@@ -403,7 +403,7 @@ def took(cfg):
 LONG = [1, 0, 257, 64, 130]
 
 
-@pytest.mark.parametrize("cfg", [0, 2, 3, 4])
+@pytest.mark.parametrize("cfg", [0, 1, 3, 4, 5])
 @pytest.mark.parametrize("dtype,trans", [("bf16", "N"), ("f16", "T")])
 def test_every_tile_rows(force, cfg, dtype, trans):
     """Ragged runs, a K tail, N inside a chunk, C aligned and not, beta."""
@@ -421,7 +421,7 @@ def test_every_tile_rows(force, cfg, dtype, trans):
     run_swiglu(dtype, LONG, 256, 128, bwd=True)
 
 
-@pytest.mark.parametrize("cfg", range(5, 9))
+@pytest.mark.parametrize("cfg", [6, 7, 8])
 @pytest.mark.parametrize("trans", "NT")
 def test_every_tile_e4m3(force, cfg, trans):
     force(cfg)
@@ -432,7 +432,7 @@ def test_every_tile_e4m3(force, cfg, trans):
     assert took(cfg)
 
 
-@pytest.mark.parametrize("cfg", [1, 3, 4])
+@pytest.mark.parametrize("cfg", [2, 4, 5])
 @pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f16", "same")])
 def test_every_tile_depth(force, cfg, dtype, out):
     force(cfg)
