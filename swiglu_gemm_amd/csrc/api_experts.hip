@@ -155,8 +155,9 @@ int run_rows(const char* what, int epi, bool tb, int dtype, GroupedParams q, hip
     q.g.tiles_n = (int)cdiv(q.g.N, bn);
     q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0;
     describe("%s cfg=%d %s", what, cfg, cfg < 0 ? "any 64x64x32" : kGroupCfg[cfg].name);
-    return status_of(launch_dt(dtype, epi, false, tb, cfg, q,
-                               most_row_tiles(q.rows, q.experts, bm) * q.g.tiles_n, st));
+    return status_of(launch_dt(
+        dtype, epi, false, tb, cfg, q,
+        group_blocks(most_row_tiles(q.rows, q.experts, bm) * q.g.tiles_n, 2), st));
 }
 
 // Products that sum over the rows of each expert.
@@ -194,10 +195,11 @@ int run_mx4(const char* what, int epi, int dtype, MxParams x, hipStream_t st) {
     q.g.tiles_n = (int)cdiv(q.g.N, c.BN);
     q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0;
     const int64_t tiles_m = q.offsets ? most_row_tiles(q.rows, q.experts, c.BM) : cdiv(q.rows, c.BM);
-    if (tiles_m * q.g.tiles_n > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
+    const int64_t blocks = group_blocks(tiles_m * q.g.tiles_n, 2);
+    if (blocks > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
     describe("%s cfg=%d %s", what, cfg, c.name);
     return status_of(launch_mx4(epi, dtype == SG_F16 ? DT_F16 : DT_BF16, cfg, x,
-                                (unsigned)(tiles_m * q.g.tiles_n), st));
+                                (unsigned)blocks, st));
 }
 
 }  // namespace

@@ -44,18 +44,54 @@ __device__ __forceinline__ int group_offset(const GroupedParams& q, int e) {
 }
 
 // The work of one work-group: expert e, whose rows are [row0, row0 + rows), and the rows from
-// m0 on and columns from tile tn of its product.
+// m0 on and columns from tile tn of its product; half: only half of the tile's rows.
 struct GroupItem {
     int e, row0, rows, m0, tn;
+    bool half;
 };
 
-// The sum of x over the lanes up to and including this one.
-__device__ __forceinline__ int lane_scan(int x, int lane) {
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int up = __shfl_up(x, d);
-        if (lane >= d) x += up;
+// The item of work-group `bid` among `total`: consecutive items share an XCD (as xcd_remap).
+// OCC > 0 (the work-groups of a CU, for kernels that have a tile of half the rows): where the
+// items of an XCD leave its last round at most half full, that round's items are split into
+// two halves each, which finish it in 0.6 of the time (32 uneven experts, 16384 rows, see
+// kGroupCfg).  The launch has room for them: group_blocks().
+constexpr int kXcds = 8, kXcdCus = 32;
+template <int OCC>
+__device__ __forceinline__ bool xcd_item(int bid, int total, int& lid, int& part) {
+    part = -1;
+    if (total < kXcds) {
+        lid = bid;
+        return bid < total;
     }
+    const int x = bid % kXcds, i = bid / kXcds, per = total / kXcds, rem = total % kXcds;
+    const int n = per + (x < rem), first = x * per + min(x, rem);
+    int split = 0;
+    if constexpr (OCC > 0) {
+        constexpr int slots = kXcdCus * OCC;
+        split = n % slots;
+        if (n <= slots || 2 * split > slots) split = 0;
+    }
+    const int j = i - (n - split);
+    if (j >= 2 * split) return false;
+    lid = first + (j < 0 ? i : n - split + j / 2);
+    if (j >= 0) part = j & 1;
+    return true;
+}
+inline int64_t group_blocks(int64_t items, int occ) { return items + kXcds * kXcdCus * occ / 2; }
+
+// The sum of x over the lanes up to and including this one: data-parallel moves within rows of
+// 16 lanes (row_shr), then the rows' last values to the rows behind (row_bcast).
+template <int CTRL, int ROWS, int BANKS>
+__device__ __forceinline__ int lane_moved(int x) {
+    return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, BANKS, false);
+}
+__device__ __forceinline__ int lane_scan(int x) {
+    x += lane_moved<0x111, 0xf, 0xf>(x);       // row_shr:1
+    x += lane_moved<0x112, 0xf, 0xf>(x);       // row_shr:2
+    x += lane_moved<0x114, 0xf, 0xe>(x);       // row_shr:4
+    x += lane_moved<0x118, 0xf, 0xc>(x);       // row_shr:8
+    x += lane_moved<0x142, 0xa, 0xf>(x);       // row_bcast:15
+    x += lane_moved<0x143, 0xc, 0xf>(x);       // row_bcast:31
     return x;
 }
 
@@ -65,45 +101,50 @@ __device__ __forceinline__ int lane_scan(int x, int lane) {
 // ceil(experts / 64), a scan over the lanes finds the one that holds the item, and its
 // experts are walked.  Consecutive items share an XCD, and an expert's items follow one
 // another, so that its weight is read while it is in that XCD's L2.
-template <int BM>
+template <int BM, int OCC = 0>
 __device__ __forceinline__ bool find_rows(const GroupedParams& q, int bid, int lane,
                                           GroupItem& it) {
     const int tiles_n = q.g.tiles_n;
-    int tm;
+    int tm, lid, part;
     if (!q.offsets) {
         const int tiles_m = (q.rows + BM - 1) / BM;
-        if (bid >= tiles_m * tiles_n) return false;
+        if (!xcd_item<OCC>(bid, tiles_m * tiles_n, lid, part)) return false;
         it.e = 0;
         it.row0 = 0;
         it.rows = q.rows;
-        tile_coords(xcd_remap(bid, tiles_m * tiles_n), tiles_m, tiles_n, q.g.group_m, tm, it.tn);
-        it.m0 = tm * BM;
-        return true;
+        tile_coords(lid, tiles_m, tiles_n, q.g.group_m, tm, it.tn);
+        it.m0 = tm * BM + (part > 0 ? BM / 2 : 0);
+        it.half = part >= 0;
+        return it.m0 < it.rows;
     }
     const int per = (q.experts + 63) / 64;
-    int mine = 0;
+    int mine = 0, row = 0, len = 0;                // row, len: the lane's last expert
     for (int j = 0; j < per; ++j) {
         const int e = lane * per + j;
         if (e >= q.experts) break;
-        const int n = group_offset(q, e + 1) - group_offset(q, e);
-        if (n > 0) mine += (n + BM - 1) / BM;
+        row = group_offset(q, e);
+        len = group_offset(q, e + 1) - row;
+        if (len > 0) mine += (len + BM - 1) / BM;
     }
-    const int incl = lane_scan(mine, lane);
+    const int incl = lane_scan(mine);
     const int total = __builtin_amdgcn_readlane(incl, 63) * tiles_n;
-    if (bid >= total) return false;
-    const int lid = xcd_remap(bid, total);
+    if (!xcd_item<OCC>(bid, total, lid, part)) return false;
     const uint64_t past = __ballot(incl * tiles_n > lid);
     if (past == 0) return false;
     const int owner = __builtin_ctzll(past);
     int first = __builtin_amdgcn_readlane(incl - mine, owner) * tiles_n;
     const int last = min(q.experts, (owner + 1) * per) - 1;
-    int e = owner * per, row0 = 0, n = 0, tiles_m = 0;
-    for (;; ++e) {
-        row0 = __builtin_amdgcn_readfirstlane(group_offset(q, e));
-        n = __builtin_amdgcn_readfirstlane(group_offset(q, e + 1)) - row0;
-        tiles_m = n > 0 ? (n + BM - 1) / BM : 0;
-        if (lid < first + tiles_m * tiles_n || e >= last) break;
-        first += tiles_m * tiles_n;
+    int e = owner * per;
+    int row0 = __builtin_amdgcn_readlane(row, owner), n = __builtin_amdgcn_readlane(len, owner);
+    int tiles_m = n > 0 ? (n + BM - 1) / BM : 0;
+    if (per > 1) {
+        for (;; ++e) {
+            row0 = __builtin_amdgcn_readfirstlane(group_offset(q, e));
+            n = __builtin_amdgcn_readfirstlane(group_offset(q, e + 1)) - row0;
+            tiles_m = n > 0 ? (n + BM - 1) / BM : 0;
+            if (lid < first + tiles_m * tiles_n || e >= last) break;
+            first += tiles_m * tiles_n;
+        }
     }
     // a table that does not ascend can count more tiles than an int holds: no item then
     if (lid < first || lid - first >= tiles_m * tiles_n) return false;
@@ -111,8 +152,9 @@ __device__ __forceinline__ bool find_rows(const GroupedParams& q, int bid, int l
     it.row0 = row0;
     it.rows = n;
     tile_coords(lid - first, tiles_m, tiles_n, q.g.group_m, tm, it.tn);
-    it.m0 = tm * BM;
-    return true;
+    it.m0 = tm * BM + (part > 0 ? BM / 2 : 0);
+    it.half = part >= 0;
+    return it.m0 < n;
 }
 
 // The same for products that sum over an expert's rows: tiles_m x tiles_n tiles of C for
@@ -126,19 +168,23 @@ __device__ __forceinline__ bool find_depth(const GroupedParams& q, int bid, int 
     const int per = q.g.tiles_m * q.g.tiles_n;
     if (bid >= per * q.experts) return false;
     const int place = bid / per;
-    it.e = place;
+    int n;
     if (q.experts <= 64) {
-        const int e = min(lane, q.experts - 1);
-        const int rows = lane < q.experts ? group_offset(q, e + 1) - group_offset(q, e) : -1;
+        const int e = min(lane, q.experts - 1), row = group_offset(q, e);
+        const int rows = lane < q.experts ? group_offset(q, e + 1) - row : -1;
         int before = 0;
         for (int j = 0; j < q.experts; ++j) {
             const int other = __builtin_amdgcn_readlane(rows, j);
             before += other > rows || (other == rows && j < lane);
         }
         it.e = __builtin_ctzll(__ballot(lane < q.experts && before == place));
+        it.row0 = __builtin_amdgcn_readlane(row, it.e);
+        n = __builtin_amdgcn_readlane(rows, it.e);
+    } else {
+        it.e = place;
+        it.row0 = __builtin_amdgcn_readfirstlane(group_offset(q, place));
+        n = __builtin_amdgcn_readfirstlane(group_offset(q, place + 1)) - it.row0;
     }
-    it.row0 = __builtin_amdgcn_readfirstlane(group_offset(q, it.e));
-    const int n = __builtin_amdgcn_readfirstlane(group_offset(q, it.e + 1)) - it.row0;
     it.rows = n > 0 ? n : 0;
     int tm;
     tile_coords(xcd_remap(bid - place * per, per), q.g.tiles_m, q.g.tiles_n, q.g.group_m, tm,

@@ -211,11 +211,11 @@ __global__ void __launch_bounds__(
     if constexpr (TA) {
         if (!find_depth<BM>(q, blockIdx.x, lane, it)) return;
     } else {
-        if (!find_rows<BM>(q, blockIdx.x, lane, it)) return;
+        if (!find_rows<BM, HALF ? group_occ(D::LDS) : 0>(q, blockIdx.x, lane, it)) return;
     }
     const Gemm16Params p = group_problem<TA, D::ESZ, EPI == EPI_GEMM_F32 ? 4 : 2>(q, it);
     if constexpr (HALF) {
-        if (it.rows - it.m0 <= BM / 2) {
+        if (it.half || it.rows - it.m0 <= BM / 2) {
             grouped_tile<DT, TA, TB, EPI, BM / 2, BN, BK, S2, WM2, WN2>(q, it, p, smem, wave, lane);
             return;
         }

@@ -161,8 +161,9 @@ __global__ void __launch_bounds__(256) mx_quantize_kernel(const MxQuantParams p)
 #pragma unroll
         for (int e = 0; e < 8; ++e)
             t = max(t, __builtin_bit_cast(uint32_t, v[i][e]) & 0x7fffffffu);
-        t = max(t, (uint32_t)__shfl_xor((int)t, 1));
-        t = max(t, (uint32_t)__shfl_xor((int)t, 2));
+        // over the block's four lanes: quad_perm [1,0,3,2], then [2,3,0,1]
+        t = max(t, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t, 0xB1, 0xf, 0xf, false));
+        t = max(t, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)t, 0x4E, 0xf, 0xf, false));
         const bool bad = t >= 0x7f800000u;
         const int s = bad ? kMxNaN : max((int)(t >> 23) - 2, 0);
         float y[8];

@@ -257,11 +257,11 @@ __global__ void __launch_bounds__(64 * WM * WN, group_occ(MxShape<BM, BN, S, WM,
     __shared__ __attribute__((aligned(1024))) char smem[LDS_HALF > D::LDS ? LDS_HALF : D::LDS];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     GroupItem it;
-    if (!find_rows<BM>(x.q, blockIdx.x, lane, it)) return;
+    if (!find_rows<BM, HALF ? group_occ(D::LDS) : 0>(x.q, blockIdx.x, lane, it)) return;
     const Gemm16Params p = group_problem<false, 1, EPI == EPI_GEMM_F32 ? 4 : 2>(x.q, it);
     if constexpr (HALF) {
         static_assert(WM * WN == 8, "the half tile's waves");
-        if (it.rows - it.m0 <= BM / 2) {
+        if (it.half || it.rows - it.m0 <= BM / 2) {
             mx_tile<DT_OUT, EPI, BM / 2, BN, S2, 2, 4>(x, it, p, smem, wave, lane);
             return;
         }
