@@ -1150,8 +1150,10 @@ int check_gemm(char transA, char transB, int64_t M, int64_t N, int64_t K, float 
 
 namespace sg {
 // the description sg_last_config() returns, for the entry points of api_experts.hip
-void set_last_config(const char* text) {
-    std::snprintf(g_last_cfg, sizeof(g_last_cfg), "%s", text);
+void set_last_config(const char* text, size_t len) {
+    if (len >= sizeof(g_last_cfg)) len = sizeof(g_last_cfg) - 1;
+    std::memcpy(g_last_cfg, text, len);
+    g_last_cfg[len] = 0;
 }
 }  // namespace sg
 

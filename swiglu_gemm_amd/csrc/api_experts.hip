@@ -6,8 +6,8 @@
 
 #include <cmath>
 #include <cstdint>
-#include <cstdio>
 #include <cstdlib>
+#include <cstddef>
 
 #include "grouped.hpp"
 #include "grouped_dma.hpp"
@@ -19,7 +19,7 @@
 using namespace sg;
 
 namespace sg {
-void set_last_config(const char* text);   // api.hip
+void set_last_config(const char* text, size_t len);   // api.hip
 }
 
 namespace {
@@ -40,11 +40,24 @@ int64_t most_row_tiles(int64_t M, int64_t experts, int bm) {
     return (M + runs * (bm - 1)) / bm;
 }
 
-template <typename... A>
-void describe(const char* format, A... args) {
+// "<what> cfg=<id> <name>" for sg_last_config(); put together by hand: snprintf takes half a
+// microsecond of calls that take eight.
+void describe(const char* what, int cfg, const char* name) {
     char text[160];
-    std::snprintf(text, sizeof(text), format, args...);
-    set_last_config(text);
+    size_t n = 0;
+    auto put = [&](const char* s) {
+        while (*s && n + 1 < sizeof(text)) text[n++] = *s++;
+    };
+    put(what);
+    if (cfg >= -1) {
+        const char digits[] = {(char)('0' + cfg / 10), (char)('0' + cfg % 10), 0};
+        put(" cfg=");
+        put(cfg < 0 ? "-1" : cfg < 10 ? digits + 1 : digits);
+        put(" ");
+        put(name);
+    }
+    text[n] = 0;
+    set_last_config(text, n);
 }
 
 hipError_t launch_dt(int dtype, int epi, bool ta, bool tb, int cfg, const GroupedParams& q,
@@ -154,7 +167,7 @@ int run_rows(const char* what, int epi, bool tb, int dtype, GroupedParams q, hip
     q.g.group_m = 4;
     q.g.tiles_n = (int)cdiv(q.g.N, bn);
     q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0;
-    describe("%s cfg=%d %s", what, cfg, cfg < 0 ? "any 64x64x32" : kGroupCfg[cfg].name);
+    describe(what, cfg, cfg < 0 ? "any 64x64x32" : kGroupCfg[cfg].name);
     return status_of(launch_dt(
         dtype, epi, false, tb, cfg, q,
         group_blocks(most_row_tiles(q.rows, q.experts, bm) * q.g.tiles_n, 2), st));
@@ -168,7 +181,7 @@ int run_depth(const char* what, int epi, int dtype, GroupedParams q, hipStream_t
     q.g.tiles_m = (int)cdiv(q.g.M, bm);
     q.g.tiles_n = (int)cdiv(q.g.N, bn);
     q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0 && q.sC % 8 == 0;
-    describe("%s cfg=%d %s", what, cfg, cfg < 0 ? "any 64x64x32" : kGroupCfg[cfg].name);
+    describe(what, cfg, cfg < 0 ? "any 64x64x32" : kGroupCfg[cfg].name);
     return status_of(launch_dt(dtype, epi, true, false, cfg, q,
                                (int64_t)q.experts * q.g.tiles_m * q.g.tiles_n, st));
 }
@@ -197,7 +210,7 @@ int run_mx4(const char* what, int epi, int dtype, MxParams x, hipStream_t st) {
     const int64_t tiles_m = q.offsets ? most_row_tiles(q.rows, q.experts, c.BM) : cdiv(q.rows, c.BM);
     const int64_t blocks = group_blocks(tiles_m * q.g.tiles_n, 2);
     if (blocks > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
-    describe("%s cfg=%d %s", what, cfg, c.name);
+    describe(what, cfg, c.name);
     return status_of(launch_mx4(epi, dtype == SG_F16 ? DT_F16 : DT_BF16, cfg, x,
                                 (unsigned)blocks, st));
 }
@@ -390,7 +403,7 @@ int sg_mxfp4_quantize(const void* X, int64_t ldx, int64_t strideX, int64_t batch
     p.vec_v = aligned(values, 16) && K * esz % 16 == 0;
     const dim3 grid((unsigned)blocks, 1, (unsigned)batch);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    describe("mxfp4_quantize %lld tiles", (long long)blocks);
+    describe("mxfp4_quantize", -2, "");
     if (dtype == SG_F32)
         hipLaunchKernelGGL(mx_quantize_kernel<DT_F32>, grid, dim3(256), 0, st, p);
     else if (dtype == SG_F16)
@@ -428,7 +441,7 @@ int sg_mxfp4_dequantize(const void* codes, const void* scales, int64_t batch, in
     p.vec_v = aligned(X, 16) && ldx * esz % 16 == 0 && p.sV % 16 == 0;
     const dim3 grid((unsigned)blocks, 1, (unsigned)batch);
     hipStream_t st = static_cast<hipStream_t>(stream);
-    describe("mxfp4_dequantize %lld tiles", (long long)blocks);
+    describe("mxfp4_dequantize", -2, "");
     if (dtype == SG_F32)
         hipLaunchKernelGGL(mx_dequantize_kernel<DT_F32>, grid, dim3(256), 0, st, p);
     else if (dtype == SG_F16)
@@ -451,7 +464,7 @@ int sg_mxfp4_tile_scales(const void* src, int64_t ld, int64_t stride, int64_t ba
     if (!any) return 0;
     const int64_t work = cdiv(cdiv(M, 32) * cdiv(blocks, 8) * (kMxTileBytes / 4), 256);
     const dim3 grid((unsigned)(work < 8192 ? work : 8192), 1, (unsigned)batch);
-    describe("mxfp4_tile_scales");
+    describe("mxfp4_tile_scales", -2, "");
     hipLaunchKernelGGL(mx_tile_scales_kernel, grid, dim3(256), 0,
                        static_cast<hipStream_t>(stream), static_cast<const uint8_t*>(src), ld,
                        stride, static_cast<uint8_t*>(dst), (int)M, (int)blocks);
