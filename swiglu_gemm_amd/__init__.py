@@ -776,13 +776,11 @@ def mxfp4_quantize(X, codes=None, scales=None, values=None):
     if codes is not None:
         _mx_bytes(codes, "codes", lead + (M, nb))
     elif values is None:
-        torch = _torch()[0]
-        codes = torch.empty(lead + (M, nb), dtype=torch.uint8, device=X.device)
+        codes = X.new_empty(lead + (M, nb), dtype=_torch()[0].uint8)
     if scales is not None:
         _mx_bytes(scales, "scales", lead + (ns,))
     elif values is None:
-        torch = _torch()[0]
-        scales = torch.empty(lead + (ns,), dtype=torch.uint8, device=X.device)
+        scales = X.new_empty(lead + (ns,), dtype=_torch()[0].uint8)
     if values is not None:
         if values.dtype != X.dtype:
             raise TypeError("values must have X's dtype")
@@ -810,11 +808,10 @@ def mxfp4_dequantize(codes, scales, X):
 def mxfp4_tile_scales(S):
     """Scales stored as rows of bytes, S [rows, blocks] or [batch, rows, blocks] uint8, in the
     tiles that mxfp4_gemm reads."""
-    torch = _torch()[0]
-    if S.dtype != torch.uint8:
+    if S.dtype is not _torch()[0].uint8:
         raise TypeError("scales must be uint8")
     lead, batch, M, nb, ld, stride = _mx_matrices(S, "scales")
-    out = torch.empty(lead + (mxfp4_shapes(M, 32 * nb)[1],), dtype=torch.uint8, device=S.device)
+    out = S.new_empty(lead + (mxfp4_shapes(M, 32 * nb)[1],))
     _launch("sg_mxfp4_tile_scales", lib().sg_mxfp4_tile_scales, (S, out), S.data_ptr(), ld, stride,
             batch, M, nb, out.data_ptr())
     return out

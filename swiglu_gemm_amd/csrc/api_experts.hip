@@ -91,15 +91,14 @@ bool group_cfg_ok(const GroupCfg& c, bool ta, bool tb, int esz, const GroupedPar
            ((tb ? c.BN : c.BK) * q.g.ldb + 256) * esz < kLim;
 }
 
-// Rounds of work-groups over the CUs, `occ` to a CU: whole ones while there are few, the mean
-// when there are many.  Where two share a CU, one that has it alone takes 0.62 of the time.
+// Rounds of work-groups over the CUs, `occ` to a CU: whole ones while there are few and one
+// work-group fills a CU, the mean when there are many or two share it (one that has a CU alone
+// takes 0.62 of the time).
 constexpr int kNumCU = 256;
 double rounds_of(double w, int occ) {
     if (w <= 1.0) return occ == 1 || w > 0.5 ? 1.0 : 0.62;
-    if (w >= 4.0) return w + (occ == 1 ? 0.4 : 0.25);
-    if (occ == 1) return std::ceil(w - 0.06);
-    const double rest = w - std::floor(w);
-    return std::floor(w) + (rest < 0.05 ? 0.0 : rest <= 0.5 ? 0.62 : 1.0);
+    if (occ == 2) return w + 0.45;
+    return w < 4.0 ? std::ceil(w - 0.06) : w + 0.4;
 }
 
 // Microseconds of `tiles` tiles of `flops` each that move `bytes` in all: never less than the

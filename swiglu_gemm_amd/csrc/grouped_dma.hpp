@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(
 // of a CU and the time a tile costs beside its products (_d: products that sum over rows; 0:
 // not for these).  They were fitted, near the rates of single tiles, to every tile forced on
 // 38 problems (1 to 64 experts, 1 to 16384 rows, K and N 724 to 5000) for each layout, SwiGLU
-// and the weight gradient; the model's choice is 1.2 % above the best tile in the mean for
-// 16-bit and 1.1 % for e4m3 rows, 2.0 % for weight gradients.
+// and the weight gradient; the model's choice is 1.6 % above the best tile in the mean for
+// 16-bit and 1.1 % for e4m3 rows, 2.5 % for weight gradients.
 //
 // What the tiles are for (MI355X, bf16, weights cold): 32 x 128, which streams a weight for a
 // few rows: 64 experts of 4 rows, 2048 x 1536: 72 us, 76-81 us on the wider ones; 32 x 64 where

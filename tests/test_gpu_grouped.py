@@ -440,3 +440,73 @@ def test_every_tile_depth(force, cfg, dtype, out):
                             (512, 512, (0, 0, 0), 0.0)):
         run_wgrad(dtype, out, LONG, N, K, beta=beta, pad=pad, before=3, behind=5)
         assert took(cfg)
+
+
+# ------------------------------------------------------------------ what lies behind K, far offsets
+@pytest.mark.parametrize("trans", "NT")
+@pytest.mark.parametrize("K", [8, 72, 200])
+def test_neighbours_behind_k_do_not_count(trans, K):
+    """A partial K tile may be loaded whole: the next row of A, the next row or the next
+    expert's weight come in with it.  NaN and infinities there leave no mark."""
+    import swiglu_gemm_amd as sg
+    off = table([64, 64, 64, 64])
+    A, B = rand((256, K), "bf16", 1.0, 1), rand((4, 160, K) if trans == "T" else (4, K, 160), "bf16",
+                                                0.1, 2)
+    bad = torch.arange(256) % 2 == 1
+    A[bad] = float("nan")
+    B[1] = float("inf")
+    B[3] = float("nan")
+    C = torch.zeros(256, 160, dtype=torch.bfloat16, device="cuda:0")
+    sg.grouped_gemm(A.cuda(), B.cuda(), C, off.cuda(), transB=trans)
+    assert "cfg=-1" not in sg.last_config()
+    got = C.cpu()
+    clean = [r for r in range(256) if not bad[r] and r // 64 in (0, 2)]
+    A[bad] = 0
+    B[1], B[3] = 0, 0
+    want, tol = ref.gemm_rows(A, B, off, trans, 1.0, None, None, 0.0, torch.bfloat16)
+    ref.check(got[clean], want[clean], tol[clean])
+
+
+def test_rows_past_32_bits():
+    """Rows whose offset in A passes 2^31 elements, and an expert's weight that does."""
+    import swiglu_gemm_amd as sg
+    K, N, far = 2048, 64, (1 << 20) + 3
+    off = table([far, 0, 70])
+    M = far + 70
+    A = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda:0")
+    assert A.numel() > 1 << 31
+    tail = rand((200, K), "bf16", 1.0, 1)
+    A[-200:] = tail.cuda()
+    stride = (1 << 30) + 64
+    store = torch.zeros(2 * stride + K * N, dtype=torch.bfloat16, device="cuda:0")
+    B = torch.as_strided(store, (3, K, N), (stride, N, 1))
+    w = rand((3, K, N), "bf16", 0.02, 2)
+    B.copy_(w.cuda())
+    C = torch.ones(M, N, dtype=torch.bfloat16, device="cuda:0")
+    sg.grouped_gemm(A, B, C, off.cuda())
+    near = table([130, 0, 70])
+    want, tol = ref.gemm_rows(tail, w, near, "N", 1.0, None, None, 0.0, torch.bfloat16)
+    ref.check(C[-200:], want, tol)
+    assert torch.count_nonzero(C[:-200]) == 0
+    # the weight gradient sums the far rows
+    G = torch.empty(3, K, N, device="cuda:0")
+    D = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda:0")
+    d = rand((200, N), "bf16", 1.0, 3)
+    D[-200:] = d.cuda()
+    sg.grouped_gemm_wgrad(A, D, G, off.cuda())
+    want, tol = ref.wgrad(tail, d, near, 1.0, None, 0.0, torch.float32)
+    ref.check(G, want, tol)
+
+
+def test_offsets_that_do_not_ascend_stay_inside():
+    """A bad table: unspecified rows, but only rows of C and whole calls (the offsets are cut to
+    [0, M])."""
+    import swiglu_gemm_amd as sg
+    A, B = rand((100, 64), "bf16", 1.0, 1).cuda(), rand((3, 64, 48), "bf16", 0.1, 2).cuda()
+    whole = torch.full((300, 48), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    for bad in ([0, 90, 20, 100], [-50, 40, 1 << 30, 100], [100, 50, 0, 0], [-(1 << 31), 5, -3, 99]):
+        o = torch.tensor(bad, dtype=torch.int32, device="cuda:0")
+        sg.grouped_gemm(A, B, whole[100:200], o)
+        sg.grouped_gemm_wgrad(A, A[:, :48].contiguous(), torch.empty(3, 64, 48, device="cuda:0"), o)
+        torch.cuda.synchronize()
+        assert (whole[:100] == 7).all() and (whole[200:] == 7).all()

@@ -276,3 +276,58 @@ def test_every_tile(monkeypatch, cfg):
     run_product(300, 324, 1312, "f16", spread=0, pad=4)
     run_product(sizes, 164, 416, swiglu=True, spread=0, before=3, behind=5)
     run_product(260, 256, 1024, "f16", swiglu=True, spread=0)
+
+
+def test_graph_and_two_streams():
+    """Quantisation and product captured together follow new inputs and offsets; two streams at
+    once give the bits of one after the other."""
+    import swiglu_gemm_amd as sg
+    offs = [table([100, 0, 156]).cuda(), table([1, 255, 0]).cuda()]
+    g = torch.Generator().manual_seed(9)
+    Xs = [torch.randn(256, 320, generator=g).bfloat16().cuda() for _ in range(2)]
+    W = sg.mxfp4_quantize((torch.randn(3, 512, 320, generator=g) * 0.05).bfloat16().cuda())
+    new = lambda: torch.zeros(256, 256, dtype=torch.bfloat16, device="cuda:0")
+    run = lambda x, o, y: sg.mxfp4_swiglu_gemm(*sg.mxfp4_quantize(x), *W, y, offsets=o)
+    alone = [run(x, o, new()) for x, o in zip(Xs, offs)]
+    both, streams = [new(), new()], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(8):
+        for s, x, o, y in zip(streams, Xs, offs, both):
+            with torch.cuda.stream(s):
+                run(x, o, y)
+    torch.cuda.synchronize()
+    assert torch.equal(both[0], alone[0]) and torch.equal(both[1], alone[1])
+    X, off, Y = Xs[0].clone(), offs[0].clone(), new()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(X, off, Y)
+    for i in (0, 1, 0, 1):
+        X.copy_(Xs[i])
+        off.copy_(offs[i])
+        Y.zero_()
+        assert torch.equal(run(Xs[i], offs[i], new()), alone[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(Y, alone[i])
+
+
+def test_quantize_past_32_bits():
+    import swiglu_gemm_amd as sg
+    R, K = (1 << 20) + 40, 2080
+    X = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda:0")
+    assert X.numel() > 1 << 31
+    tail = torch.randn(72, K, generator=torch.Generator().manual_seed(1)).bfloat16()
+    X[-72:] = tail.cuda()
+    codes, scales = sg.mxfp4_quantize(X)
+    wc, ws, wv = ref.quantize(tail)
+    assert torch.equal(codes[-72:].cpu(), wc)
+    nb = ws.shape[1]
+    rows = scales.view(-1, (nb + 7) // 8 * 256)[-3:].flatten().cpu()     # the last 96 rows' tiles
+    first = (R - 72) % 32                                  # the tail's first row in them
+    assert torch.equal(ref.untile_scales(rows, first + 72, nb)[first:], ws)
+    assert torch.count_nonzero(codes[:-72]) == 0
+    B, Bs, b = random_mx(1, 64, K, 2, 1)
+    C = torch.empty(R, 64, device="cuda:0")
+    sg.mxfp4_gemm(codes, scales, B[0].cuda(), Bs[0].cuda(), C)
+    s, err = ref.matmul(wv, b[0].t())
+    ref.check(C[-72:], s, err + ref.half_step(s, torch.float32))
