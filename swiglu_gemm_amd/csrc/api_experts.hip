@@ -26,6 +26,8 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
 constexpr int64_t kMaxExperts = (int64_t)1 << 16;
+// tile-rows of an expert walked together (2, 8 and 16 measured the same)
+constexpr int kGroupM = 4;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 23;   // work-groups of one launch
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p % bytes) == 0; }
@@ -111,14 +113,15 @@ double est_us(double tiles, int occ, double flops, double rate, double fixed, do
 }
 
 // The rows of each expert are not known here, so their mean stands for them: a run of n rows is
-// taken for n/BM + 1/2 tiles, never less than one (half of one costs 0.6).
+// taken for n/BM + 1/2 tiles, never less than one; less where the tile has a low form (0.6 of
+// the time of a whole one).
 double est_rows(const GroupCfg& c, bool tb, int esz, const GroupedParams& q) {
     const double runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
-    const bool half = group_half(false, c.BM, c.BN, c.WM, c.WN);
-    double per = std::fmax(half && mean <= c.BM / 2 ? 0.6 : 1.0, mean / c.BM + (half ? 0.35 : 0.5));
+    const int low = group_low(false, c.BM, c.BN, c.WM, c.WN);
+    double per = std::fmax(mean <= low ? 0.6 : 1.0, mean / c.BM + (low ? 0.35 : 0.5));
     if (q.experts == 1) {
         const int rest = q.rows % c.BM;
-        per = q.rows / c.BM + (rest == 0 ? 0.0 : half && rest <= c.BM / 2 ? 0.6 : 1.0);
+        per = q.rows / c.BM + (rest == 0 ? 0.0 : rest <= low ? 0.6 : 1.0);
     }
     const double bytes = (double)q.rows * q.g.K * esz + runs * q.g.K * (double)q.g.N * esz +
                          (double)q.rows * q.g.N * 2.0;
@@ -163,7 +166,7 @@ int run_rows(const char* what, int epi, bool tb, int dtype, GroupedParams q, hip
     const int esz = dtype == SG_F8E4M3 ? 1 : 2;
     const int cfg = q.g.K > 0 ? choose_group(false, tb, esz, q) : -1;
     const int bm = cfg < 0 ? 64 : kGroupCfg[cfg].BM, bn = cfg < 0 ? 64 : kGroupCfg[cfg].BN;
-    q.g.group_m = 4;
+    q.g.group_m = kGroupM;
     q.g.tiles_n = (int)cdiv(q.g.N, bn);
     q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0;
     describe(what, cfg, cfg < 0 ? "any 64x64x32" : kGroupCfg[cfg].name);
@@ -176,7 +179,7 @@ int run_rows(const char* what, int epi, bool tb, int dtype, GroupedParams q, hip
 int run_depth(const char* what, int epi, int dtype, GroupedParams q, hipStream_t st) {
     const int cfg = q.rows > 0 ? choose_group(true, false, 2, q) : -1;
     const int bm = cfg < 0 ? 64 : kGroupCfg[cfg].BM, bn = cfg < 0 ? 64 : kGroupCfg[cfg].BN;
-    q.g.group_m = 4;
+    q.g.group_m = kGroupM;
     q.g.tiles_m = (int)cdiv(q.g.M, bm);
     q.g.tiles_n = (int)cdiv(q.g.N, bn);
     q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0 && q.sC % 8 == 0;
@@ -203,7 +206,7 @@ int run_mx4(const char* what, int epi, int dtype, MxParams x, hipStream_t st) {
     if (256 * q.g.lda + 256 >= (int64_t)1 << 31) return status_of(hipErrorInvalidConfiguration);
     const int cfg = choose_mx4(q);
     const MxCfg& c = kMxCfg[cfg];
-    q.g.group_m = 4;
+    q.g.group_m = kGroupM;
     q.g.tiles_n = (int)cdiv(q.g.N, c.BN);
     q.g.vec_c = aligned(q.g.C, 8) && q.g.ldc % 4 == 0;
     const int64_t tiles_m = q.offsets ? most_row_tiles(q.rows, q.experts, c.BM) : cdiv(q.rows, c.BM);
