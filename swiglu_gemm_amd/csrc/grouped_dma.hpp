@@ -261,6 +261,10 @@ constexpr GroupCfg kGroupCfg[] = {
     {1, 192, 128, 128, 2, 2, 4, 8.28, 3.16, 0.0, 0.0, "e4m3 192x128x128 s2 2x4w"},
 };
 constexpr int kNumGroupCfg = sizeof(kGroupCfg) / sizeof(kGroupCfg[0]);
+constexpr int kFewRows = 1, kTwoPerCu = 4;       // 16-bit: 32 x 128; 128 x 256, 32 deep
+static_assert(kGroupCfg[kFewRows].BM == 32 && kGroupCfg[kFewRows].BN == 128 &&
+                  kGroupCfg[kTwoPerCu].BN == 256 && kGroupCfg[kTwoPerCu].BK == 32,
+              "the tiles the choice names");
 
 #define SG_GROUPED_16(X)          \
     X(0, 32, 64, 64, 6, 1, 2)     \
