@@ -277,7 +277,8 @@ int sg_silu_mul(const void* G, const void* U, void* Y, int64_t M, int64_t N,
  * Alignment: any element-aligned pointers and leading dimensions are accepted; 16-byte
  * aligned operands with rows and strides of 16-byte multiples run on the direct-to-LDS
  * tile kernels, others on a 64 x 64 tile kernel that loads element by element.
- * A problem of more than 2^23 output tiles returns hipErrorInvalidConfiguration.
+ * A problem of more than about 2^22 output tiles, or a 4-bit one whose 256 rows of codes
+ * exceed 2^31 bytes, returns hipErrorInvalidConfiguration.
  */
 
 /*
@@ -312,7 +313,7 @@ int sg_grouped_gemm(char transB, int64_t experts, const int32_t* offsets, int64_
  *  15 dtype  of A and D: SG_F16 or SG_BF16.   16 c_dtype   dtype or SG_F32.
  *  17 stream.
  * Quick returns: N == 0 or K == 0 does nothing; M == 0 or alpha == 0 computes
- * C_e = beta * C_e.
+ * C_e = beta * C_e (alpha does not count where there are no products).
  */
 int sg_grouped_gemm_wgrad(int64_t experts, const int32_t* offsets, int64_t M, int64_t N,
                           int64_t K, float alpha, const void* A, int64_t lda, const void* D,
@@ -378,8 +379,8 @@ int sg_grouped_swiglu_gemm_bwd(int64_t experts, const int32_t* offsets, const vo
  *  4 batch (0..65535), 5 M, 6 K   >= 0.   7 dtype   of X: SG_F32, SG_F16 or SG_BF16.
  *  8 codes, 9 scales   outputs, 4-byte aligned, or NULL.
  *  10 values   NULL, or the values the codes and scales stand for, batch x M x K
- *            contiguous, rounded to X's type (exact but for fp16 values below 2^-24 or
- *            above 65504).
+ *            contiguous, rounded to X's type (exact but for multiples of scales below
+ *            2^-23 in fp16).
  *  11 stream.
  * Invalid: as above; codes, scales and values all NULL (-8).
  */

@@ -5,13 +5,13 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <cstdlib>
-#include <cstddef>
 
+#include "configs16.hpp"
 #include "grouped.hpp"
 #include "grouped_dma.hpp"
-#include "configs16.hpp"
 #include "mx4.hpp"
 #include "mx4_dma.hpp"
 #include "swiglu_gemm.h"
@@ -28,7 +28,7 @@ constexpr int64_t kMaxDim = (int64_t)1 << 30;
 constexpr int64_t kMaxExperts = (int64_t)1 << 16;
 // tile-rows of an expert walked together (2, 8 and 16 measured the same)
 constexpr int kGroupM = 4;
-constexpr int64_t kMaxBlocks = (int64_t)1 << 23;   // work-groups of one launch
+constexpr int64_t kMaxBlocks = (int64_t)1 << 22;   // work-groups of one launch
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p % bytes) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -264,11 +264,11 @@ int sg_grouped_gemm(char transB, int64_t experts, const int32_t* offsets, int64_
     q.g.ldb = ldb;
     q.g.ldc = ldc;
     q.g.N = (int)N;
-    q.g.K = alpha == 0.0f ? 0 : (int)K;
-    q.g.alpha = alpha;
+    q.g.K = reads ? (int)K : 0;
+    q.g.alpha = reads ? alpha : 0.0f;    // no products: no factor of theirs, infinite or not
     q.g.beta = beta;
     q.offsets = offsets;
-    q.scale = scale;
+    q.scale = reads ? scale : nullptr;
     q.experts = (int)experts;
     q.rows = (int)M;
     q.sB = strideB * esz;
@@ -343,7 +343,7 @@ int sg_grouped_swiglu_gemm(int64_t experts, const int32_t* offsets, const void* 
     q.g.alpha = alpha;
     q.g.epi_flags = aligned(Y, 16) && N % 8 == 0 ? EPI_Y16 : 0;
     q.offsets = offsets;
-    q.scale = scale;
+    q.scale = reads ? scale : nullptr;
     q.experts = (int)experts;
     q.rows = (int)M;
     q.sB = K * 2 * N * (dtype == SG_F8E4M3 ? 1 : 2);
@@ -510,7 +510,7 @@ int sg_mxfp4_gemm(int64_t experts, const int32_t* offsets, int64_t M, int64_t N,
     x.q.g.ldc = ldc;
     x.q.g.N = (int)N;
     x.q.g.K = reads ? (int)mx_blocks(K) : 0;
-    x.q.g.alpha = alpha;
+    x.q.g.alpha = reads ? alpha : 0.0f;
     x.q.offsets = offsets;
     x.q.experts = (int)experts;
     x.q.rows = (int)M;

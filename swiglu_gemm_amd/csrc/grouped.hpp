@@ -53,8 +53,8 @@ struct GroupItem {
 // The item of work-group `bid` among `total`: consecutive items share an XCD (as xcd_remap).
 // OCC > 0 (the work-groups of a CU, for kernels that have a tile of half the rows): where the
 // items of an XCD leave its last round at most half full, that round's items are split into
-// two halves each, which finish it in 0.6 of the time (32 uneven experts, 16384 rows, see
-// kGroupCfg).  The launch has room for them: group_blocks().
+// two halves each, which finish it in 0.6 of the time (4-bit, 8 experts of 1024 rows, 4096 x
+// 4096: 109 -> 98 us).  The launch has room for them: group_blocks().
 constexpr int kXcds = 8, kXcdCus = 32;
 template <int OCC>
 __device__ __forceinline__ bool xcd_item(int bid, int total, int& lid, int& part) {
@@ -118,7 +118,7 @@ __device__ __forceinline__ bool find_rows(const GroupedParams& q, int bid, int l
         return it.m0 < it.rows;
     }
     const int per = (q.experts + 63) / 64;
-    int mine = 0, row = 0, len = 0;                // row, len: the lane's last expert
+    int mine = 0, row = 0, len = 0;                // row, len: the lane's expert where per is 1
     for (int j = 0; j < per; ++j) {
         const int e = lane * per + j;
         if (e >= q.experts) break;
@@ -194,8 +194,8 @@ __device__ __forceinline__ bool find_depth(const GroupedParams& q, int bid, int 
 }
 
 // The expert's own problem: operands, output and sizes from the item.  ESZ: bytes of an
-// operand element; CSZ: of an output element.  row_of_c: the first row of the expert in C
-// counts in rows of C (rows); C_e follows C by sC bytes (depth).
+// operand element; CSZ: of an output element.  Depth: an expert without rows has no products,
+// and alpha, which may be infinite, does not count.
 template <bool TA, int ESZ, int CSZ>
 __device__ __forceinline__ Gemm16Params group_problem(const GroupedParams& q,
                                                       const GroupItem& it) {
@@ -207,6 +207,7 @@ __device__ __forceinline__ Gemm16Params group_problem(const GroupedParams& q,
         p.B = reinterpret_cast<const uint16_t*>(B + (int64_t)it.row0 * p.ldb * ESZ);
         p.C = reinterpret_cast<char*>(q.g.C) + it.e * q.sC;
         p.K = it.rows;
+        if (it.rows == 0) p.alpha = 0.0f;
     } else {
         p.B = reinterpret_cast<const uint16_t*>(B + it.e * q.sB);
         p.C = reinterpret_cast<char*>(q.g.C) + (int64_t)it.row0 * p.ldc * CSZ;

@@ -510,3 +510,35 @@ def test_offsets_that_do_not_ascend_stay_inside():
         sg.grouped_gemm_wgrad(A, A[:, :48].contiguous(), torch.empty(3, 64, 48, device="cuda:0"), o)
         torch.cuda.synchronize()
         assert (whole[:100] == 7).all() and (whole[200:] == 7).all()
+
+
+def test_factors_of_no_products_do_not_count():
+    """alpha = 0 or K = 0 with infinite or NaN scales, and infinite alpha for an expert without
+    rows: beta * C_old all the same."""
+    import swiglu_gemm_amd as sg
+    off = table([3, 0, 2]).cuda()
+    inf = float("inf")
+    C = torch.full((5, 24), 2.0, dtype=torch.bfloat16, device="cuda:0")
+    scale = torch.tensor([inf, float("nan"), -inf], device="cuda:0")
+    A, B = rand((5, 32), "bf16", 1.0, 1).cuda(), rand((3, 32, 24), "bf16", 1.0, 2).cuda()
+    sg.grouped_gemm(A, B, C, off, alpha=0.0, beta=0.5, scale=scale)
+    assert (C == 1).all()
+    sg.grouped_gemm(A[:, :0].contiguous(), B[:, :0].contiguous(), C, off, alpha=inf, beta=0.5,
+                    scale=scale)
+    assert (C == 0.5).all()
+    G = torch.full((3, 32, 24), 2.0, device="cuda:0")
+    sg.grouped_gemm_wgrad(A, rand((5, 24), "bf16", 1.0, 3).cuda(), G, off, alpha=inf, beta=0.5)
+    assert (G[1] == 1).all()
+
+
+def test_a_bad_table_of_many_experts_stays_inside():
+    import swiglu_gemm_amd as sg
+    g = torch.Generator().manual_seed(3)
+    A, B = rand((100, 64), "bf16", 1.0, 1).cuda(), rand((100, 64, 48), "bf16", 0.1, 2).cuda()
+    whole = torch.full((300, 48), 7.0, dtype=torch.bfloat16, device="cuda:0")
+    for _ in range(4):
+        o = torch.randint(-(1 << 31), (1 << 31) - 1, (101,), generator=g).int().cuda()
+        sg.grouped_gemm(A, B, whole[100:200], o)
+        sg.grouped_gemm_wgrad(A, A[:, :48].contiguous(), torch.empty(100, 64, 48, device="cuda:0"), o)
+        torch.cuda.synchronize()
+        assert (whole[:100] == 7).all() and (whole[200:] == 7).all()

@@ -331,3 +331,20 @@ def test_quantize_past_32_bits():
     sg.mxfp4_gemm(codes, scales, B[0].cuda(), Bs[0].cuda(), C)
     s, err = ref.matmul(wv, b[0].t())
     ref.check(C[-72:], s, err + ref.half_step(s, torch.float32))
+
+
+def test_far_scales_meet():
+    """The smallest scales of one matrix against the largest of the other: the exponents add
+    before anything is rounded away.  2^-127 * 2^127, codes up to 6: sums of at most 36 K."""
+    import swiglu_gemm_amd as sg
+    K = 320
+    A, _, _ = random_mx(1, 40, K, 1)
+    B, _, _ = random_mx(1, 72, K, 2)
+    low = torch.arange(40 * 10).view(40, 10) % 3
+    sa, sb = low.to(torch.uint8), (254 - torch.arange(72 * 10).view(72, 10) % 3).to(torch.uint8)
+    for x, sx, y, sy in ((A, sa, B, sb), (A, 254 - sa, B, 254 - sb)):
+        a, b = ref.values(x[0], sx), ref.values(y[0], sy)
+        C = torch.empty(40, 72, device="cuda:0")
+        sg.mxfp4_gemm(x[0].cuda(), ref.tile_scales(sx).cuda(), y[0].cuda(), ref.tile_scales(sy).cuda(), C)
+        s, err = ref.matmul(a, b.t())
+        ref.check(C, s, err + ref.half_step(s, torch.float32))
