@@ -647,8 +647,8 @@ def grouped_gemm(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, transB
     op = _experts(offsets, E)
     sp = _scale(scale, E)
     _launch("sg_grouped_gemm", lib().sg_grouped_gemm, (C, A, B, offsets, scale), transB.encode(), E,
-            op, M, N, K, float(alpha), sp, A.data_ptr(), lda, B.data_ptr(), ldb, sB, float(beta), C.data_ptr(),
-            ldc, code)
+            op, M, N, K, float(alpha), sp, A.data_ptr(), lda, B.data_ptr(), ldb, sB, float(beta),
+            C.data_ptr(), ldc, code)
     return C
 
 
@@ -674,9 +674,9 @@ def grouped_gemm_wgrad(A, D, C, offsets, alpha: float = 1.0, beta: float = 0.0):
         raise ValueError("C has shape %s, expected (experts, %d, %d)" % (tuple(csh), K, N))
     op = _experts(offsets, E)
     lda, ldd = _rows(A, "A", K), _rows(D, "D", N)
-    _launch("sg_grouped_gemm_wgrad", lib().sg_grouped_gemm_wgrad, (C, A, D, offsets), E, op, M, N, K,
-            float(alpha), A.data_ptr(), lda, D.data_ptr(), ldd, float(beta), C.data_ptr(), ldc, sC, code,
-            _dtype_code(C))
+    _launch("sg_grouped_gemm_wgrad", lib().sg_grouped_gemm_wgrad, (C, A, D, offsets), E, op, M, N,
+            K, float(alpha), A.data_ptr(), lda, D.data_ptr(), ldd, float(beta), C.data_ptr(), ldc,
+            sC, code, _dtype_code(C))
     return C
 
 
@@ -857,7 +857,8 @@ def mxfp4_gemm(A, As, B, Bs, C, offsets=None, alpha: float = 1.0):
     E, op, M, K = _mx_product(A, As, B, Bs, offsets, C, N)
     ldc = _rows(C, "C", N)
     _launch("sg_mxfp4_gemm", lib().sg_mxfp4_gemm, (C, A, As, B, Bs, offsets), E, op, M, N, K,
-            float(alpha), A.data_ptr(), As.data_ptr(), B.data_ptr(), Bs.data_ptr(), C.data_ptr(), ldc, code)
+            float(alpha), A.data_ptr(), As.data_ptr(), B.data_ptr(), Bs.data_ptr(), C.data_ptr(),
+            ldc, code)
     return C
 
 
@@ -873,6 +874,6 @@ def mxfp4_swiglu_gemm(A, As, W, Ws, Y, offsets=None):
     N = Y.shape[1]
     E, op, M, K = _mx_product(A, As, W, Ws, offsets, Y, 2 * N)
     _contig(Y, "Y", (M, N))
-    _launch("sg_mxfp4_swiglu_gemm", lib().sg_mxfp4_swiglu_gemm, (Y, A, As, W, Ws, offsets), E, op, M,
-            N, K, A.data_ptr(), As.data_ptr(), W.data_ptr(), Ws.data_ptr(), Y.data_ptr(), code)
+    _launch("sg_mxfp4_swiglu_gemm", lib().sg_mxfp4_swiglu_gemm, (Y, A, As, W, Ws, offsets), E, op,
+            M, N, K, A.data_ptr(), As.data_ptr(), W.data_ptr(), Ws.data_ptr(), Y.data_ptr(), code)
     return Y

@@ -11,6 +11,11 @@
 // A row may end inside a K tile: the ring loads the row's last chunk again for the chunks
 // past its end, and the tile is finished apart from the loop with those chunks of A as zero
 // codes and both scales 1, so neither stray codes nor padding of the scales count.
+//
+// Large products are bound by the matrix cores and power: 8192^3 258 us, 4.3 PFLOP/s.  A tile
+// of K = 2048 is 8 K tiles, so its fill and epilogue show: 16384 rows of 32 uneven experts,
+// 2048 x 2 x 1408 with SwiGLU, 81 us, 2.3 PFLOP/s.  Few rows are bound by reading the weights
+// and by latency: 8 rows, 4096 x 11008 (24 MB), 8.8 us.
 #pragma once
 
 #include "gemm16_dma.hpp"
