@@ -293,8 +293,7 @@ __global__ void __launch_bounds__(64 * NW) decode_kernel(const DecodeParams p) {
             }
             if (ahead) wait_vmcnt<(S - 2) * NL>();
             else wait_vmcnt<0>();
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
+            stage_barrier();
             // the next unit's first fragments (stale and unused after the last unit)
             read_all(smem + ((i + 1) % S) * STAGE, 0, fa[0], fb[0]);
             mfma_all(fa[1], fb[1]);

@@ -87,6 +87,16 @@ __device__ __forceinline__ void wait_vmcnt() {
     __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
 }
 
+// The barrier at the end of a tile of the ring, behind the wait for the wave's own loads of
+// the next tile.  Any wave may then issue loads into the stage that the tile was read from,
+// and s_barrier does not wait for LDS reads: the wave's last reads of that stage must be done
+// first (without the wait only the loads' latency would keep them apart).
+__device__ __forceinline__ void stage_barrier() {
+    __builtin_amdgcn_s_waitcnt(15 | (7 << 4) | (0 << 8) | (3 << 14));      // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // One operand's DMA stream: NI instructions per thread per K tile.  Each lane's
 // chunk is a fixed 32-bit byte offset from a wave-uniform tile base held in SGPRs
 // (the global_load_lds "saddr" form), so advancing a K tile costs one scalar add
@@ -128,7 +138,7 @@ struct DmaStream {
     // Issue the DMA of K tile `t` (relative to the split start) into stage memory.
     // Written as inline asm so the compiler does not model the asynchronous LDS
     // write (it would otherwise drain every outstanding load before each LDS
-    // read); completion is enforced by wait_vmcnt + s_barrier in the main loop.
+    // read); completion is enforced by wait_vmcnt + stage_barrier in the main loop.
     // The LDS-DMA reads M0 as its LDS address; a scalar write of M0 needs one wait
     // state before that read on this GPU family (the s_nop the compiler's hazard
     // recognizer would insert, which it cannot do inside an asm statement).
@@ -448,11 +458,10 @@ __device__ __forceinline__ void dma_mainloop(
                     __builtin_amdgcn_sched_barrier(0);
                 }
             }
-            // tile t+1 must have landed (own DMAs), then everyone's
+            // tile t+1 must have landed (own DMAs), then everyone's; tile t's reads are done
             if (ahead) wait_vmcnt<(S - 2) * NL>();
             else wait_vmcnt<0>();
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
+            stage_barrier();
             // last k-step of tile t overlaps the first fragments of tile t+1 (on
             // the last tile this reads a stale stage whose values are never used)
             read_all(sn, 0, fa[0], fb[0]);
@@ -616,8 +625,7 @@ __device__ __forceinline__ void dma_mainloop_seq(
             }
             if (ahead) wait_vmcnt<(S - 2) * NL>();
             else wait_vmcnt<0>();
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
+            stage_barrier();
             // the next tile's first fragments (on the last tile: a stale stage, unused)
             read_all(smem + ((t + 1) % S) * STAGE, 0, fa[0], fb[0]);
             mfma_all(fa[1], fb[1]);
@@ -751,8 +759,7 @@ __device__ __forceinline__ void ws_mainloop_seq(
                 sched_interleave<NMF, NRD, 0, 0>();
                 __builtin_amdgcn_sched_barrier(0);
             }
-            __builtin_amdgcn_s_barrier();
-            __builtin_amdgcn_sched_barrier(0);
+            stage_barrier();
             // the next tile's first fragments (on the last tile: a stale stage, unused)
             read_all(smem + ((t + 1) % S) * STAGE, 0, fa[0], fb[0]);
             mfma_all(fa[1], fb[1]);

@@ -181,8 +181,7 @@ __device__ __forceinline__ void mx_mainloop(const MxParams& x, const GroupItem& 
         });
         if (ahead) wait_vmcnt<(S - 2) * NL>();
         else wait_vmcnt<0>();
-        __builtin_amdgcn_s_barrier();
-        __builtin_amdgcn_sched_barrier(0);
+        stage_barrier();
         // the next tile's scales and first codes under this tile's last MFMAs (after the
         // last tile: a stale stage, unused)
         read_scales(nxt, na, nb);
