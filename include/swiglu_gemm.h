@@ -268,10 +268,12 @@ int sg_silu_mul(const void* G, const void* U, void* Y, int64_t M, int64_t N,
  * The M rows of A are sorted by expert: expert e owns rows offsets[e] .. offsets[e+1]-1,
  * R_e for short.  `offsets` is DEVICE memory, experts + 1 ascending int32 row numbers in
  * [0, M] (experts 1..65536); an expert may own no row.  Rows before offsets[0] and from
- * offsets[experts] on belong to no expert: they are neither read nor written.  The host
- * never reads the offsets, so a call can be captured into a HIP graph and replayed with
- * other offsets.  The kernels clamp each offset to [0, M]; a table that does not ascend
- * gives unspecified rows of the output (nothing outside it is written).
+ * offsets[experts] on belong to no expert: they are neither read nor written, nor are gaps
+ * between the experts' matrices.  What lies between the end of one row and the next, and
+ * the rest of the 16-byte piece that holds a row's last element, may be loaded; it never
+ * counts.  The host never reads the offsets, so a call can be captured into a HIP graph
+ * and replayed with other offsets.  The kernels clamp each offset to [0, M]; a table that
+ * does not ascend gives unspecified rows of the output (nothing outside it is written).
  * These calls allocate nothing and use no workspace: calls on different streams may
  * overlap.  Results are run-to-run identical.
  * Alignment: any element-aligned pointers and leading dimensions are accepted; 16-byte

@@ -138,21 +138,25 @@ __device__ __forceinline__ void epilogue_swiglu_bwd_lds(const Gemm16Params& p, c
     }
 }
 
-// Whether the partial K tile at the end of a tile's loop may be read whole: every row of
-// op(A) and op(B) it touches, to the end of the K tile, lies in front of the operands' ends
-// (the bytes past K are the next row's, the next expert's, or padding).
+// Whether the partial K tile at the end of a tile's loop may be read whole: everything it would
+// load behind K, rows clamped to the tile's own, lies in front of the end of the experts' rows and
+// inside their matrices.  Rows of no expert and gaps between the matrices are not read; what lies
+// between one row's end and the next row may be, and the fragments are cut so that none of it
+// counts.
 template <bool TA, bool TB, int BM, int BN, int BK, int ESZ>
-__device__ __forceinline__ bool tail_readable(const GroupedParams& q, const GroupItem& it,
+__host__ __device__ inline bool tail_readable(const GroupedParams& q, const GroupItem& it,
                                               const Gemm16Params& p, int m0, int n0, int nkt) {
+    const int past = (nkt + 1) * BK;                     // the whole tile's last k, plus 1
     if constexpr (TA) {
         // k are rows of A and D; past the expert's rows come the next expert's
-        return it.row0 + (nkt + 1) * BK <= q.rows;
+        return it.row0 + past <= it.end;
     } else {
         // A: k run along a row, so past K comes the next row, if there is one
-        const bool a_in = it.row0 + min(m0 + BM, p.M) < q.rows && (nkt + 1) * BK <= q.g.lda + p.K;
-        const bool more = it.e + 1 < q.experts && q.sB >= (int64_t)(TB ? p.N : p.K) * p.ldb * ESZ;
-        const bool b_in = TB ? (more || min(n0 + BN, p.N) < p.N) && (nkt + 1) * BK <= p.ldb + p.K
-                             : more && (nkt + 1) * BK - p.K <= p.K;
+        const int rows = m0 + BM < p.M ? m0 + BM : p.M;
+        const bool a_in = it.row0 + rows < it.end && past <= q.g.lda + p.K;
+        const bool more = it.e + 1 < q.experts && q.sB == (int64_t)(TB ? p.N : p.K) * p.ldb * ESZ;
+        const bool b_in = TB ? (more || n0 + BN < p.N) && past <= p.ldb + p.K
+                             : more && past - p.K <= p.K;
         return a_in && b_in;
     }
 }
