@@ -564,6 +564,15 @@ def _launch(what: str, fn, tensors, *args) -> None:
         _check(status, what)
 
 
+def _no_bytes(A, B, other: str) -> None:
+    """uint8 tensors hold the codes of 4-bit matrices: taken for e4m3 here, they would give
+    something else without an error."""
+    u8 = _torch()[0].uint8
+    if A.dtype is u8 or B.dtype is u8:
+        raise TypeError("e4m3 operands must be torch.float8_e4m3fn (view uint8 codes as that); "
+                        "4-bit codes go to %s" % other)
+
+
 def _experts(offsets, experts: int) -> int:
     if offsets.dtype is not _torch()[0].int32:
         raise TypeError("offsets must be int32, not %s" % offsets.dtype)
@@ -618,12 +627,15 @@ def grouped_gemm(A, B, C, offsets, alpha: float = 1.0, beta: float = 0.0, transB
                  scale=None):
     """C[r] = alpha * scale[e] * A[r] @ op(B[e]) + beta * C[r] for the rows offsets[e] <= r <
     offsets[e + 1] of each expert, in place on C; other rows stay as they are.  A [M, K];
-    B [experts, K, N], or [experts, N, K] with transB='T'; C [M, N] of A's dtype (bf16 for
-    e4m3 operands); scale: None or float32 [experts]."""
+    B [experts, K, N], or [experts, N, K] with transB='T', both bf16, fp16 or float8_e4m3fn
+    (uint8 is refused: it holds 4-bit codes); C [M, N] of A's dtype (bf16 for e4m3 operands);
+    scale: None or float32 [experts]."""
     codes, outs = _tables()[:2]
     code = _dtype_code(A)
     if code == SG_F32:
         raise TypeError("grouped products take bf16, fp16 or e4m3 operands")
+    if code == SG_F8E4M3:
+        _no_bytes(A, B, "mxfp4_gemm")
     if transB not in ("N", "T", "n", "t"):
         raise ValueError("transB must be 'N' or 'T'")
     ash = A.shape
@@ -684,6 +696,8 @@ def _grouped_swiglu(A, Wfused):
     code = _dtype_code(A)
     if code == SG_F32:
         raise TypeError("SwiGLU takes bf16, fp16 or e4m3 operands")
+    if code == SG_F8E4M3:
+        _no_bytes(A, Wfused, "mxfp4_swiglu_gemm")
     if _tables()[0].get(Wfused.dtype) != code:
         raise TypeError("Wfused must have A's dtype")
     ash, wsh = A.shape, Wfused.shape
@@ -702,7 +716,8 @@ def _grouped_swiglu(A, Wfused):
 def grouped_swiglu_gemm(A, Wfused, Y, offsets, alpha: float = 1.0, scale=None):
     """Y[r] = SiLU(s*A[r]@W1[e]) * (s*A[r]@W2[e]) for the rows of each expert, s = alpha *
     scale[e], from the column-interleaved Wfused [experts, K, 2N] (interleave_gate_up on
-    each); A [M, K], Y [M, N], all contiguous.  alpha and scale: e4m3 operands only."""
+    each); A [M, K], Y [M, N], all contiguous.  Operands as grouped_gemm; alpha and scale: e4m3
+    operands only."""
     code, E, M, N, K = _grouped_swiglu(A, Wfused)
     if Y.dtype not in _out_dtypes(code):
         raise TypeError("Y has dtype %s, expected %s" % (Y.dtype, _out_dtypes(code)[0]))
