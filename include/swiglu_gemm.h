@@ -280,7 +280,8 @@ int sg_silu_mul(const void* G, const void* U, void* Y, int64_t M, int64_t N,
  * aligned operands with rows and strides of 16-byte multiples run on the direct-to-LDS
  * tile kernels, others on a 64 x 64 tile kernel that loads element by element.
  * A problem of more than about 2^22 output tiles, or a 4-bit one whose 256 rows of codes
- * exceed 2^31 bytes, returns hipErrorInvalidConfiguration.
+ * exceed 2^31 bytes, returns hipErrorInvalidConfiguration.  Matrices more than 2^44
+ * elements apart are an invalid stride; the stride of a single matrix does not count.
  */
 
 /*

@@ -29,10 +29,17 @@ constexpr int64_t kMaxExperts = (int64_t)1 << 16;
 // tile-rows of an expert walked together (2, 8 and 16 measured the same)
 constexpr int kGroupM = 4;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 22;   // work-groups of one launch
+// elements from one matrix to the next: with 65536 of them no offset in bytes passes 64 bits
+constexpr int64_t kMaxStride = (int64_t)1 << 44;
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p % bytes) == 0; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int status_of(hipError_t e) { return e == hipSuccess ? 0 : (int)e; }
+// Whether matrices of `rows` rows, `stride` elements apart, do not reach into one another (no
+// product is formed that could pass 64 bits).
+bool apart(int64_t stride, int64_t rows, int64_t ld, int64_t cols) {
+    return stride >= cols && (rows <= 1 || (stride - cols) / (rows - 1) >= ld);
+}
 bool finite_positive(float x) { return std::isfinite(x) && x > 0.0f; }
 
 // Upper bound of the tiles of bm rows that `experts` runs of M rows in all can have: every
@@ -84,11 +91,12 @@ bool forced_group(int* cfg) {
 bool group_cfg_ok(const GroupCfg& c, bool ta, bool tb, int esz, const GroupedParams& q) {
     if ((c.e4m3 != 0) != (esz == 1) || (ta ? c.rate_d : c.rate) <= 0.0) return false;
     if (!aligned(q.g.A, 16) || !aligned(q.g.B, 16)) return false;
+    constexpr int64_t kLim = (int64_t)1 << 31;
+    if (q.g.lda >= kLim || q.g.ldb >= kLim) return false;
     if (q.g.lda * esz % 16 != 0 || q.g.ldb * esz % 16 != 0 || q.sB % 16 != 0) return false;
     const int nw = c.WM * c.WN;
     if (!dma_tile_ok(!ta, c.BM, c.BK, esz, nw) || !dma_tile_ok(tb, c.BN, c.BK, esz, nw))
         return false;
-    constexpr int64_t kLim = (int64_t)1 << 31;
     return ((ta ? c.BK : c.BM) * q.g.lda + 256) * esz < kLim &&
            ((tb ? c.BN : c.BK) * q.g.ldb + 256) * esz < kLim;
 }
@@ -250,7 +258,7 @@ int sg_grouped_gemm(char transB, int64_t experts, const int32_t* offsets, int64_
     if (reads && !B) return -11;
     const int64_t brow = tb ? K : N;
     if (ldb < (brow > 1 ? brow : 1)) return -12;
-    if (strideB < 0) return -13;
+    if (strideB < 0 || (experts > 1 && strideB > kMaxStride)) return -13;
     if (M > 0 && N > 0 && !C) return -15;
     if (ldc < (N > 1 ? N : 1)) return -16;
     if (dtype != SG_F16 && dtype != SG_BF16 && dtype != SG_F8E4M3) return -17;
@@ -271,7 +279,7 @@ int sg_grouped_gemm(char transB, int64_t experts, const int32_t* offsets, int64_
     q.scale = reads ? scale : nullptr;
     q.experts = (int)experts;
     q.rows = (int)M;
-    q.sB = strideB * esz;
+    q.sB = experts > 1 ? strideB * esz : 0;
     return run_rows("grouped_gemm", EPI_GEMM, tb, dtype, q, static_cast<hipStream_t>(stream));
 }
 
@@ -291,7 +299,8 @@ int sg_grouped_gemm_wgrad(int64_t experts, const int32_t* offsets, int64_t M, in
     if (ldd < (N > 1 ? N : 1)) return -10;
     if (N > 0 && K > 0 && !C) return -12;
     if (ldc < (N > 1 ? N : 1)) return -13;
-    if (experts > 1 && N > 0 && K > 0 && strideC < (K - 1) * ldc + N) return -14;
+    if (experts > 1 && N > 0 && K > 0 && (strideC > kMaxStride || !apart(strideC, K, ldc, N)))
+        return -14;
     if (dtype != SG_F16 && dtype != SG_BF16) return -15;
     if (c_dtype != dtype && c_dtype != SG_F32) return -16;
     if (N == 0 || K == 0) return 0;
@@ -310,7 +319,7 @@ int sg_grouped_gemm_wgrad(int64_t experts, const int32_t* offsets, int64_t M, in
     q.offsets = offsets;
     q.experts = (int)experts;
     q.rows = reads ? (int)M : 0;      // nothing is summed, and nothing read, past row 0
-    q.sC = strideC * (f32 ? 4 : 2);
+    q.sC = experts > 1 ? strideC * (f32 ? 4 : 2) : 0;
     return run_depth("grouped_wgrad", f32 ? EPI_GEMM_F32 : EPI_GEMM, dtype, q,
                      static_cast<hipStream_t>(stream));
 }
@@ -390,7 +399,7 @@ int sg_mxfp4_quantize(const void* X, int64_t ldx, int64_t strideX, int64_t batch
                       void* stream) {
     if (M > 0 && K > 0 && batch > 0 && !X) return -1;
     if (ldx < (K > 1 ? K : 1)) return -2;
-    if (strideX < 0) return -3;
+    if (strideX < 0 || (batch > 1 && strideX > kMaxStride)) return -3;
     if (batch < 0 || batch > 65535) return -4;
     if (M < 0 || M > kMaxDim) return -5;
     if (K < 0 || K > kMaxDim) return -6;
@@ -409,11 +418,11 @@ int sg_mxfp4_quantize(const void* X, int64_t ldx, int64_t strideX, int64_t batch
     p.values = values;
     p.ldx = ldx;
     p.ldv = K;
-    p.sX = strideX * esz;
+    p.sX = batch > 1 ? strideX * esz : 0;
     p.sV = M * K * esz;
     p.M = (int)M;
     p.K = (int)K;
-    p.vec_x = aligned(X, 16) && ldx * esz % 16 == 0 && p.sX % 16 == 0;
+    p.vec_x = aligned(X, 16) && ldx % (16 / esz) == 0 && p.sX % 16 == 0;
     p.vec_v = aligned(values, 16) && K * esz % 16 == 0;
     const dim3 grid((unsigned)blocks, 1, (unsigned)batch);
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -438,7 +447,8 @@ int sg_mxfp4_dequantize(const void* codes, const void* scales, int64_t batch, in
     if (K < 0 || K > kMaxDim) return -5;
     if (any && !X) return -6;
     if (ldx < (K > 1 ? K : 1)) return -7;
-    if (strideX < 0 || (batch > 1 && any && strideX < (M - 1) * ldx + K)) return -8;
+    if (strideX < 0) return -8;
+    if (batch > 1 && any && (strideX > kMaxStride || !apart(strideX, M, ldx, K))) return -8;
     if (dtype < SG_F32 || dtype > SG_BF16) return -9;
     if (!any) return 0;
     const int64_t blocks = cdiv(M, 32) * mx_tiles_k(K);
@@ -449,10 +459,10 @@ int sg_mxfp4_dequantize(const void* codes, const void* scales, int64_t batch, in
     p.scales = const_cast<uint8_t*>(static_cast<const uint8_t*>(scales));
     p.values = X;
     p.ldv = ldx;
-    p.sV = strideX * esz;
+    p.sV = batch > 1 ? strideX * esz : 0;
     p.M = (int)M;
     p.K = (int)K;
-    p.vec_v = aligned(X, 16) && ldx * esz % 16 == 0 && p.sV % 16 == 0;
+    p.vec_v = aligned(X, 16) && ldx % (16 / esz) == 0 && p.sV % 16 == 0;
     const dim3 grid((unsigned)blocks, 1, (unsigned)batch);
     hipStream_t st = static_cast<hipStream_t>(stream);
     describe("mxfp4_dequantize", -2, "");
@@ -470,7 +480,7 @@ int sg_mxfp4_tile_scales(const void* src, int64_t ld, int64_t stride, int64_t ba
     const bool any = batch > 0 && M > 0 && blocks > 0;
     if (any && !src) return -1;
     if (ld < (blocks > 1 ? blocks : 1)) return -2;
-    if (stride < 0) return -3;
+    if (stride < 0 || (batch > 1 && stride > kMaxStride)) return -3;
     if (batch < 0 || batch > 65535) return -4;
     if (M < 0 || M > kMaxDim) return -5;
     if (blocks < 0 || blocks > kMaxDim / kMxBlock) return -6;
