@@ -44,10 +44,9 @@ __device__ __forceinline__ int group_offset(const GroupedParams& q, int e) {
 }
 
 // The work of one work-group: expert e, whose rows are [row0, row0 + rows), and the rows from
-// m0 on and columns from tile tn of its product; half: only half of the tile's rows; end: the
-// row behind the last expert's.
+// m0 on and columns from tile tn of its product; half: only half of the tile's rows.
 struct GroupItem {
-    int e, row0, rows, m0, tn, end;
+    int e, row0, rows, m0, tn;
     bool half;
 };
 
@@ -112,7 +111,7 @@ __device__ __forceinline__ bool find_rows(const GroupedParams& q, int bid, int l
         if (!xcd_item<OCC>(bid, tiles_m * tiles_n, lid, part)) return false;
         it.e = 0;
         it.row0 = 0;
-        it.rows = it.end = q.rows;
+        it.rows = q.rows;
         tile_coords(lid, tiles_m, tiles_n, q.g.group_m, tm, it.tn);
         it.m0 = tm * BM + (part > 0 ? BM / 2 : 0);
         it.half = part >= 0;
@@ -152,8 +151,6 @@ __device__ __forceinline__ bool find_rows(const GroupedParams& q, int bid, int l
     it.e = e;
     it.row0 = row0;
     it.rows = n;
-    it.end = per == 1 ? __builtin_amdgcn_readlane(row + len, q.experts - 1)
-                      : __builtin_amdgcn_readfirstlane(group_offset(q, q.experts));
     tile_coords(lid - first, tiles_m, tiles_n, q.g.group_m, tm, it.tn);
     it.m0 = tm * BM + (part > 0 ? BM / 2 : 0);
     it.half = part >= 0;
@@ -183,12 +180,10 @@ __device__ __forceinline__ bool find_depth(const GroupedParams& q, int bid, int 
         it.e = __builtin_ctzll(__ballot(lane < q.experts && before == place));
         it.row0 = __builtin_amdgcn_readlane(row, it.e);
         n = __builtin_amdgcn_readlane(rows, it.e);
-        it.end = __builtin_amdgcn_readlane(row + rows, q.experts - 1);
     } else {
         it.e = place;
         it.row0 = __builtin_amdgcn_readfirstlane(group_offset(q, place));
         n = __builtin_amdgcn_readfirstlane(group_offset(q, place + 1)) - it.row0;
-        it.end = __builtin_amdgcn_readfirstlane(group_offset(q, q.experts));
     }
     it.rows = n > 0 ? n : 0;
     int tm;

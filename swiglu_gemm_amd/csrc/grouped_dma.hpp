@@ -139,21 +139,22 @@ __device__ __forceinline__ void epilogue_swiglu_bwd_lds(const Gemm16Params& p, c
 }
 
 // Whether the partial K tile at the end of a tile's loop may be read whole: everything it would
-// load behind K, rows clamped to the tile's own, lies in front of the end of the experts' rows and
-// inside their matrices.  Rows of no expert and gaps between the matrices are not read; what lies
-// between one row's end and the next row may be, and the fragments are cut so that none of it
-// counts.
+// load behind K, rows clamped to the tile's own, lies in front of `end`, the row behind the last
+// expert's, and inside the experts' matrices.  Rows of no expert and gaps between the matrices are
+// not read; what lies between one row's end and the next row may be, and the fragments are cut so
+// that none of it counts.
 template <bool TA, bool TB, int BM, int BN, int BK, int ESZ>
 __host__ __device__ inline bool tail_readable(const GroupedParams& q, const GroupItem& it,
-                                              const Gemm16Params& p, int m0, int n0, int nkt) {
+                                              const Gemm16Params& p, int end, int m0, int n0,
+                                              int nkt) {
     const int past = (nkt + 1) * BK;                     // the whole tile's last k, plus 1
     if constexpr (TA) {
         // k are rows of A and D; past the expert's rows come the next expert's
-        return it.row0 + past <= it.end;
+        return it.row0 + past <= end;
     } else {
         // A: k run along a row, so past K comes the next row, if there is one
         const int rows = m0 + BM < p.M ? m0 + BM : p.M;
-        const bool a_in = it.row0 + rows < it.end && past <= q.g.lda + p.K;
+        const bool a_in = it.row0 + rows < end && past <= q.g.lda + p.K;
         const bool more = it.e + 1 < q.experts && q.sB == (int64_t)(TB ? p.N : p.K) * p.ldb * ESZ;
         const bool b_in = TB ? (more || n0 + BN < p.N) && past <= p.ldb + p.K
                              : more && past - p.K <= p.K;
@@ -175,8 +176,11 @@ __device__ __forceinline__ void grouped_tile(const GroupedParams& q, const Group
         for (int j = 0; j < D::FM; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    const bool ring_tail =
-        ktail > 0 && tail_readable<TA, TB, BM, BN, BK, D::ESZ>(q, it, p, m0, n0, nkt);
+    bool ring_tail = false;
+    if (ktail > 0) {
+        const int end = __builtin_amdgcn_readfirstlane(group_offset(q, q.experts));
+        ring_tail = tail_readable<TA, TB, BM, BN, BK, D::ESZ>(q, it, p, end, m0, n0, nkt);
+    }
     dma_mainloop<DT, TA, TB, EPI, BM, BN, BK, S, WM, WN, true>(p, smem, m0, n0, 0, nkt, ktail, acc,
                                                                wave, lane, ring_tail);
     const int wm = wave % WM, wn = wave / WM;

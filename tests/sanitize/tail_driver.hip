@@ -54,7 +54,6 @@ static void problem(const std::vector<int>& off, int rows, int N, int K, int pad
         GroupItem it{};
         it.e = e;
         it.row0 = off[e];
-        it.end = end;
         it.rows = off[e + 1] - off[e];
         if (it.rows <= 0) continue;
         Gemm16Params p = q.g;
@@ -64,7 +63,7 @@ static void problem(const std::vector<int>& off, int rows, int N, int K, int pad
         if (p.K % BK == 0) continue;
         for (int m0 = 0; m0 < p.M; m0 += BM)
             for (int n0 = 0; n0 < N; n0 += BN) {
-                if (!tail_readable<TA, TB, BM, BN, BK, 2>(q, it, p, m0, n0, nkt)) continue;
+                if (!tail_readable<TA, TB, BM, BN, BK, 2>(q, it, p, end, m0, n0, nkt)) continue;
                 ++let;
                 const long k0 = (long)nkt * BK;
                 if (TA) {
