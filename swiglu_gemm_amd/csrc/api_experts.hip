@@ -168,9 +168,12 @@ int choose_group(bool depth, bool tb, int esz, const GroupedParams& q) {
     }
     // A few rows each against weights stored K x N: where 256-wide tiles make close to one round
     // (3/4 of the CUs to all), their 512-byte pieces of a weight's rows stream faster than twice
-    // as many of 256 bytes (K = 2048; 32 experts, N = 2048, 64 and 512 rows in all: 45.0 -> 41.4,
-    // 52.3 -> 48.7 us; 64 experts, N = 1024, 512 rows: 52.9 -> 50.8 us; with more tiles, N =
-    // 2816, 512 rows of 48 experts, 80.4 against 89.8 us).
+    // as many of 256 bytes.  Measured on 306 such calls (8 to 64 experts, N = 768 to 8192, K = 512
+    // to 4096, 1 to 32 rows each, plain and SwiGLU), 256 wide over 128 wide: at 192 tiles 1.05 for
+    // K = 512, 1.00 for 1024, 0.99 for 2048, 0.94 for 4096; at 256 tiles 0.94, 0.93, 0.91, 0.86
+    // (K = 2048, 32 experts, N = 2048: 49.3 -> 46.5 us); all of them 0.95 in the mean, the worst
+    // 1.10 (K = 512, 64 experts, N = 768: 12.8 -> 14.1 us).  With more tiles it loses: N = 2816,
+    // 512 rows of 48 experts, 80.4 -> 89.8 us.
     if (cfg == kFewRows && !depth && !tb) {
         const int64_t runs = q.experts < q.rows ? q.experts : q.rows;
         const int64_t wide = runs * cdiv(q.g.N, kGroupCfg[kTwoPerCu].BN);
@@ -208,6 +211,15 @@ int run_depth(const char* what, int epi, int dtype, GroupedParams q, hipStream_t
                                (int64_t)q.experts * q.g.tiles_m * q.g.tiles_n, st));
 }
 
+// Wide tiles where they fill the chip, 32-row ones for a few rows, the narrow ones of those where
+// even they leave CUs idle.  Measured against every tile forced on 130 problems (one weight of 1 to
+// 8192 rows, N = 2048 to 11008; 8 to 64 experts of 1 to 1024 rows, plain and SwiGLU; K = 2048 and
+// 4096): the choice takes 1.03 of the best tile's time in the mean, at most 1.22.  32-row tiles are
+// mostly ahead of 128 x 128 while there are fewer than 256 of the latter (one weight, 1024 rows,
+// 2048 x 2048: 9.1 against 10.5 us; not so 256 rows, 2048 x 11008: 13.8 against 11.6 us), 256 x 256
+// of 128 x 128 in long runs (32 experts of 512 rows, 2048 x 2 x 1408: 69 against 83 us).  It errs
+// most where 128 x 128 runs what makes 150 to 512 tiles of 256 x 256 (64 experts of 256 rows, 2048 x
+// 2048: 68 against 56 us).
 int choose_mx4(const GroupedParams& q) {
     if (const char* s = std::getenv("SG_FORCE_MX4")) {
         const int c = std::atoi(s);
