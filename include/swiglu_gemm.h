@@ -367,7 +367,8 @@ int sg_grouped_swiglu_gemm_bwd(int64_t experts, const int32_t* offsets, const vo
  *           256*((r/32)*ceil(K/256) + b/8) + 128*((b/4)%2) + 4*(r%32) + b%4.
  *           Bytes of rows and blocks outside the matrix are not used.
  * A batch of matrices follows one another, each with its own codes and tiles of scales.
- * These calls allocate nothing and use no workspace.
+ * These calls allocate nothing and use no workspace.  A matrix of more than 2^22 tiles of
+ * scales returns hipErrorInvalidConfiguration from the quantisation and its inverse.
  */
 #define SG_MXFP4_ROW_BYTES(K) ((((int64_t)(K) + 31) / 32) * 16)
 #define SG_MXFP4_SCALE_BYTES(M, K) \
