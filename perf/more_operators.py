@@ -4,7 +4,7 @@ elementary torch operations, and the library's own calls.
 
     route_experts         each token's top_k experts and their weights, from the router's logits
     sort_experts          rows sorted by expert: offsets, the order of the rows and its inverse
-    gather_rows           the tokens' rows in that order
+    spread_rows           the tokens' rows in that order
     combine_rows          each token's weighted sum of its experts' rows; backward
     int4_gemm / _swiglu   products with weights of 4-bit codes, a scale (and zero) for each group
 
@@ -356,7 +356,7 @@ def _own(s):
         return out
     if op == "rows":
         offsets, order, place = sg.sort_experts(s["ids"], case["experts"])
-        sg.gather_rows(s["X"], order, s["Y"], top_k=case["top_k"])
+        sg.spread_rows(s["X"], place, s["Y"])
         return [offsets, order, place, s["Y"]]
     if op == "combine":
         out = [sg.combine_rows(s["Z"], s["place"], s["Z"].new_empty((case["tokens"], case["width"])),
