@@ -433,6 +433,200 @@ int sg_mxfp4_swiglu_gemm(int64_t experts, const int32_t* offsets, int64_t M, int
                          int64_t K, const void* A, const void* As, const void* W,
                          const void* Ws, void* Y, int dtype, void* stream);
 
+/*
+ * Routing to experts
+ * ------------------
+ * What stands around the products grouped by expert: each token's experts and their weights
+ * from the router's logits, the rows sorted by expert, and each token's rows to their places
+ * and back.  A token's place (t, j), j < top_k, is its j-th expert; flat, place t * top_k + j.
+ * These calls allocate nothing and use no workspace; results are run-to-run identical.
+ * Any element-aligned pointers and leading dimensions are accepted.
+ */
+typedef enum { SG_ROUTE_SOFTMAX = 0, SG_ROUTE_SIGMOID = 1 } sg_route_scoring;
+#define SG_ROUTE_MAX_EXPERTS 1024
+#define SG_ROUTE_MAX_TOP_K 64
+
+/*
+ * sg_route_experts: for each row x of X, s = softmax(x) or s = 1 / (1 + e^-x), and
+ *     ids = the top_k experts by c = s + bias, the largest first, of equal ones the lowest index
+ *     weights = scale * s[id], with renormalize scale * s[id] / (sum of s over the chosen)
+ * In groups (groups > 1) of experts / groups neighbours each, the experts come from the
+ * top_groups groups whose group_top best c have the largest sum.  c is compared in 64 bits;
+ * without bias the logits are, which order the experts as their scores do.  Weights are
+ * computed in fp32 (renormalised ones from the chosen experts' log scores, so that they do
+ * not underflow all together).
+ * A logit of -infinity, or a bias of -infinity or NaN, keeps the expert from being chosen; where fewer than
+ * top_k are left, the places behind get id -1 and weight 0.  A NaN logit is not chosen and
+ * makes the weights of the token's chosen experts NaN, as does, with softmax, +infinity.
+ *  1 X, 2 ldx   T x E logits.   3 T (0..2^30)   4 E (1..SG_ROUTE_MAX_EXPERTS)
+ *  5 dtype   of X: SG_F32, SG_F16, SG_BF16.   6 top_k   1..min(E, SG_ROUTE_MAX_TOP_K).
+ *  7 scoring   sg_route_scoring.   8 bias   NULL, or E fp32 values.
+ *  9 groups   1..64, divides E.   10 top_groups   1..groups.   11 group_top   1 or 2.
+ *  12 renormalize   0 or 1.   13 scale   fp32, finite.
+ *  14 mask   NULL, or T bytes: where 0, the row is not read, its ids are -1, its weights 0.
+ *  15 ids   T x top_k int32, contiguous.   16 weights   T x top_k fp32, contiguous.
+ *  17 stream.
+ */
+int sg_route_experts(const void* X, int64_t ldx, int64_t T, int64_t E, int dtype, int64_t top_k,
+                     int scoring, const float* bias, int64_t groups, int64_t top_groups,
+                     int group_top, int renormalize, float scale, const uint8_t* mask,
+                     int32_t* ids, float* weights, void* stream);
+
+/*
+ * sg_route_experts_bwd: dX from the gradient g of the weights, the choice held fixed.  With
+ * p = weights / scale and G = scale * g:
+ *     renormalised       dx[id] = p (G - sum G p), times (1 - s) for sigmoid; 0 elsewhere
+ *     softmax            dx[e] = s_e * (G_e - sum G p), G_e = 0 where e is not chosen
+ *     sigmoid            dx[id] = G s (1 - s); 0 elsewhere
+ * in fp32, rounded once.  Ids outside 0..E-1 are empty places; a row of empty places gets
+ * zeros and is not read.
+ *  1 X, 2 ldx, 3 T, 4 E, 5 dtype, 6 top_k, 7 scoring   as the forward.   8 renormalize
+ *  9 scale   10 ids, 11 dweights   T x top_k.   12 dX, 13 lddx   T x E of X's type.  14 stream.
+ */
+int sg_route_experts_bwd(const void* X, int64_t ldx, int64_t T, int64_t E, int dtype,
+                         int64_t top_k, int scoring, int renormalize, float scale,
+                         const int32_t* ids, const float* dweights, void* dX, int64_t lddx,
+                         void* stream);
+
+/*
+ * sg_sort_experts: the places 0..n-1 sorted by their expert, stably:
+ *     offsets[e]   places of experts below e (experts + 1 of them: the grouped products' table)
+ *     order[r]     the place that is row r, -1 from offsets[experts] on
+ *     place[i]     the row of place i (order[place[i]] == i), -1 where ids[i] is outside
+ *                  0..experts-1
+ *  1 ids, 2 n (0..2^30)   3 experts (1..65536)   4 offsets, 5 order, 6 place (order or place
+ *  may be NULL)   7 stream.
+ */
+int sg_sort_experts(const int32_t* ids, int64_t n, int64_t experts, int32_t* offsets,
+                    int32_t* order, int32_t* place, void* stream);
+
+/*
+ * sg_spread_rows: Y[place[t, j]] = X[t], or weights[t, j] * X[t] (fp32, rounded once).  Places
+ * outside 0..M-1 are empty; rows of Y that no place names stay as they are.  Its gradient is
+ * sg_combine_rows of Y's gradient.
+ *  1 X, 2 ldx   T x D.   3 T, 4 D   >= 0.   5 dtype   SG_F32, SG_F16 or SG_BF16.
+ *  6 place   T x top_k, no two places of one row (or either's values).   7 top_k (1..65536)
+ *  8 weights   NULL, or T x top_k fp32.   9 M   rows of Y.   10 Y, 11 ldy.   12 stream.
+ */
+int sg_spread_rows(const void* X, int64_t ldx, int64_t T, int64_t D, int dtype,
+                   const int32_t* place, int64_t top_k, const float* weights, int64_t M, void* Y,
+                   int64_t ldy, void* stream);
+
+/*
+ * sg_combine_rows: out[t] = residual[t] + sum over j of weights[t, j] * Z[place[t, j]], summed
+ * in fp32 in the order of j, rounded once.  Places outside 0..M-1 are left out (their weights
+ * do not count); a token without a place gets its residual, or zeros.
+ *  1 Z, 2 ldz   M x D.   3 M, 4 D, 5 T   >= 0.   6 dtype   of Z, residual and out.
+ *  7 place, 8 top_k, 9 weights   as sg_spread_rows; weights NULL: 1.
+ *  10 residual (NULL: none), 11 ldr   T x D.   12 out, 13 ldo   T x D.   14 stream.
+ */
+int sg_combine_rows(const void* Z, int64_t ldz, int64_t M, int64_t D, int64_t T, int dtype,
+                    const int32_t* place, int64_t top_k, const float* weights,
+                    const void* residual, int64_t ldr, void* out, int64_t ldo, void* stream);
+
+/*
+ * sg_combine_rows_bwd, from the gradient dOut (T x D) of out:
+ *     dZ[place[t, j]] = weights[t, j] * dOut[t]       rows that no place names stay as they are
+ *     dweights[t, j] = dot(dOut[t], Z[place[t, j]])   0 for an empty place
+ *  1 dOut, 2 lddo, 3 Z, 4 ldz, 5 M, 6 D, 7 T, 8 dtype, 9 place, 10 top_k, 11 weights (not NULL).
+ *  12 dZ, 13 lddz   M x D, or NULL.   14 dweights   T x top_k fp32, or NULL (Z is then not read).
+ *  15 stream.
+ */
+int sg_combine_rows_bwd(const void* dOut, int64_t lddo, const void* Z, int64_t ldz, int64_t M,
+                        int64_t D, int64_t T, int dtype, const int32_t* place, int64_t top_k,
+                        const float* weights, void* dZ, int64_t lddz, float* dweights,
+                        void* stream);
+
+/*
+ * 4-bit integer weights with group scales
+ * ---------------------------------------
+ * A weight of N rows and K columns (the B of C = A * B^T) is held as codes 0..15, and for each
+ * `group` (32, 64 or 128) columns of a row a scale of the activations' type (SG_F16 or SG_BF16)
+ * and, optionally, a zero point of 8 bits:
+ *     W[n, k] = scale[n, k / group] * (code[n, k] - zero[n, k / group]),  zero = 8 where none is held
+ *   codes   SG_INT4_CODE_BYTES(N, K) bytes: tiles of 16 rows x 128 columns, 1024 bytes each, all
+ *           tiles of 16 rows one after the other.  Element (r, c) of a tile, with s = c / 32,
+ *           q = c % 32 / 8, i = c % 8: nibble i / 2 + 4 * (i % 2), counted from the low half of the
+ *           first byte, of the four bytes at 16 * (16 * q + r) + 4 * s.
+ *   scales  SG_INT4_SCALES(N, K, group) values: tiles of 16 rows x 4 groups: row r, group g at
+ *   zeros   64 * ((r / 16) * ceil(groups / 4) + g / 4) + 4 * (r % 16) + g % 4; as many bytes.
+ *           What lies outside the matrix is not used; sg_int4_quantize and _pack write zeros.
+ * A batch of weights follows one another.  These calls allocate nothing and use no workspace;
+ * results are run-to-run identical.
+ */
+#define SG_INT4_CODE_BYTES(N, K) \
+    ((((int64_t)(N) + 15) / 16) * (((int64_t)(K) + 127) / 128) * 1024)
+#define SG_INT4_SCALES(N, K, group) \
+    ((((int64_t)(N) + 15) / 16) * ((((int64_t)(K) + (group) - 1) / (group) + 3) / 4) * 64)
+
+/*
+ * sg_int4_quantize: the codes of W.  For each group, without zeros: scale = max |w| / 7, codes
+ * w / scale + 8; with zeros: lo = min(0, w), hi = max(0, w), scale = (hi - lo) / 15, zero =
+ * -lo / scale and codes w / scale + zero.  The scale is computed in fp32 and rounded to its type
+ * first; zeros and codes follow from the rounded one, to the nearest integer, ties to even,
+ * saturating at 0 and 15.  A group of zeros, or whose scale rounds to 0, gets scale 0, zero 8
+ * and codes 8.  An infinity or a NaN, or a scale past its type's range, makes the group's scale
+ * NaN (zero and codes 8).
+ *  1 W, 2 ldw, 3 strideW   `batch` weights N x K, strideW elements apart.   4 batch (0..65535)
+ *  5 N, 6 K   >= 0.   7 dtype   of W: SG_F32, SG_F16 or SG_BF16.   8 group.
+ *  9 codes (16-byte aligned), 10 scales (8), 11 zeros (4; NULL: none).
+ *  12 scale_dtype   SG_F16 or SG_BF16.   13 stream.
+ */
+int sg_int4_quantize(const void* W, int64_t ldw, int64_t strideW, int64_t batch, int64_t N,
+                     int64_t K, int dtype, int64_t group, void* codes, void* scales, void* zeros,
+                     int scale_dtype, void* stream);
+
+/*
+ * sg_int4_pack: the same from codes, scales and zeros held one after the other: src codes N x K
+ * bytes (their low four bits count), scales and zeros N x ceil(K / group) (zeros: bytes, or NULL), all contiguous, for
+ * `batch` weights.
+ *  1 src, 2 src_scales, 3 src_zeros (NULL with 10 NULL), 4 batch, 5 N, 6 K, 7 group, 8 codes,
+ *  9 scales, 10 zeros, 11 stream.   Alignment as above; src_scales 2 bytes.
+ */
+int sg_int4_pack(const void* src, const void* src_scales, const void* src_zeros, int64_t batch,
+                 int64_t N, int64_t K, int64_t group, void* codes, void* scales, void* zeros,
+                 void* stream);
+
+/*
+ * sg_int4_dequantize: W = the values, fp32, rounded once to W's type.
+ *  1 codes, 2 scales, 3 zeros (NULL: 8), 4 scale_dtype, 5 batch, 6 N, 7 K, 8 group, 9 W, 10 ldw,
+ *  11 strideW (>= (N-1)*ldw + K for more than one), 12 dtype of W, 13 stream.
+ */
+int sg_int4_dequantize(const void* codes, const void* scales, const void* zeros, int scale_dtype,
+                       int64_t batch, int64_t N, int64_t K, int64_t group, void* W, int64_t ldw,
+                       int64_t strideW, int dtype, void* stream);
+
+/*
+ * sg_int4_gemm: C = alpha * A * W^T; with offsets C[r] = alpha * A[row(r)] * W_e^T for r in R_e (see the products
+ * grouped by expert), W a batch of `experts` weights.  row(r) = r, or with `order` (the
+ * table of sg_sort_experts) order[r] / top_k, so that the tokens' rows need not be spread first;
+ * rows of C whose order is outside 0 .. T * top_k - 1 are undefined.  Sums are fp32: codes
+ * meet A unscaled, each group's sum then its scale, so the weights are not rounded.  bf16
+ * products take the codes from 16 up and the zero points out of the sum: an infinity in A, or a value of it above 2^120,
+ * gives NaN where it counts.
+ *  1 experts, 2 offsets   as sg_mxfp4_gemm.   3 order   NULL, or M int32.   4 top_k (1..65536; 1 without
+ *  order).   5 T   rows of A (T = M without order).   6 M   rows of C.   7 N, 8 K, 9 group.
+ *  10 alpha   fp32.   11 A, 12 lda   T x K.   13 codes (16-byte aligned), 14 scales (8),
+ *  15 zeros (4, or NULL).   16 C, 17 ldc   M x N, written only.
+ *  18 dtype   of A and the scales: SG_F16 or SG_BF16.   19 c_dtype   dtype or SG_F32.  20 stream.
+ * Quick returns: M == 0 or N == 0 does nothing; K == 0 or alpha == 0 writes zeros.
+ */
+int sg_int4_gemm(int64_t experts, const int32_t* offsets, const int32_t* order, int64_t top_k,
+                 int64_t T, int64_t M, int64_t N, int64_t K, int64_t group, float alpha,
+                 const void* A, int64_t lda, const void* codes, const void* scales,
+                 const void* zeros, void* C, int64_t ldc, int dtype, int c_dtype, void* stream);
+
+/*
+ * sg_int4_swiglu_gemm: Y = SiLU(A * W1^T) ⊙ (A * W2^T) from W of 2N rows, gate and up
+ * interleaved (row 2n = W1's row n, row 2n+1 = W2's); the rest as sg_int4_gemm.
+ *  1 experts, 2 offsets, 3 order, 4 top_k, 5 T, 6 M, 7 N, 8 K, 9 group, 10 A, 11 lda, 12 codes,
+ *  13 scales, 14 zeros, 15 Y, 16 ldy   M x N.   17 dtype   of A, the scales and Y.   18 stream.
+ */
+int sg_int4_swiglu_gemm(int64_t experts, const int32_t* offsets, const int32_t* order,
+                        int64_t top_k, int64_t T, int64_t M, int64_t N, int64_t K, int64_t group,
+                        const void* A, int64_t lda, const void* codes, const void* scales,
+                        const void* zeros, void* Y, int64_t ldy, int dtype, void* stream);
+
 /* Text for a status code returned by any sg_* call (static storage). */
 const char* sg_status_string(int status);
 

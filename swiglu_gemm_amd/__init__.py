@@ -22,6 +22,16 @@ microscaled 4-bit floating point:
     mxfp4_quantize(X) -> codes, scales                       # and mxfp4_dequantize
     mxfp4_gemm(A, As, B, Bs, C, offsets=None)                # C = A @ B^T
     mxfp4_swiglu_gemm(A, As, W, Ws, Y, offsets=None)
+
+The routing around them, and weights of 4-bit integers with group scales:
+
+    route_experts(X, top_k, ...) -> ids, weights             # and route_experts_bwd
+    sort_experts(ids, experts) -> offsets, order, place      # rows sorted by expert
+    spread_rows(X, place, Y)                                 # Y[place[t, j]] = X[t]
+    combine_rows(Z, place, out, weights)                     # and combine_rows_bwd
+    int4_quantize(W, group=128) -> codes, scales, zeros      # int4_pack, int4_dequantize
+    int4_gemm(A, codes, scales, C, offsets=None)             # C = A @ W^T
+    int4_swiglu_gemm(A, codes, scales, Y, offsets=None)
 """
 from __future__ import annotations
 
@@ -35,6 +45,7 @@ LIB_PATH = os.path.join(HERE, "libswiglu_gemm.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "swiglu_gemm.h")
 
 SG_F32, SG_F16, SG_BF16, SG_F8E4M3 = 0, 1, 2, 3
+SCORINGS = {"softmax": 0, "sigmoid": 1}
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
 
 
@@ -99,6 +110,21 @@ def lib() -> ctypes.CDLL:
             "sg_mxfp4_tile_scales": [vp, i64, i64, i64, i64, i64, vp, vp],
             "sg_mxfp4_gemm": [i64, vp, i64, i64, i64, f32, vp, vp, vp, vp, vp, i64, ci, vp],
             "sg_mxfp4_swiglu_gemm": [i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, ci, vp],
+            "sg_route_experts": [vp, i64, i64, i64, ci, i64, ci, vp, i64, i64, ci, ci, f32, vp, vp,
+                                 vp, vp],
+            "sg_route_experts_bwd": [vp, i64, i64, i64, ci, i64, ci, ci, f32, vp, vp, vp, i64, vp],
+            "sg_sort_experts": [vp, i64, i64, vp, vp, vp, vp],
+            "sg_spread_rows": [vp, i64, i64, i64, ci, vp, i64, vp, i64, vp, i64, vp],
+            "sg_combine_rows": [vp, i64, i64, i64, i64, ci, vp, i64, vp, vp, i64, vp, i64, vp],
+            "sg_combine_rows_bwd": [vp, i64, vp, i64, i64, i64, i64, ci, vp, i64, vp, vp, i64, vp,
+                                    vp],
+            "sg_int4_quantize": [vp, i64, i64, i64, i64, i64, ci, i64, vp, vp, vp, ci, vp],
+            "sg_int4_pack": [vp, vp, vp, i64, i64, i64, i64, vp, vp, vp, vp],
+            "sg_int4_dequantize": [vp, vp, vp, ci, i64, i64, i64, i64, vp, i64, i64, ci, vp],
+            "sg_int4_gemm": [i64, vp, vp, i64, i64, i64, i64, i64, i64, f32, vp, i64, vp, vp, vp,
+                             vp, i64, ci, ci, vp],
+            "sg_int4_swiglu_gemm": [i64, vp, vp, i64, i64, i64, i64, i64, i64, vp, i64, vp, vp, vp,
+                                    vp, i64, ci, vp],
         }
         for name, types in experts.items():
             getattr(L, name).argtypes = types
@@ -891,4 +917,373 @@ def mxfp4_swiglu_gemm(A, As, W, Ws, Y, offsets=None):
     _contig(Y, "Y", (M, N))
     _launch("sg_mxfp4_swiglu_gemm", lib().sg_mxfp4_swiglu_gemm, (Y, A, As, W, Ws, offsets), E, op,
             M, N, K, A.data_ptr(), As.data_ptr(), W.data_ptr(), Ws.data_ptr(), Y.data_ptr(), code)
+    return Y
+
+
+# ------------------------------------------------- routing to experts
+def _ints(t, name: str, shape) -> int:
+    if t.dtype is not _torch()[0].int32:
+        raise TypeError("%s must be int32, not %s" % (name, t.dtype))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous of shape %s, not %s" % (name, tuple(shape),
+                                                                        tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _floats(t, name: str, shape) -> int:
+    if t.dtype is not _torch()[0].float32:
+        raise TypeError("%s must be float32, not %s" % (name, t.dtype))
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s must be contiguous of shape %s, not %s" % (name, tuple(shape),
+                                                                        tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _row_type(t, name: str) -> int:
+    code = _dtype_code(t)
+    if code == SG_F8E4M3:
+        raise TypeError("%s must be fp32, fp16 or bf16" % name)
+    if len(t.shape) != 2:
+        raise ValueError("%s must be 2-D" % name)
+    return code
+
+
+def _places(place):
+    if len(place.shape) != 2 or place.shape[1] < 1:
+        raise ValueError("place must be 2-D, the places of each token")
+    return _ints(place, "place", place.shape)
+
+
+def route_experts(X, top_k: int, scoring: str = "softmax", bias=None, groups: int = 1,
+                  top_groups: int = 1, group_top: int = 2, renormalize: bool = True,
+                  scale: float = 1.0, mask=None, ids=None, weights=None):
+    """The top_k experts of each token (row of X [T, E], fp32, fp16 or bf16; rows may be strided)
+    and their weights: returns (ids int32 [T, top_k], weights float32 [T, top_k]), best first.
+    scoring: 'softmax' over the experts or 'sigmoid'; bias: None or float32 [E], added for the
+    choice only; groups > 1: the experts come from the top_groups groups of neighbours whose
+    group_top (1 or 2) best have the largest sum; renormalize: the weights of a token sum to 1;
+    scale multiplies them.  Equal values go to the lowest index.  mask: None or bool [T], tokens
+    where it is False get id -1 and weight 0 and are not read; so do places for which no expert is
+    left (a logit of -inf takes one out).  ids, weights: tensors to write."""
+    code = _row_type(X, "X")
+    if scoring not in SCORINGS:
+        raise ValueError("scoring must be one of %s" % ", ".join(SCORINGS))
+    T, E = X.shape
+    ldx = _rows(X, "X", E)
+    top_k, groups, top_groups = int(top_k), int(groups), int(top_groups)
+    if not 1 <= top_k <= min(E, 64):
+        raise ValueError("top_k must be 1 to %d, not %d" % (min(E, 64), top_k))
+    if E > 1024:
+        raise ValueError("X has %d experts, at most 1024 are supported" % E)
+    if not 1 <= groups <= 64 or E % groups or not 1 <= top_groups <= groups:
+        raise ValueError("groups (1 to 64) must divide the %d experts, top_groups be 1 to groups" % E)
+    if group_top not in (1, 2):
+        raise ValueError("group_top must be 1 or 2")
+    bp = None if bias is None else _floats(bias, "bias", (E,))
+    torch = _torch()[0]
+    mp = None
+    if mask is not None:
+        if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
+            raise TypeError("mask must be bool")
+        if mask.shape != (T,) or not mask.is_contiguous():
+            raise ValueError("mask must be a contiguous vector of %d tokens" % T)
+        mp = mask.data_ptr()
+    if ids is None:
+        ids = X.new_empty((T, top_k), dtype=torch.int32)
+    if weights is None:
+        weights = X.new_empty((T, top_k), dtype=torch.float32)
+    ip, wp = _ints(ids, "ids", (T, top_k)), _floats(weights, "weights", (T, top_k))
+    _launch("sg_route_experts", lib().sg_route_experts, (ids, X, bias, mask, weights), X.data_ptr(),
+            ldx, T, E, code, top_k, SCORINGS[scoring], bp, groups, top_groups, group_top,
+            int(bool(renormalize)), float(scale), mp, ip, wp)
+    return ids, weights
+
+
+def route_experts_bwd(X, ids, dweights, dX, scoring: str = "softmax", renormalize: bool = True,
+                      scale: float = 1.0):
+    """dX [T, E] (X's dtype): the gradient of route_experts' weights, the choice ids [T, top_k]
+    held fixed, from the weights' gradient dweights (float32 [T, top_k])."""
+    code = _row_type(X, "X")
+    if scoring not in SCORINGS:
+        raise ValueError("scoring must be one of %s" % ", ".join(SCORINGS))
+    T, E = X.shape
+    ldx = _rows(X, "X", E)
+    if E > 1024:
+        raise ValueError("X has %d experts, at most 1024 are supported" % E)
+    if len(ids.shape) != 2 or ids.shape[0] != T or not 1 <= ids.shape[1] <= min(E, 64):
+        raise ValueError("ids must be the 1 to %d experts of each token" % min(E, 64))
+    k = ids.shape[1]
+    ip, gp = _ints(ids, "ids", (T, k)), _floats(dweights, "dweights", (T, k))
+    if dX.dtype != X.dtype:
+        raise TypeError("dX must have X's dtype")
+    lddx = _rows(dX, "dX", E)
+    if dX.shape[0] != T:
+        raise ValueError("dX has %d rows, X %d" % (dX.shape[0], T))
+    _launch("sg_route_experts_bwd", lib().sg_route_experts_bwd, (dX, X, ids, dweights),
+            X.data_ptr(), ldx, T, E, code, k, SCORINGS[scoring], int(bool(renormalize)),
+            float(scale), ip, gp, dX.data_ptr(), lddx)
+    return dX
+
+
+def sort_experts(ids, experts: int):
+    """The places of ids (int32, [T, top_k] as route_experts gives them, or any shape) sorted by
+    expert, stably: returns (offsets [experts + 1], order [ids.numel()], place like ids), all
+    int32.  offsets is the table of the grouped products; order[r] is the flat place that is row r,
+    place[t, j] the row of place (t, j).  Places of no expert (id -1) come last in order, as -1, and
+    have place -1."""
+    torch = _torch()[0]
+    experts = int(experts)
+    if not 1 <= experts <= 65536:
+        raise ValueError("experts must be 1 to 65536, not %d" % experts)
+    ip = _ints(ids, "ids", ids.shape)
+    n = ids.numel()
+    offsets = ids.new_empty((experts + 1,))
+    order, place = ids.new_empty((n,)), torch.empty_like(ids)
+    _launch("sg_sort_experts", lib().sg_sort_experts, (ids, offsets), ip, n, experts,
+            offsets.data_ptr(), order.data_ptr(), place.data_ptr())
+    return offsets, order, place
+
+
+def spread_rows(X, place, Y, weights=None):
+    """Y[place[t, j]] = X[t], times weights[t, j] (float32 [T, top_k]) where given, in place on Y
+    [M, D]; X [T, D] of Y's dtype (fp32, fp16 or bf16), rows may be strided.  Negative places
+    (and any outside Y) are left out; rows of Y that no place names stay as they are.  The gradient
+    is combine_rows(dY, place, dX)."""
+    code = _row_type(X, "X")
+    T, D = X.shape
+    ldx, ldy = _rows(X, "X", D), _rows(Y, "Y", D)
+    if Y.dtype != X.dtype:
+        raise TypeError("Y must have X's dtype")
+    pp = _places(place)
+    if place.shape[0] != T:
+        raise ValueError("place has %d tokens, X %d" % (place.shape[0], T))
+    wp = None if weights is None else _floats(weights, "weights", place.shape)
+    _launch("sg_spread_rows", lib().sg_spread_rows, (Y, X, place, weights), X.data_ptr(), ldx, T, D,
+            code, pp, place.shape[1], wp, Y.shape[0], Y.data_ptr(), ldy)
+    return Y
+
+
+def combine_rows(Z, place, out, weights=None, residual=None):
+    """out[t] = residual[t] + the sum over j of weights[t, j] * Z[place[t, j]], in place on out
+    [T, D] of Z's dtype (fp32, fp16 or bf16; summed in fp32); weights: None (1) or float32 [T,
+    top_k]; residual: None or like out.  Rows may be strided.  Places outside Z are left out."""
+    code = _row_type(Z, "Z")
+    M, D = Z.shape
+    ldz, ldo = _rows(Z, "Z", D), _rows(out, "out", D)
+    T = out.shape[0]
+    if out.dtype != Z.dtype:
+        raise TypeError("out must have Z's dtype")
+    pp = _places(place)
+    if place.shape[0] != T:
+        raise ValueError("place has %d tokens, out %d" % (place.shape[0], T))
+    wp = None if weights is None else _floats(weights, "weights", place.shape)
+    rp, ldr = None, D or 1
+    if residual is not None:
+        if residual.dtype != Z.dtype:
+            raise TypeError("residual must have Z's dtype")
+        ldr = _rows(residual, "residual", D)
+        if residual.shape[0] != T:
+            raise ValueError("residual has %d rows, out %d" % (residual.shape[0], T))
+        rp = residual.data_ptr()
+    _launch("sg_combine_rows", lib().sg_combine_rows, (out, Z, place, weights, residual),
+            Z.data_ptr(), ldz, M, D, T, code, pp, place.shape[1], wp, rp, ldr, out.data_ptr(), ldo)
+    return out
+
+
+def combine_rows_bwd(dOut, Z, place, weights, dZ=None, dweights=None):
+    """The gradients of combine_rows from dOut [T, D]: dZ[place[t, j]] = weights[t, j] * dOut[t]
+    (like Z [M, D]; rows that no place names stay as they are) and dweights[t, j] = dOut[t] .
+    Z[place[t, j]] (float32 [T, top_k], 0 for empty places), each where given.  Returns (dZ,
+    dweights).  The residual's gradient is dOut itself."""
+    code = _row_type(Z, "Z")
+    M, D = Z.shape
+    ldz, lddo = _rows(Z, "Z", D), _rows(dOut, "dOut", D)
+    if dOut.dtype != Z.dtype:
+        raise TypeError("dOut must have Z's dtype")
+    pp = _places(place)
+    T = dOut.shape[0]
+    if place.shape[0] != T:
+        raise ValueError("place has %d tokens, dOut %d" % (place.shape[0], T))
+    wp = _floats(weights, "weights", place.shape)
+    zp, lddz = None, D or 1
+    if dZ is not None:
+        if dZ.dtype != Z.dtype:
+            raise TypeError("dZ must have Z's dtype")
+        lddz = _rows(dZ, "dZ", D)
+        if dZ.shape[0] != M:
+            raise ValueError("dZ has %d rows, Z %d" % (dZ.shape[0], M))
+        zp = dZ.data_ptr()
+    gp = None if dweights is None else _floats(dweights, "dweights", place.shape)
+    _launch("sg_combine_rows_bwd", lib().sg_combine_rows_bwd,
+            (dOut, Z, place, weights, dZ, dweights), dOut.data_ptr(), lddo, Z.data_ptr(), ldz, M, D,
+            T, code, pp, place.shape[1], wp, zp, lddz, gp)
+    return dZ, dweights
+
+
+# ------------------------------------------------- 4-bit integer weights
+def int4_shapes(rows: int, cols: int, group: int = 128):
+    """(bytes of the codes, number of the scales) of a rows x cols weight."""
+    tiles = -(-rows // 16)
+    return tiles * -(-cols // 128) * 1024, tiles * -(-(-(-cols // group)) // 4) * 64
+
+
+def _int4_group(group) -> int:
+    if group not in (32, 64, 128):
+        raise ValueError("group must be 32, 64 or 128, not %r" % (group,))
+    return int(group)
+
+
+def _int4_scale(t, name: str) -> int:
+    code = _dtype_code(t)
+    if code not in (SG_F16, SG_BF16):
+        raise TypeError("%s must be fp16 or bf16" % name)
+    return code
+
+
+def _int4_held(codes, scales, zeros, lead, N, K, group) -> None:
+    nc, ns = int4_shapes(N, K, group)
+    _mx_bytes(codes, "codes", lead + (nc,))
+    _contig(scales, "scales", lead + (ns,))
+    if zeros is not None:
+        _mx_bytes(zeros, "zeros", lead + (ns,))
+
+
+def _int4_new(like, lead, N, K, group, dtype, with_zeros):
+    nc, ns = int4_shapes(N, K, group)
+    u8 = _torch()[0].uint8
+    return (like.new_empty(lead + (nc,), dtype=u8), like.new_empty(lead + (ns,), dtype=dtype),
+            like.new_empty(lead + (ns,), dtype=u8) if with_zeros else None)
+
+
+def int4_quantize(W, group: int = 128, zero_points: bool = False, scale_dtype=None):
+    """W [N, K] or [experts, N, K] (fp32, fp16 or bf16; rows may be strided) as 4-bit codes in the
+    kernels' layout: returns (codes, scales, zeros), zeros None without zero_points; the formulas
+    are in include/swiglu_gemm.h.  scale_dtype: fp16 or bf16, the type of the activations that
+    will meet them (W's own if it is one of these)."""
+    code = _mx_float(W, "W")
+    group = _int4_group(group)
+    lead, batch, N, K, ld, stride = _mx_matrices(W, "W")
+    if scale_dtype is None:
+        if code == SG_F32:
+            raise TypeError("scale_dtype must be given for an fp32 W")
+        scale_dtype = W.dtype
+    out = _int4_new(W, lead, N, K, group, scale_dtype, zero_points)
+    scode = _int4_scale(out[1], "scale_dtype")
+    _launch("sg_int4_quantize", lib().sg_int4_quantize, (W,) + out, W.data_ptr(), ld, stride, batch,
+            N, K, code, group, out[0].data_ptr(), out[1].data_ptr(),
+            out[2].data_ptr() if zero_points else None, scode)
+    return out
+
+
+def int4_pack(codes, scales, zeros=None):
+    """The same from codes [N, K] or [experts, N, K] (uint8, one 0..15 a byte) and their scales
+    (fp16 or bf16) and zero points (uint8) [.., N, K / group rounded up], all contiguous; the group
+    follows from the shapes."""
+    torch = _torch()[0]
+    if len(codes.shape) not in (2, 3) or (len(codes.shape) == 3 and codes.shape[0] < 1):
+        raise ValueError("codes must be 2-D, or 3-D with one weight for each expert")
+    lead, (N, K) = tuple(codes.shape[:-2]), codes.shape[-2:]
+    if len(scales.shape) != len(codes.shape):
+        raise ValueError("scales must have one value for each group of a row")
+    fits = [g for g in (128, 64, 32) if -(-K // g) == scales.shape[-1]]
+    if not fits:
+        raise ValueError("scales have %d groups in a row of %d codes, none of 32, 64 or 128"
+                         % (scales.shape[-1], K))
+    group = fits[0]                      # more than one fits where a row is one group: all the same
+    _int4_scale(scales, "scales")
+    _mx_bytes(codes, "codes", lead + (N, K))
+    _contig(scales, "scales", lead + (N, scales.shape[-1]))
+    if zeros is not None:
+        _mx_bytes(zeros, "zeros", scales.shape)
+    out = _int4_new(codes, lead, N, K, group, scales.dtype, zeros is not None)
+    _launch("sg_int4_pack", lib().sg_int4_pack, (codes, scales, zeros) + out, codes.data_ptr(),
+            scales.data_ptr(), zeros.data_ptr() if zeros is not None else None,
+            lead[0] if lead else 1, N, K, group, out[0].data_ptr(), out[1].data_ptr(),
+            out[2].data_ptr() if zeros is not None else None)
+    return out
+
+
+def int4_dequantize(codes, scales, W, zeros=None, group: int = 128):
+    """W [N, K] or [experts, N, K] (fp32, fp16 or bf16, in place; rows may be strided) = the
+    values of codes, scales and zeros, rounded once."""
+    code = _mx_float(W, "W")
+    group = _int4_group(group)
+    lead, batch, N, K, ld, stride = _mx_matrices(W, "W", True)
+    scode = _int4_scale(scales, "scales")
+    _int4_held(codes, scales, zeros, lead, N, K, group)
+    _launch("sg_int4_dequantize", lib().sg_int4_dequantize, (W, codes, scales, zeros),
+            codes.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None else None,
+            scode, batch, N, K, group, W.data_ptr(), ld, stride, code)
+    return W
+
+
+def _int4_product(A, codes, scales, zeros, group, offsets, order, top_k, out, rows_of_w):
+    """Checks of a product: the arguments up to K in the library's order."""
+    code = _dtype_code(A)
+    if code not in (SG_F16, SG_BF16):
+        raise TypeError("A must be fp16 or bf16")
+    if scales.dtype != A.dtype:
+        raise TypeError("scales have dtype %s, expected A's %s" % (scales.dtype, A.dtype))
+    if len(A.shape) != 2 or len(out.shape) != 2:
+        raise ValueError("A and the output must be 2-D")
+    group = _int4_group(group)
+    T, K = A.shape
+    M = out.shape[0]
+    E, op, lead = 1, None, ()
+    if offsets is not None:
+        if len(codes.shape) != 2 or codes.shape[0] < 1:
+            raise ValueError("with offsets the codes must be 2-D, one weight for each expert")
+        E = codes.shape[0]
+        lead = (E,)
+        op = _experts(offsets, E)
+    top_k = int(top_k)
+    rp = None
+    if order is not None:
+        rp = _ints(order, "order", (M,))
+        if top_k < 1:
+            raise ValueError("top_k must be at least 1")
+        if T == 0 and M > 0:
+            raise ValueError("A has no rows for order to name")
+    else:
+        top_k = 1
+        if T != M:
+            raise ValueError("the output has %d rows, A %d" % (M, T))
+    _int4_held(codes, scales, zeros, lead, rows_of_w, K, group)
+    return code, (E, op, rp, top_k, T, M), K, group
+
+
+def int4_gemm(A, codes, scales, C, zeros=None, group: int = 128, offsets=None, order=None,
+              top_k: int = 1, alpha: float = 1.0):
+    """C = alpha * A @ W^T, W [N, K] held as (codes, scales, zeros): A [M, K] fp16 or bf16, scales
+    of its dtype, C [M, N] of its dtype or fp32; rows may be strided.  With offsets (codes, scales
+    and zeros with a leading dimension of experts) the rows of each expert meet its own weight;
+    rows of no expert stay as they are.  With order (sort_experts'), row r of C is computed from row
+    order[r] // top_k of A, so that the tokens' rows need not be spread first."""
+    N = C.shape[-1]
+    code, head, K, group = _int4_product(A, codes, scales, zeros, group, offsets, order, top_k, C, N)
+    if C.dtype != A.dtype and C.dtype is not _torch()[0].float32:
+        raise TypeError("C has dtype %s, expected %s or float32" % (C.dtype, A.dtype))
+    lda, ldc = _rows(A, "A", K), _rows(C, "C", N)
+    _launch("sg_int4_gemm", lib().sg_int4_gemm, (C, A, codes, scales, zeros, offsets, order), *head,
+            N, K, group, float(alpha), A.data_ptr(), lda, codes.data_ptr(), scales.data_ptr(),
+            zeros.data_ptr() if zeros is not None else None, C.data_ptr(), ldc, code,
+            _dtype_code(C))
+    return C
+
+
+def int4_swiglu_gemm(A, codes, scales, Y, zeros=None, group: int = 128, offsets=None, order=None,
+                     top_k: int = 1):
+    """Y = SiLU(A @ W1^T) * (A @ W2^T) from W [2N, K] held as (codes, scales, zeros) with gate and up
+    rows interleaved (torch.stack((W1, W2), 1).flatten(0, 1) before quantising); Y [M, N] of A's
+    dtype.  The rest as int4_gemm."""
+    N = Y.shape[-1]
+    code, head, K, group = _int4_product(A, codes, scales, zeros, group, offsets, order, top_k, Y,
+                                         2 * N)
+    if Y.dtype != A.dtype:
+        raise TypeError("Y has dtype %s, expected %s" % (Y.dtype, A.dtype))
+    lda, ldy = _rows(A, "A", K), _rows(Y, "Y", N)
+    _launch("sg_int4_swiglu_gemm", lib().sg_int4_swiglu_gemm,
+            (Y, A, codes, scales, zeros, offsets, order), *head, N, K, group, A.data_ptr(), lda,
+            codes.data_ptr(), scales.data_ptr(), zeros.data_ptr() if zeros is not None else None,
+            Y.data_ptr(), ldy, code)
     return Y

@@ -1,0 +1,238 @@
+// api_int4.hip -- the C ABI of 4-bit integer weights: argument checks, kernel choice and launches
+// on the caller's stream.  Declarations and contracts are in include/swiglu_gemm.h.  Nothing here
+// allocates or keeps a workspace.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "abi_checks.hpp"
+#include "int4.hpp"
+#include "swiglu_gemm.h"
+
+using namespace sg;
+
+namespace {
+
+bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128; }
+bool half_type(int dtype) { return dtype == SG_F16 || dtype == SG_BF16; }
+
+int run_product(const char* what, int64_t experts, const int32_t* offsets, const int32_t* order,
+                int64_t top_k, int64_t T, int64_t M, int64_t N, int64_t K, int64_t group,
+                const void* A, int64_t lda, const void* codes, const void* scales,
+                const void* zeros, int dtype, Int4Params& x, void* stream) {
+    x.q.g.A = static_cast<const uint16_t*>(A);
+    x.q.g.lda = lda;
+    x.q.g.N = (int)N;
+    x.q.g.K = (int)K;
+    x.q.g.group_m = 4;
+    x.q.offsets = offsets;
+    x.q.experts = (int)experts;
+    x.q.rows = (int)M;
+    x.order = order;
+    x.top_k = (int)top_k;
+    x.T = (int)T;
+    x.codes = static_cast<const uint8_t*>(codes);
+    x.scales = static_cast<const uint16_t*>(scales);
+    x.zeros = static_cast<const uint8_t*>(zeros);
+    x.s_codes = SG_INT4_CODE_BYTES(N, K);
+    x.s_scales = SG_INT4_SCALES(N, K, group);
+    x.tiles_k = (int)int4_tiles_k(K);
+    x.tiles_g = (int)int4_tiles_g(K, group);
+    const int64_t mean = M / (experts < M ? experts : M);
+    const int mt = mean > 16 ? 2 : 1;
+    const int nt = mt == 1 && cdiv(N, 64) * experts < 512 ? cdiv(N, 32) * experts < 512 ? 1 : 2 : 4;
+    x.q.g.tiles_n = (int)cdiv(N, 16 * nt);
+    const int64_t tiles_m = offsets ? most_row_tiles(M, experts, 16 * mt) : cdiv(M, 16 * mt);
+    const int64_t blocks = tiles_m * x.q.g.tiles_n;
+    if (blocks > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
+    describe(what, -2, "");
+    return status_of(launch_int4(dtype == SG_F16 ? DT_F16 : DT_BF16, (int)group, mt, nt, x,
+                                 (unsigned)blocks, static_cast<hipStream_t>(stream)));
+}
+
+void launch_pack(const Int4PackParams& p, bool pack, int dtype, unsigned batch, hipStream_t st) {
+    const int64_t rows = cdiv(p.N, 16) * 16;
+    const int64_t groups = std::max<int64_t>((int64_t)p.tiles_k * 128 / p.group, p.tiles_g * 4);
+    const int64_t blocks = cdiv(rows * groups, 256);
+    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536), 1, batch);
+    if (pack)
+        hipLaunchKernelGGL((int4_pack_kernel<DT_F32, true>), grid, dim3(256), 0, st, p);
+    else if (dtype == SG_F32)
+        hipLaunchKernelGGL((int4_pack_kernel<DT_F32, false>), grid, dim3(256), 0, st, p);
+    else if (dtype == SG_F16)
+        hipLaunchKernelGGL((int4_pack_kernel<DT_F16, false>), grid, dim3(256), 0, st, p);
+    else
+        hipLaunchKernelGGL((int4_pack_kernel<DT_BF16, false>), grid, dim3(256), 0, st, p);
+}
+
+Int4PackParams pack_params(int64_t N, int64_t K, int64_t group, const void* codes,
+                           const void* scales, const void* zeros) {
+    Int4PackParams p{};
+    p.N = (int)N;
+    p.K = (int)K;
+    p.group = (int)group;
+    p.codes = static_cast<uint8_t*>(const_cast<void*>(codes));
+    p.scales = static_cast<uint16_t*>(const_cast<void*>(scales));
+    p.zeros = static_cast<uint8_t*>(const_cast<void*>(zeros));
+    p.s_codes = SG_INT4_CODE_BYTES(N, K);
+    p.s_scales = SG_INT4_SCALES(N, K, group);
+    p.tiles_k = (int)int4_tiles_k(K);
+    p.tiles_g = (int)int4_tiles_g(K, group);
+    return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+int sg_int4_quantize(const void* W, int64_t ldw, int64_t strideW, int64_t batch, int64_t N,
+                     int64_t K, int dtype, int64_t group, void* codes, void* scales, void* zeros,
+                     int scale_dtype, void* stream) {
+    const bool any = batch > 0 && N > 0 && K > 0;
+    if (any && !W) return -1;
+    if (ldw < (K > 1 ? K : 1)) return -2;
+    if (strideW < 0 || (batch > 1 && strideW > kMaxStride)) return -3;
+    if (batch < 0 || batch > 65535) return -4;
+    if (N < 0 || N > kMaxDim) return -5;
+    if (K < 0 || K > kMaxDim) return -6;
+    if (dtype != SG_F32 && !half_type(dtype)) return -7;
+    if (!group_ok(group)) return -8;
+    if (any && (!codes || !aligned(codes, 16))) return -9;
+    if (any && (!scales || !aligned(scales, 8))) return -10;
+    if (!aligned(zeros, 4)) return -11;
+    if (!half_type(scale_dtype)) return -12;
+    if (!any) return 0;
+    Int4PackParams p = pack_params(N, K, group, codes, scales, zeros);
+    p.W = W;
+    p.ldw = ldw;
+    p.sW = batch > 1 ? strideW : 0;
+    p.scale_bf16 = scale_dtype == SG_BF16;
+    describe("int4_quantize", -2, "");
+    launch_pack(p, false, dtype, (unsigned)batch, static_cast<hipStream_t>(stream));
+    return status_of(hipGetLastError());
+}
+
+int sg_int4_pack(const void* src, const void* src_scales, const void* src_zeros, int64_t batch,
+                 int64_t N, int64_t K, int64_t group, void* codes, void* scales, void* zeros,
+                 void* stream) {
+    const bool any = batch > 0 && N > 0 && K > 0;
+    if (any && !src) return -1;
+    if (any && (!src_scales || !aligned(src_scales, 2))) return -2;
+    if (any && !src_zeros != !zeros) return -3;
+    if (batch < 0 || batch > 65535) return -4;
+    if (N < 0 || N > kMaxDim) return -5;
+    if (K < 0 || K > kMaxDim) return -6;
+    if (!group_ok(group)) return -7;
+    if (any && (!codes || !aligned(codes, 16))) return -8;
+    if (any && (!scales || !aligned(scales, 8))) return -9;
+    if (!aligned(zeros, 4)) return -10;
+    if (!any) return 0;
+    Int4PackParams p = pack_params(N, K, group, codes, scales, zeros);
+    p.src = static_cast<const uint8_t*>(src);
+    p.src_scales = static_cast<const uint16_t*>(src_scales);
+    p.src_zeros = static_cast<const uint8_t*>(src_zeros);
+    describe("int4_pack", -2, "");
+    launch_pack(p, true, SG_F32, (unsigned)batch, static_cast<hipStream_t>(stream));
+    return status_of(hipGetLastError());
+}
+
+int sg_int4_dequantize(const void* codes, const void* scales, const void* zeros, int scale_dtype,
+                       int64_t batch, int64_t N, int64_t K, int64_t group, void* W, int64_t ldw,
+                       int64_t strideW, int dtype, void* stream) {
+    const bool any = batch > 0 && N > 0 && K > 0;
+    if (any && (!codes || !aligned(codes, 16))) return -1;
+    if (any && (!scales || !aligned(scales, 8))) return -2;
+    if (!aligned(zeros, 4)) return -3;
+    if (!half_type(scale_dtype)) return -4;
+    if (batch < 0 || batch > 65535) return -5;
+    if (N < 0 || N > kMaxDim) return -6;
+    if (K < 0 || K > kMaxDim) return -7;
+    if (!group_ok(group)) return -8;
+    if (any && !W) return -9;
+    if (ldw < (K > 1 ? K : 1)) return -10;
+    if (strideW < 0) return -11;
+    if (batch > 1 && any && (strideW > kMaxStride || !apart(strideW, N, ldw, K))) return -11;
+    if (dtype != SG_F32 && !half_type(dtype)) return -12;
+    if (!any) return 0;
+    Int4PackParams p = pack_params(N, K, group, codes, scales, zeros);
+    p.out = W;
+    p.ldw = ldw;
+    p.sW = batch > 1 ? strideW : 0;
+    p.scale_bf16 = scale_dtype == SG_BF16;
+    const int64_t blocks = cdiv(N * cdiv(K, 8), 256);
+    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536), 1, (unsigned)batch);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    describe("int4_dequantize", -2, "");
+    if (dtype == SG_F32)
+        hipLaunchKernelGGL(int4_dequantize_kernel<DT_F32>, grid, dim3(256), 0, st, p);
+    else if (dtype == SG_F16)
+        hipLaunchKernelGGL(int4_dequantize_kernel<DT_F16>, grid, dim3(256), 0, st, p);
+    else
+        hipLaunchKernelGGL(int4_dequantize_kernel<DT_BF16>, grid, dim3(256), 0, st, p);
+    return status_of(hipGetLastError());
+}
+
+int sg_int4_gemm(int64_t experts, const int32_t* offsets, const int32_t* order, int64_t top_k,
+                 int64_t T, int64_t M, int64_t N, int64_t K, int64_t group, float alpha,
+                 const void* A, int64_t lda, const void* codes, const void* scales,
+                 const void* zeros, void* C, int64_t ldc, int dtype, int c_dtype, void* stream) {
+    if (experts < 1 || experts > kMaxExperts) return -1;
+    if (!offsets && experts != 1) return -2;
+    if (top_k < 1 || top_k > 65536 || (!order && top_k != 1)) return -4;
+    if (M < 0 || M > kMaxDim) return -6;
+    if (N < 0 || N > kMaxDim) return -7;
+    if (K < 0 || K > kMaxDim) return -8;
+    const bool reads = M > 0 && N > 0 && K > 0 && alpha != 0.0f;
+    if (T < 0 || T > kMaxDim || (!order && T != M) || (reads && T == 0)) return -5;
+    if (!group_ok(group)) return -9;
+    if (reads && !A) return -11;
+    if (lda < (K > 1 ? K : 1)) return -12;
+    if (reads && (!codes || !aligned(codes, 16))) return -13;
+    if (reads && (!scales || !aligned(scales, 8))) return -14;
+    if (!aligned(zeros, 4)) return -15;
+    if (M > 0 && N > 0 && !C) return -16;
+    if (ldc < (N > 1 ? N : 1)) return -17;
+    if (!half_type(dtype)) return -18;
+    if (c_dtype != dtype && c_dtype != SG_F32) return -19;
+    if (M == 0 || N == 0) return 0;
+    Int4Params x{};
+    x.q.g.C = C;
+    x.q.g.ldc = ldc;
+    x.q.g.alpha = reads ? alpha : 0.0f;
+    x.c_f32 = c_dtype == SG_F32;
+    return run_product("int4_gemm", experts, offsets, order, top_k, T, M, N, reads ? K : 0, group,
+                       A, lda, codes, scales, zeros, dtype, x, stream);
+}
+
+int sg_int4_swiglu_gemm(int64_t experts, const int32_t* offsets, const int32_t* order,
+                        int64_t top_k, int64_t T, int64_t M, int64_t N, int64_t K, int64_t group,
+                        const void* A, int64_t lda, const void* codes, const void* scales,
+                        const void* zeros, void* Y, int64_t ldy, int dtype, void* stream) {
+    if (experts < 1 || experts > kMaxExperts) return -1;
+    if (!offsets && experts != 1) return -2;
+    if (top_k < 1 || top_k > 65536 || (!order && top_k != 1)) return -4;
+    if (M < 0 || M > kMaxDim) return -6;
+    if (N < 0 || N > kMaxDim / 2) return -7;
+    if (K < 0 || K > kMaxDim) return -8;
+    const bool reads = M > 0 && N > 0 && K > 0;
+    if (T < 0 || T > kMaxDim || (!order && T != M) || (reads && T == 0)) return -5;
+    if (!group_ok(group)) return -9;
+    if (reads && !A) return -10;
+    if (lda < (K > 1 ? K : 1)) return -11;
+    if (reads && (!codes || !aligned(codes, 16))) return -12;
+    if (reads && (!scales || !aligned(scales, 8))) return -13;
+    if (!aligned(zeros, 4)) return -14;
+    if (M > 0 && N > 0 && !Y) return -15;
+    if (ldy < (N > 1 ? N : 1)) return -16;
+    if (!half_type(dtype)) return -17;
+    if (M == 0 || N == 0) return 0;
+    Int4Params x{};
+    x.q.g.C = Y;
+    x.q.g.ldc = ldy;
+    x.q.g.alpha = 1.0f;
+    x.swiglu = 1;
+    return run_product("int4_swiglu", experts, offsets, order, top_k, T, M, 2 * N, reads ? K : 0,
+                       group, A, lda, codes, scales, zeros, dtype, x, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,347 @@
+// int4.hpp -- products with weights of 4-bit integers that share a scale (and a zero point) in
+// groups of 32, 64 or 128 along K:  W[n, k] = scale[n, g] * (code[n, k] - zero[n, g]).
+//
+// Codes lie in tiles of 16 rows x 128 columns (1024 bytes) in the order in which a wave's lanes
+// feed them to the 16 x 16 x 32 matrix instruction: lane 16 q + r loads 16 bytes, and dword s of
+// them holds W[r, 32 s + 8 q .. + 7], element i in nibble i/2 + 4 (i % 2), so that masking out
+// one nibble of each half gives two neighbours of k.  A tile is one 1024-byte load of a wave.
+//
+// The codes meet the activations unscaled: a group's sum over k of a * (code - zero) is taken in
+// fp32 accumulators, then multiplied by the group's scale and added to the running sum, so
+// neither the weights nor the groups' sums are rounded to 16 bits.
+//   fp16: 0x6400 | code is 1024 + code; subtracting 1024 + zero leaves code - zero exactly.
+//   bf16: there is no packed bf16 subtraction, so 0x4180 | code << 3, which is 16 + code, goes
+//         into the product as it is, and (16 + zero) * sum of a is taken out afterwards, the sum
+//         of a from a product with ones (it stands in the same registers as the group's sums).
+//         The fp32 sums then hold numbers up to 31 / |code - zero| times larger: still 2^-24 of
+//         them, far below the 2^-9 of a bf16 output.
+#pragma once
+
+#include "grouped.hpp"
+#include "sg_device.hpp"
+
+namespace sg {
+
+struct Int4Params {
+    GroupedParams q;          // g.A, g.lda: activations; g.C, g.ldc; g.N: rows of the weight
+    const int32_t* order;     // nullptr: row r of C is row r of A
+    int top_k, T;             // row of A: order[r] / top_k, of T
+    const uint8_t* codes;
+    const uint16_t* scales;
+    const uint8_t* zeros;     // nullptr: 8
+    int64_t s_codes, s_scales;   // codes' bytes and scales' elements of one expert
+    int tiles_k, tiles_g;     // tiles along K of codes (128) and of scales (4 groups)
+    int swiglu, c_f32;
+};
+
+inline int64_t int4_tiles_k(int64_t K) { return (K + 127) / 128; }
+inline int64_t int4_tiles_g(int64_t K, int64_t group) {
+    return ((K + group - 1) / group + 3) / 4;
+}
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4_a2 __attribute__((ext_vector_type(4), aligned(2)));
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma_16x16x32(const u32x4& a, const u32x4& b, const f32x4& c) {
+    if constexpr (DT == DT_F16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                      __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                       __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Eight codes as an operand: fp16: code - zero, with zero packed twice as 1024 + zero; bf16: 16 +
+// code.
+template <int DT>
+__device__ __forceinline__ u32x4 int4_operand(uint32_t w, uint32_t zero2) {
+    u32x4 o;
+    if constexpr (DT == DT_F16) {
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint32_t v = (w >> (4 * p) & 0x000F000Fu) | 0x64006400u;
+            o[p] = __builtin_bit_cast(
+                uint32_t, __builtin_bit_cast(f16x2, v) - __builtin_bit_cast(f16x2, zero2));
+        }
+    } else {
+        o[0] = (w << 3 & 0x00780078u) | 0x41804180u;
+#pragma unroll
+        for (int p = 1; p < 4; ++p) o[p] = (w >> (4 * p - 3) & 0x00780078u) | 0x41804180u;
+    }
+    return o;
+}
+
+// Eight activations from column k on of a row of K; zeros behind it, nothing read there.
+__device__ __forceinline__ u32x4 int4_act(const uint16_t* row, int k, int K) {
+    if (k + 8 <= K) return *reinterpret_cast<const u32x4_a2*>(row + k);
+    u32x4 v = {0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (k + i < K) v[i / 2] |= (uint32_t)row[k + i] << (16 * (i % 2));
+    return v;
+}
+
+// One work-group: 16 MT rows x 16 NT columns of the product; its waves take every NW-th tile of
+// 128 along K and their sums meet in LDS, in the order of the waves.
+template <int DT, int GROUP, int MT, int NT, int NW>
+__global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
+    constexpr int BM = 16 * MT, BN = 16 * NT, STEPS = GROUP / 32, PER = 128 / GROUP;
+    __shared__ float part[NW][BM * BN];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const GroupedParams& q = x.q;
+    GroupItem it;
+    if (!find_rows<BM>(q, blockIdx.x, lane, it)) return;
+    const int N = q.g.N, K = q.g.K, n0 = it.tn * BN, lr = lane & 15, lq = lane >> 4;
+    const uint16_t* row[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        // rows past the expert's last one: that one again, their sums are not stored
+        int r = it.row0 + min(it.m0 + 16 * i + lr, it.rows - 1);
+        if (x.order) r = min(max(x.order[r] / x.top_k, 0), x.T - 1);
+        row[i] = q.g.A + (int64_t)r * q.g.lda;
+    }
+    const int tn0 = it.tn * NT, tiles_n = (N + 15) / 16;
+    const u32x4* codes[NT];
+    const uint16_t* scales[NT];
+    const uint8_t* zeros[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int tn = min(tn0 + j, tiles_n - 1);
+        codes[j] = reinterpret_cast<const u32x4*>(x.codes + it.e * x.s_codes +
+                                                  (int64_t)tn * x.tiles_k * 1024) + lane;
+        const int64_t at = it.e * x.s_scales + (int64_t)tn * x.tiles_g * 64 + 4 * lr;
+        scales[j] = x.scales + at;
+        zeros[j] = x.zeros ? x.zeros + at : nullptr;
+    }
+    f32x4 sum[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) sum[i][j] = f32x4{0, 0, 0, 0};
+    const uint32_t one = 0x3F803F80u;
+    for (int kt = wave; kt * 128 < K; kt += NW) {
+        u32x4 w[NT], a[MT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) w[j] = codes[j][kt * 64];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int s = 0; s < 4; ++s) a[i][s] = int4_act(row[i], kt * 128 + 32 * s + 8 * lq, K);
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            const int g = kt * PER + p, gat = g / 4 * 64 + g % 4;
+            if (kt * 128 + p * GROUP >= K) break;
+            f32x4 asum[MT];
+            if constexpr (DT == DT_BF16) {
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    asum[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s)
+                        asum[i] = mfma_16x16x32<DT>(a[i][p * STEPS + s], u32x4{one, one, one, one},
+                                                    asum[i]);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const float f = to_f32<DT>(scales[j][gat]);
+                const int z = zeros[j] ? zeros[j][gat] : 8;
+                uint32_t zero2 = 0;
+                if constexpr (DT == DT_F16) {
+                    const uint32_t h = from_f32<DT_F16>((float)(1024 + z));
+                    zero2 = h | h << 16;
+                }
+                f32x4 acc[MT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    const u32x4 b = int4_operand<DT>(w[j][p * STEPS + s], zero2);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        acc[i] = mfma_16x16x32<DT>(a[i][p * STEPS + s], b, acc[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        float v = acc[i][r];
+                        if constexpr (DT == DT_BF16)
+                            v = __builtin_fmaf((float)(-16 - z), asum[i][r], v);
+                        sum[i][j][r] = __builtin_fmaf(f, v, sum[i][j][r]);
+                    }
+            }
+        }
+    }
+    // D[m][n]: lane 16 q + r holds rows 4 q .. 4 q + 3 of column r
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                part[wave][(16 * i + 4 * lq + r) * BN + 16 * j + lr] = sum[i][j][r];
+    __syncthreads();
+    for (int o = 2 * threadIdx.x; o < BM * BN; o += 128 * NW) {
+        float u = 0.0f, v = 0.0f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            u += part[w][o];
+            v += part[w][o + 1];
+        }
+        const int m = it.m0 + o / BN, n = n0 + o % BN;
+        if (m >= it.rows || n >= N) continue;
+        const int64_t r = (int64_t)(it.row0 + m) * q.g.ldc;
+        if (x.swiglu) {
+            reinterpret_cast<uint16_t*>(q.g.C)[r + n / 2] = from_f32<DT>(silu(u) * v);
+        } else if (x.c_f32) {
+            float* c = reinterpret_cast<float*>(q.g.C) + r + n;
+            c[0] = q.g.alpha * u;
+            if (n + 1 < N) c[1] = q.g.alpha * v;
+        } else {
+            uint16_t* c = reinterpret_cast<uint16_t*>(q.g.C) + r + n;
+            c[0] = from_f32<DT>(q.g.alpha * u);
+            if (n + 1 < N) c[1] = from_f32<DT>(q.g.alpha * v);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Quantisation, packing and the way back.  One thread a row's group of columns.
+// ---------------------------------------------------------------------------
+struct Int4PackParams {
+    const void* W;              // quantise
+    const uint8_t *src, *src_zeros;    // pack
+    const uint16_t* src_scales;
+    int64_t ldw, sW;            // elements
+    int N, K, group, scale_bf16;
+    uint8_t* codes;
+    uint16_t* scales;
+    uint8_t* zeros;
+    void* out;                  // dequantise
+    int64_t s_codes, s_scales;
+    int tiles_k, tiles_g;
+};
+
+__device__ __forceinline__ int64_t int4_scale_at(const Int4PackParams& p, int r, int g) {
+    return ((int64_t)(r / 16) * p.tiles_g + g / 4) * 64 + 4 * (r % 16) + g % 4;
+}
+// The 4 bytes that hold columns c .. c + 7 of row r (c a multiple of 8).
+__device__ __forceinline__ int64_t int4_code_at(const Int4PackParams& p, int r, int c) {
+    return ((int64_t)(r / 16) * p.tiles_k + c / 128) * 1024 + 16 * (16 * (c % 32 / 8) + r % 16) +
+           4 * (c % 128 / 32);
+}
+
+template <int DT>
+__device__ __forceinline__ float int4_load(const void* p, int64_t i) {
+    if constexpr (DT == DT_F32) return reinterpret_cast<const float*>(p)[i];
+    else return to_f32<DT>(reinterpret_cast<const uint16_t*>(p)[i]);
+}
+
+// Rows and groups past the matrix, up to whole tiles, get zeros: g counts groups of whole tiles
+// of scales and of codes.
+template <int DT, bool PACK>
+__global__ void __launch_bounds__(256) int4_pack_kernel(const Int4PackParams q) {
+    Int4PackParams p = q;
+    const int64_t b = blockIdx.z;
+    const int rows = (p.N + 15) / 16 * 16;
+    const int code_groups = p.tiles_k * 128 / p.group;
+    const int groups = max(code_groups, p.tiles_g * 4), real = (p.K + p.group - 1) / p.group;
+    uint8_t* codes = p.codes + b * p.s_codes;
+    uint16_t* scales = p.scales + b * p.s_scales;
+    uint8_t* zeros = p.zeros ? p.zeros + b * p.s_scales : nullptr;
+    const int64_t work = (int64_t)rows * groups;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < work;
+         i += (int64_t)gridDim.x * 256) {
+        const int r = (int)(i / groups), g = (int)(i % groups);
+        const int k0 = g * p.group, k1 = r < p.N ? min(p.K, k0 + p.group) : 0;
+        uint16_t scale = 0;
+        int zero = 8;
+        float s = 0.0f;
+        int64_t at = 0;
+        if (k0 < k1) {
+            if constexpr (PACK) {
+                at = (b * p.N + r) * (int64_t)p.K;
+                const int64_t sat = (b * p.N + r) * (int64_t)real + g;
+                scale = p.src_scales[sat];
+                if (p.src_zeros) zero = p.src_zeros[sat];
+            } else {
+                at = b * p.sW + (int64_t)r * p.ldw;
+                float lo = 0.0f, hi = 0.0f;
+                bool bad = false;
+                for (int k = k0; k < k1; ++k) {
+                    const float v = int4_load<DT>(p.W, at + k);
+                    bad |= !(__builtin_fabsf(v) < __builtin_huge_valf());
+                    lo = fminf(lo, v);
+                    hi = fmaxf(hi, v);
+                }
+                s = zeros ? (hi - lo) / 15.0f : fmaxf(hi, -lo) / 7.0f;
+                scale = p.scale_bf16 ? from_f32<DT_BF16>(s) : from_f32<DT_F16>(s);
+                s = p.scale_bf16 ? to_f32<DT_BF16>(scale) : to_f32<DT_F16>(scale);
+                if (bad || !(s < __builtin_huge_valf())) {
+                    scale = p.scale_bf16 ? 0x7FC0 : 0x7E00;
+                    s = 0.0f;
+                }
+                if (zeros && s > 0.0f)
+                    zero = (int)fmin(fmax(rint(-(double)lo / (double)s), 0.0), 15.0);
+            }
+        }
+        if (g < p.tiles_g * 4) {
+            const int64_t sat = int4_scale_at(p, r, g);
+            scales[sat] = scale;
+            if (zeros) zeros[sat] = (uint8_t)(k0 < k1 ? zero : 0);
+        }
+        if (g >= code_groups) continue;
+        for (int c = k0; c < k0 + p.group; c += 8) {
+            uint32_t w = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (c + e >= k1) continue;
+                uint32_t code;
+                if constexpr (PACK) {
+                    code = p.src[at + c + e] & 15;
+                } else {
+                    const double v = (double)int4_load<DT>(p.W, at + c + e);
+                    code = s > 0.0f ? (uint32_t)fmin(fmax(rint(v / (double)s) + zero, 0.0), 15.0)
+                                    : 8u;
+                }
+                w |= code << (4 * (e / 2 + 4 * (e % 2)));
+            }
+            *reinterpret_cast<uint32_t*>(codes + int4_code_at(p, r, c)) = w;
+        }
+    }
+}
+
+// One thread eight columns of a row.
+template <int DT>
+__global__ void __launch_bounds__(256) int4_dequantize_kernel(const Int4PackParams p) {
+    const int64_t b = blockIdx.z;
+    const int pieces = (p.K + 7) / 8;
+    const int64_t work = (int64_t)p.N * pieces;
+    const uint8_t* codes = p.codes + b * p.s_codes;
+    const uint16_t* scales = p.scales + b * p.s_scales;
+    const uint8_t* zeros = p.zeros ? p.zeros + b * p.s_scales : nullptr;
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < work;
+         i += (int64_t)gridDim.x * 256) {
+        const int r = (int)(i / pieces), c = (int)(i % pieces) * 8;
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(codes + int4_code_at(p, r, c));
+        const int64_t sat = int4_scale_at(p, r, c / p.group);
+        const float s = p.scale_bf16 ? to_f32<DT_BF16>(scales[sat]) : to_f32<DT_F16>(scales[sat]);
+        const int z = zeros ? zeros[sat] : 8;
+        const int64_t at = b * p.sW + (int64_t)r * p.ldw + c;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (c + e >= p.K) continue;
+            const float v = s * (float)((int)(w >> (4 * (e / 2 + 4 * (e % 2))) & 15) - z);
+            if constexpr (DT == DT_F32) reinterpret_cast<float*>(p.out)[at + e] = v;
+            else reinterpret_cast<uint16_t*>(p.out)[at + e] = from_f32<DT>(v);
+        }
+    }
+}
+
+// Launches the product's kernels: mt, nt: 16-row and 16-column tiles of a work-group.
+hipError_t launch_int4(int dt, int group, int mt, int nt, const Int4Params& x, unsigned blocks,
+                       hipStream_t st);
+
+}  // namespace sg
