@@ -152,10 +152,12 @@ int sg_sort_experts(const int32_t* ids, int64_t n, int64_t experts, int32_t* off
     if (!offsets) return -4;
     SortParams p{ids, (int)n, (int)experts, offsets, order, place};
     hipStream_t st = static_cast<hipStream_t>(stream);
-    const dim3 grid((unsigned)experts + 1);
+    // the walk that writes is divided while the work-groups fit the CUs one each
+    const int64_t fit = 256 / (experts + 1), parts = n <= 16384 || fit < 1 ? 1 : fit < 8 ? fit : 8;
+    const dim3 grid((unsigned)experts + 1, (unsigned)parts);
     describe("sort_experts", -2, "");
-    if (n <= 1024) SG_LAUNCH(sort_kernel<4>, grid, dim3(256), st, p);
-    else SG_LAUNCH(sort_kernel<16>, grid, dim3(1024), st, p);
+    if (n <= 1024) SG_LAUNCH((sort_kernel<4, 1>), grid, dim3(256), st, p);
+    else SG_LAUNCH((sort_kernel<16, 4>), grid, dim3(1024), st, p);
     return status_of(hipGetLastError());
 }
 

@@ -277,49 +277,125 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
 // row, and writes the rows and places of its own; the last one does the same for the ids of no
 // expert, which behave as expert `experts`.  Every work-group reads all ids: no second launch, no
 // table between work-groups and no atomics.  Wave w owns one run of the ids, in order, so the
-// ranks are the order of the places.
+// ranks are the order of the places.  Grid y divides the second walk, the one that writes.
 // ---------------------------------------------------------------------------
+typedef int32_t i32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
 struct SortParams {
     const int32_t* ids;
     int n, experts;
     int32_t *offsets, *order, *place;
 };
 
-template <int WAVES>
+// Four ids of a lane of each of DEEP pieces of 256, ids past the end as expert ~0 and those of no
+// expert as expert `none`.  Whole pieces load 16 bytes a lane, all of them before the first is used.
+template <int DEEP>
+__device__ __forceinline__ void sort_load(const SortParams& p, int i, int lane, int last,
+                                          uint32_t none, uint32_t (&v)[DEEP][4]) {
+    const int at = i + 4 * lane;
+    i32x4_any x[DEEP];
+    if (i + 256 * DEEP <= last) {
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d)
+            x[d] = *reinterpret_cast<const i32x4_any*>(p.ids + at + 256 * d);
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[d][j] = min((uint32_t)x[d][j], none);
+        return;
+    }
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+        const int32_t* ids = p.ids + at + 256 * d;
+        if (i + 256 * (d + 1) <= last) {
+            x[d] = *reinterpret_cast<const i32x4_any*>(ids);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[d][j] = at + 256 * d + j < last ? ids[j] : 0;
+        }
+    }
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            v[d][j] = at + 256 * d + j < last ? min((uint32_t)x[d][j], none) : ~0u;
+}
+
+// A wave takes DEEP pieces of 256 ids at a time, so that as many loads are under way.
+template <int WAVES, int DEEP>
 __global__ void __launch_bounds__(64 * WAVES) sort_kernel(const SortParams p) {
     __shared__ int below[WAVES], equal[WAVES];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const uint32_t e = blockIdx.x, none = p.experts;
-    const int run = ((p.n + WAVES - 1) / WAVES + 63) / 64 * 64;
-    const int first = min((int64_t)p.n, (int64_t)wave * run), last = min(p.n - first, run) + first;
-    int lt = 0, eq = 0;
-    for (int i = first; i < last; i += 64) {
-        const bool in = i + lane < last;
-        const uint32_t v = in ? min((uint32_t)p.ids[i + lane], none) : ~0u;
-        lt += __popcll(__ballot(v < e));
-        eq += __popcll(__ballot(v == e));
+    const int64_t run = ((int64_t)p.n + WAVES * 256 - 1) / (WAVES * 256) * 256;
+    const int first = (int)min((int64_t)p.n, wave * run), last = (int)min((int64_t)p.n, first + run);
+    // this work-group's part of the run, in whole steps
+    constexpr int STEP = 256 * DEEP;
+    const int steps = (last - first + STEP - 1) / STEP, parts = gridDim.y;
+    const int begin = first + (int)((int64_t)steps * blockIdx.y / parts) * STEP;
+    const int end = min(last, first + (int)((int64_t)steps * (blockIdx.y + 1) / parts) * STEP);
+    // counts of each lane: two vector instructions an id and count, where a ballot and its bits
+    // counted keep the scalar unit busy (65536 ids of 64 experts: 20.9 us)
+    int lt = 0, eq = 0, ahead = 0;
+    for (int i = first; i < last; i += STEP) {
+        uint32_t v[DEEP][4];
+        if (i == begin) ahead = eq;
+        sort_load<DEEP>(p, i, lane, last, none, v);
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                lt += v[d][j] < e;
+                eq += v[d][j] == e;
+            }
     }
+    lt = __builtin_amdgcn_readlane(lane_scan(lt), 63);
+    eq = __builtin_amdgcn_readlane(lane_scan(eq), 63);
+    ahead = __builtin_amdgcn_readlane(lane_scan(ahead), 63);
     if (lane == 0) {
         below[wave] = lt;
         equal[wave] = eq;
     }
     __syncthreads();
     int at = 0;
+#pragma unroll
     for (int w = 0; w < WAVES; ++w) {
         at += below[w];
         if (w < wave) at += equal[w];
     }
-    if (threadIdx.x == 0) p.offsets[e] = at;
-    for (int i = first; i < last; i += 64) {
-        const bool in = i + lane < last;
-        const uint32_t v = in ? min((uint32_t)p.ids[i + lane], none) : ~0u;
-        const uint64_t m = __ballot(v == e);
-        if (v == e) {
-            const int r = at + __popcll(m & (((uint64_t)1 << lane) - 1));
-            if (p.order) p.order[r] = e < none ? i + lane : -1;
-            if (p.place) p.place[i + lane] = e < none ? r : -1;
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
+        int row = 0;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) row += below[w];
+        p.offsets[e] = row;
+    }
+    if (eq == 0) return;
+    at = __builtin_amdgcn_readfirstlane(at + ahead);
+    const uint64_t before = ((uint64_t)1 << lane) - 1;
+    for (int i = begin; i < end; i += STEP) {
+        uint32_t v[DEEP][4];
+        sort_load<DEEP>(p, i, lane, last, none, v);
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+            uint64_t m[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) m[j] = __ballot(v[d][j] == e);
+            if ((m[0] | m[1] | m[2] | m[3]) == 0) continue;
+            int r = at;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                r += __popcll(m[j] & before);
+                at += __popcll(m[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (v[d][j] == e) {
+                    const int place = i + 256 * d + 4 * lane + j;
+                    if (p.order) p.order[r] = e < none ? place : -1;
+                    if (p.place) p.place[place] = e < none ? r : -1;
+                    ++r;
+                }
         }
-        at += __popcll(m);
     }
 }
 
@@ -340,30 +416,58 @@ struct RowsParams {
 typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
-// Eight elements from column c of a row of D, fp32; zeros behind the row.
+// Eight elements from column c of a row of D, as loaded; zeros behind the row.
 template <int DT>
-__device__ __forceinline__ void load8(const char* row, int c, int D, float (&v)[8]) {
-    if (c + 8 <= D) {
-        if constexpr (DT == DT_F32) {
-            const f32x4 a = *reinterpret_cast<const f32x4_any*>(row + (int64_t)c * 4);
-            const f32x4 b = *reinterpret_cast<const f32x4_any*>(row + (int64_t)c * 4 + 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = a[i];
-                v[4 + i] = b[i];
-            }
+struct Raw8 {
+    u32x4 a;
+    __device__ __forceinline__ void load(const char* row, int c, int D) {
+        if (c + 8 <= D) {
+            a = *reinterpret_cast<const u32x4_any*>(row + (int64_t)c * 2);
         } else {
-            const u32x4 a = *reinterpret_cast<const u32x4_any*>(row + (int64_t)c * 2);
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[i] = (c + 2 * i < D ? p[2 * i] : 0u) |
+                       (c + 2 * i + 1 < D ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = to_f32<DT>((uint16_t)a[i]);
+            v[2 * i + 1] = to_f32<DT>((uint16_t)(a[i] >> 16));
+        }
+    }
+};
+template <>
+struct Raw8<DT_F32> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const char* row, int c, int D) {
+        const float* p = reinterpret_cast<const float*>(row) + c;
+        if (c + 8 <= D) {
+            a = *reinterpret_cast<const f32x4_any*>(p);
+            b = *reinterpret_cast<const f32x4_any*>(p + 4);
+        } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                v[2 * i] = to_f32<DT>((uint16_t)a[i]);
-                v[2 * i + 1] = to_f32<DT>((uint16_t)(a[i] >> 16));
+                a[i] = c + i < D ? p[i] : 0.0f;
+                b[i] = c + 4 + i < D ? p[4 + i] : 0.0f;
             }
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < D ? load_elem<DT>(row, c + i) : 0.0f;
     }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    }
+};
+template <int DT>
+__device__ __forceinline__ void load8(const char* row, int c, int D, float (&v)[8]) {
+    Raw8<DT> raw;
+    raw.load(row, c, D);
+    raw.get(v);
 }
 template <int DT>
 __device__ __forceinline__ void store8(char* row, int c, int D, const float (&v)[8]) {
@@ -414,6 +518,7 @@ __global__ void __launch_bounds__(256) spread_kernel(const RowsParams p) {
     }
 }
 
+// Rows are loaded four places at a time, so that their latencies overlap.
 template <int DT>
 __global__ void __launch_bounds__(256) combine_kernel(const RowsParams p) {
     constexpr int ESZ = DT == DT_F32 ? 4 : 2;
@@ -421,20 +526,34 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowsParams p) {
     const int64_t t = (int64_t)blockIdx.x * per + threadIdx.x / p.lanes;
     if (t >= p.T) return;
     const int32_t* place = p.place + t * p.top_k;
+    const float* weights = p.weights + t * p.top_k;
+    const char* Z = reinterpret_cast<const char*>(p.Z);
     for (int64_t c = 8 * ((int64_t)blockIdx.y * p.lanes + lx); c < p.D;
          c += 8 * (int64_t)gridDim.y * p.lanes) {
         float acc[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
         if (p.R) load8<DT>(reinterpret_cast<const char*>(p.R) + t * p.ldr * ESZ, (int)c, p.D, acc);
-        for (int j = 0; j < p.top_k; ++j) {
-            const uint32_t r = place[j];
-            if (r >= (uint32_t)p.M) continue;
-            float v[8];
-            load8<DT>(reinterpret_cast<const char*>(p.Z) + (int64_t)r * p.ldz * ESZ, (int)c, p.D, v);
-            const float w = p.weights ? p.weights[t * p.top_k + j] : 1.0f;
+        for (int j = 0; j < p.top_k; j += 4) {
+            uint32_t r[4];
+            float w[4];
+            Raw8<DT> raw[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(w, v[i], acc[i]);
+            for (int i = 0; i < 4; ++i) {
+                r[i] = j + i < p.top_k ? (uint32_t)place[j + i] : ~0u;
+                w[i] = p.weights && j + i < p.top_k ? weights[j + i] : 1.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r[i] < (uint32_t)p.M) raw[i].load(Z + (int64_t)r[i] * p.ldz * ESZ, (int)c, p.D);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (r[i] < (uint32_t)p.M) {
+                    float v[8];
+                    raw[i].get(v);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) acc[k] = __builtin_fmaf(w[i], v[k], acc[k]);
+                }
         }
         store8<DT>(reinterpret_cast<char*>(p.Y) + t * p.ldy * ESZ, (int)c, p.D, acc);
     }
