@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "abi_checks.hpp"
 #include "int4.hpp"
@@ -15,6 +16,16 @@ namespace {
 
 bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128; }
 bool half_type(int dtype) { return dtype == SG_F16 || dtype == SG_BF16; }
+
+int choose(const GroupedParams& q) {
+    if (const char* s = std::getenv("SG_FORCE_INT4")) {
+        const int c = std::atoi(s);
+        if (*s && c >= 0 && c < kNumInt4Cfg) return c;
+    }
+    const int64_t runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
+    if (mean > 16) return 9;
+    return runs * cdiv(q.g.N, 64) >= 512 ? 2 : runs * cdiv(q.g.N, 32) >= 512 ? 1 : 0;
+}
 
 int run_product(const char* what, int64_t experts, const int32_t* offsets, const int32_t* order,
                 int64_t top_k, int64_t T, int64_t M, int64_t N, int64_t K, int64_t group,
@@ -38,16 +49,20 @@ int run_product(const char* what, int64_t experts, const int32_t* offsets, const
     x.s_scales = SG_INT4_SCALES(N, K, group);
     x.tiles_k = (int)int4_tiles_k(K);
     x.tiles_g = (int)int4_tiles_g(K, group);
-    const int64_t mean = M / (experts < M ? experts : M);
-    const int mt = mean > 16 ? 2 : 1;
-    const int nt = mt == 1 && cdiv(N, 64) * experts < 512 ? cdiv(N, 32) * experts < 512 ? 1 : 2 : 4;
+    const int cfg = choose(x.q);
+    const int mt = kInt4Cfg[cfg].MT, nt = kInt4Cfg[cfg].NT;
     x.q.g.tiles_n = (int)cdiv(N, 16 * nt);
     const int64_t tiles_m = offsets ? most_row_tiles(M, experts, 16 * mt) : cdiv(M, 16 * mt);
     const int64_t blocks = tiles_m * x.q.g.tiles_n;
     if (blocks > kMaxBlocks) return status_of(hipErrorInvalidConfiguration);
-    describe(what, -2, "");
-    return status_of(launch_int4(dtype == SG_F16 ? DT_F16 : DT_BF16, (int)group, mt, nt, x,
-                                 (unsigned)blocks, static_cast<hipStream_t>(stream)));
+    describe(what, cfg, kInt4Cfg[cfg].name);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const unsigned b = (unsigned)blocks;
+    const int g = (int)group;
+    return status_of(dtype == SG_F16 ? zeros ? launch_int4<DT_F16, true>(g, cfg, x, b, st)
+                                             : launch_int4<DT_F16, false>(g, cfg, x, b, st)
+                     : zeros         ? launch_int4<DT_BF16, true>(g, cfg, x, b, st)
+                                     : launch_int4<DT_BF16, false>(g, cfg, x, b, st));
 }
 
 void launch_pack(const Int4PackParams& p, bool pack, int dtype, unsigned batch, hipStream_t st) {

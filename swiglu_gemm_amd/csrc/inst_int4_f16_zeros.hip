@@ -1,0 +1,5 @@
+#include "launch_int4.hpp"
+
+namespace sg {
+template hipError_t launch_int4<DT_F16, true>(int, int, const Int4Params&, unsigned, hipStream_t);
+}

@@ -82,17 +82,127 @@ __device__ __forceinline__ u32x4 int4_act(const uint16_t* row, int k, int K) {
     return v;
 }
 
+// One tile of 16 x 128 codes with its scales and zeros (PER groups of a row side by side).
+template <int GROUP, bool ZEROS>
+struct Int4Tile {
+    static constexpr int PER = 128 / GROUP;
+    u32x4 w;
+    uint16_t f[PER];
+    uint8_t z[PER];
+};
+// The addresses of a strip of 16 columns.
+struct Int4Strip {
+    const uint8_t *codes, *zeros;
+    const uint16_t* scales;
+};
+template <int GROUP, bool ZEROS>
+__device__ __forceinline__ void int4_load(Int4Tile<GROUP, ZEROS>& t, const Int4Strip& s, int lane,
+                                          int kt) {
+    constexpr int PER = 128 / GROUP;
+    const int g = kt * PER, at = g / 4 * 64 + g % 4 + 4 * (lane & 15);
+    t.w = *reinterpret_cast<const u32x4*>(s.codes + (int64_t)kt * 1024 + 16 * lane);
+    __builtin_memcpy(t.f, __builtin_assume_aligned(s.scales + at, 2 * PER), 2 * PER);
+    if constexpr (ZEROS) __builtin_memcpy(t.z, __builtin_assume_aligned(s.zeros + at, PER), PER);
+}
+
+// The activations of 16 MT rows and 128 columns from tile kt on.
+template <int MT, bool TAIL>
+__device__ __forceinline__ void int4_rows(u32x4 (&a)[MT][4], const uint16_t* const (&row)[MT],
+                                          int lane, int kt, int K) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int k = kt * 128 + 32 * s + 8 * (lane >> 4);
+            a[i][s] = TAIL ? int4_act(row[i], k, K)
+                           : *reinterpret_cast<const u32x4_a2*>(row[i] + k);
+        }
+}
+
+// bf16: the sums of the activations over each group, in every column of a 16 x 16 tile.
+template <int DT, int GROUP, int MT>
+__device__ __forceinline__ void int4_row_sums(f32x4 (&asum)[MT][128 / GROUP],
+                                              const u32x4 (&a)[MT][4]) {
+    if constexpr (DT == DT_BF16) {
+        constexpr int STEPS = GROUP / 32;
+        const uint32_t one = 0x3F803F80u;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int p = 0; p < 128 / GROUP; ++p) {
+                asum[i][p] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s)
+                    asum[i][p] = mfma_16x16x32<DT>(a[i][p * STEPS + s], u32x4{one, one, one, one},
+                                                   asum[i][p]);
+            }
+    }
+}
+
+// Adds the products of the activations with one tile of codes.
+template <int DT, int GROUP, bool ZEROS, int MT>
+__device__ __forceinline__ void int4_add(f32x4 (&sum)[MT], const u32x4 (&a)[MT][4],
+                                         const f32x4 (&asum)[MT][128 / GROUP],
+                                         const Int4Tile<GROUP, ZEROS>& t) {
+    constexpr int STEPS = GROUP / 32;
+#pragma unroll
+    for (int p = 0; p < 128 / GROUP; ++p) {
+        const float f = to_f32<DT>(t.f[p]);
+        const float z = ZEROS ? (float)t.z[p] : 8.0f;
+        uint32_t zero2 = 0;
+        if constexpr (DT == DT_F16) {
+            const uint32_t h = from_f32<DT_F16>(1024.0f + z);
+            zero2 = h | h << 16;
+        }
+        f32x4 acc[MT];
+#pragma unroll
+        for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const u32x4 b = int4_operand<DT>(t.w[p * STEPS + s], zero2);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                acc[i] = mfma_16x16x32<DT>(a[i][p * STEPS + s], b, acc[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                float v = acc[i][r];
+                if constexpr (DT == DT_BF16) v = __builtin_fmaf(-16.0f - z, asum[i][p][r], v);
+                sum[i][r] = __builtin_fmaf(f, v, sum[i][r]);
+            }
+    }
+}
+
 // One work-group: 16 MT rows x 16 NT columns of the product; its waves take every NW-th tile of
-// 128 along K and their sums meet in LDS, in the order of the waves.
-template <int DT, int GROUP, int MT, int NT, int NW>
+// 128 along K and their sums meet in LDS, in the order of the waves.  A wave keeps a tile of codes
+// of each of its NT strips, and the activations of a tile, under way while it works on the one
+// before.
+template <int DT, int GROUP, bool ZEROS, int MT, int NT, int NW>
 __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
-    constexpr int BM = 16 * MT, BN = 16 * NT, STEPS = GROUP / 32, PER = 128 / GROUP;
+    constexpr int BM = 16 * MT, BN = 16 * NT, PER = 128 / GROUP;
     __shared__ float part[NW][BM * BN];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const GroupedParams& q = x.q;
     GroupItem it;
     if (!find_rows<BM>(q, blockIdx.x, lane, it)) return;
     const int N = q.g.N, K = q.g.K, n0 = it.tn * BN, lr = lane & 15, lq = lane >> 4;
+    Int4Strip strip[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        const int tn = min(it.tn * NT + j, (N + 15) / 16 - 1);
+        const int64_t at = it.e * x.s_scales + (int64_t)tn * x.tiles_g * 64;
+        strip[j].codes = x.codes + it.e * x.s_codes + (int64_t)tn * x.tiles_k * 1024;
+        strip[j].scales = x.scales + at;
+        strip[j].zeros = x.zeros + at;
+    }
+    const int full = K / 128;
+    int kt = wave;
+    Int4Tile<GROUP, ZEROS> t[NT];
+    if (kt < full)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) int4_load(t[j], strip[j], lane, kt);
     const uint16_t* row[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -101,77 +211,44 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
         if (x.order) r = min(max(x.order[r] / x.top_k, 0), x.T - 1);
         row[i] = q.g.A + (int64_t)r * q.g.lda;
     }
-    const int tn0 = it.tn * NT, tiles_n = (N + 15) / 16;
-    const u32x4* codes[NT];
-    const uint16_t* scales[NT];
-    const uint8_t* zeros[NT];
+    f32x4 sum[NT][MT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j) {
-        const int tn = min(tn0 + j, tiles_n - 1);
-        codes[j] = reinterpret_cast<const u32x4*>(x.codes + it.e * x.s_codes +
-                                                  (int64_t)tn * x.tiles_k * 1024) + lane;
-        const int64_t at = it.e * x.s_scales + (int64_t)tn * x.tiles_g * 64 + 4 * lr;
-        scales[j] = x.scales + at;
-        zeros[j] = x.zeros ? x.zeros + at : nullptr;
-    }
-    f32x4 sum[MT][NT];
+    for (int j = 0; j < NT; ++j)
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) sum[i][j] = f32x4{0, 0, 0, 0};
-    const uint32_t one = 0x3F803F80u;
-    for (int kt = wave; kt * 128 < K; kt += NW) {
-        u32x4 w[NT], a[MT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) w[j] = codes[j][kt * 64];
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int s = 0; s < 4; ++s) a[i][s] = int4_act(row[i], kt * 128 + 32 * s + 8 * lq, K);
-#pragma unroll
-        for (int p = 0; p < PER; ++p) {
-            const int g = kt * PER + p, gat = g / 4 * 64 + g % 4;
-            if (kt * 128 + p * GROUP >= K) break;
-            f32x4 asum[MT];
-            if constexpr (DT == DT_BF16) {
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    asum[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int s = 0; s < STEPS; ++s)
-                        asum[i] = mfma_16x16x32<DT>(a[i][p * STEPS + s], u32x4{one, one, one, one},
-                                                    asum[i]);
-                }
-            }
+        for (int i = 0; i < MT; ++i) sum[j][i] = f32x4{0, 0, 0, 0};
+    u32x4 a[MT][4];
+    f32x4 asum[MT][PER];
+    if (kt < full) {
+        int4_rows<MT, false>(a, row, lane, kt, K);
+        for (; kt + NW < full; kt += NW) {
+            u32x4 next[MT][4];
+            int4_rows<MT, false>(next, row, lane, kt + NW, K);
+            int4_row_sums<DT, GROUP, MT>(asum, a);
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                const float f = to_f32<DT>(scales[j][gat]);
-                const int z = zeros[j] ? zeros[j][gat] : 8;
-                uint32_t zero2 = 0;
-                if constexpr (DT == DT_F16) {
-                    const uint32_t h = from_f32<DT_F16>((float)(1024 + z));
-                    zero2 = h | h << 16;
-                }
-                f32x4 acc[MT];
-#pragma unroll
-                for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    const u32x4 b = int4_operand<DT>(w[j][p * STEPS + s], zero2);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-                        acc[i] = mfma_16x16x32<DT>(a[i][p * STEPS + s], b, acc[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float v = acc[i][r];
-                        if constexpr (DT == DT_BF16)
-                            v = __builtin_fmaf((float)(-16 - z), asum[i][r], v);
-                        sum[i][j][r] = __builtin_fmaf(f, v, sum[i][j][r]);
-                    }
+                int4_add<DT, GROUP, ZEROS, MT>(sum[j], a, asum, t[j]);
+                int4_load(t[j], strip[j], lane, kt + NW);
             }
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) a[i][s] = next[i][s];
+        }
+        int4_row_sums<DT, GROUP, MT>(asum, a);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) int4_add<DT, GROUP, ZEROS, MT>(sum[j], a, asum, t[j]);
+    }
+    if (K % 128 != 0 && wave == full % NW) {
+        int4_rows<MT, true>(a, row, lane, full, K);
+        int4_row_sums<DT, GROUP, MT>(asum, a);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            int4_load(t[j], strip[j], lane, full);
+            // groups wholly behind K have no scale
+#pragma unroll
+            for (int p = 1; p < PER; ++p)
+                if (full * 128 + p * GROUP >= K) t[j].f[p] = 0;
+            int4_add<DT, GROUP, ZEROS, MT>(sum[j], a, asum, t[j]);
         }
     }
     // D[m][n]: lane 16 q + r holds rows 4 q .. 4 q + 3 of column r
@@ -181,7 +258,7 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int r = 0; r < 4; ++r)
-                part[wave][(16 * i + 4 * lq + r) * BN + 16 * j + lr] = sum[i][j][r];
+                part[wave][(16 * i + 4 * lq + r) * BN + 16 * j + lr] = sum[j][i][r];
     __syncthreads();
     for (int o = 2 * threadIdx.x; o < BM * BN; o += 128 * NW) {
         float u = 0.0f, v = 0.0f;
@@ -233,12 +310,6 @@ __device__ __forceinline__ int64_t int4_code_at(const Int4PackParams& p, int r, 
            4 * (c % 128 / 32);
 }
 
-template <int DT>
-__device__ __forceinline__ float int4_load(const void* p, int64_t i) {
-    if constexpr (DT == DT_F32) return reinterpret_cast<const float*>(p)[i];
-    else return to_f32<DT>(reinterpret_cast<const uint16_t*>(p)[i]);
-}
-
 // Rows and groups past the matrix, up to whole tiles, get zeros: g counts groups of whole tiles
 // of scales and of codes.
 template <int DT, bool PACK>
@@ -271,7 +342,7 @@ __global__ void __launch_bounds__(256) int4_pack_kernel(const Int4PackParams q) 
                 float lo = 0.0f, hi = 0.0f;
                 bool bad = false;
                 for (int k = k0; k < k1; ++k) {
-                    const float v = int4_load<DT>(p.W, at + k);
+                    const float v = load_elem<DT>(p.W, at + k);
                     bad |= !(__builtin_fabsf(v) < __builtin_huge_valf());
                     lo = fminf(lo, v);
                     hi = fmaxf(hi, v);
@@ -302,7 +373,7 @@ __global__ void __launch_bounds__(256) int4_pack_kernel(const Int4PackParams q) 
                 if constexpr (PACK) {
                     code = p.src[at + c + e] & 15;
                 } else {
-                    const double v = (double)int4_load<DT>(p.W, at + c + e);
+                    const double v = (double)load_elem<DT>(p.W, at + c + e);
                     code = s > 0.0f ? (uint32_t)fmin(fmax(rint(v / (double)s) + zero, 0.0), 15.0)
                                     : 8u;
                 }
@@ -340,8 +411,31 @@ __global__ void __launch_bounds__(256) int4_dequantize_kernel(const Int4PackPara
     }
 }
 
-// Launches the product's kernels: mt, nt: 16-row and 16-column tiles of a work-group.
-hipError_t launch_int4(int dt, int group, int mt, int nt, const Int4Params& x, unsigned blocks,
-                       hipStream_t st);
+// Configurations of the product: rows and columns of a work-group in tiles of 16, its waves.
+// Index = configuration id (SG_FORCE_INT4=<id> overrides the choice).
+struct Int4Cfg {
+    int MT, NT, NW;
+    const char* name;
+};
+#define SG_INT4_CONFIGS(X) \
+    X(0, 1, 1, 8)          \
+    X(1, 1, 2, 8)          \
+    X(2, 1, 4, 8)          \
+    X(3, 1, 8, 8)          \
+    X(4, 1, 1, 16)         \
+    X(5, 1, 2, 4)          \
+    X(6, 1, 4, 4)          \
+    X(7, 1, 8, 4)          \
+    X(8, 2, 2, 8)          \
+    X(9, 2, 4, 8)          \
+    X(10, 2, 4, 4)         \
+    X(11, 4, 4, 4)
+#define SG_INT4_ROW(ID, MT, NT, NW) {MT, NT, NW, #MT "x" #NT " " #NW "w"},
+constexpr Int4Cfg kInt4Cfg[] = {SG_INT4_CONFIGS(SG_INT4_ROW)};
+#undef SG_INT4_ROW
+constexpr int kNumInt4Cfg = sizeof(kInt4Cfg) / sizeof(kInt4Cfg[0]);
+
+template <int DT, bool ZEROS>
+hipError_t launch_int4(int group, int cfg, const Int4Params& x, unsigned blocks, hipStream_t st);
 
 }  // namespace sg

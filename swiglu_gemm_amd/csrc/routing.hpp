@@ -25,17 +25,6 @@ struct RouteParams {
     int64_t lddx;
 };
 
-template <int DT>
-__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
-    if constexpr (DT == DT_F32) return reinterpret_cast<const float*>(p)[i];
-    else return to_f32<DT>(reinterpret_cast<const uint16_t*>(p)[i]);
-}
-template <int DT>
-__device__ __forceinline__ void put_elem(void* p, int64_t i, float x) {
-    if constexpr (DT == DT_F32) reinterpret_cast<float*>(p)[i] = x;
-    else reinterpret_cast<uint16_t*>(p)[i] = from_f32<DT>(x);
-}
-
 template <typename T, typename F>
 __device__ __forceinline__ T wave_reduce(T x, F f) {
 #pragma unroll

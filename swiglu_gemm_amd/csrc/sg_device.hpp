@@ -46,6 +46,18 @@ template <> __device__ __forceinline__ uint16_t from_f32<DT_BF16>(float x) {
     return __builtin_bit_cast(uint16_t, (__bf16)x);
 }
 
+// One element of a row of DT_F32, DT_F16 or DT_BF16.
+template <int DT>
+__device__ __forceinline__ float load_elem(const void* p, int64_t i) {
+    if constexpr (DT == DT_F32) return reinterpret_cast<const float*>(p)[i];
+    else return to_f32<DT>(reinterpret_cast<const uint16_t*>(p)[i]);
+}
+template <int DT>
+__device__ __forceinline__ void put_elem(void* p, int64_t i, float x) {
+    if constexpr (DT == DT_F32) reinterpret_cast<float*>(p)[i] = x;
+    else reinterpret_cast<uint16_t*>(p)[i] = from_f32<DT>(x);
+}
+
 // SiLU(x) = x / (1 + e^-x), evaluated as x * rcp(1 + 2^(-x*log2 e)) with the
 // hardware exp2 and reciprocal (about 1 ulp each in fp32, far below the bf16 /
 // fp16 output rounding).  e^-x -> +inf for very negative x gives rcp = 0 and
