@@ -23,8 +23,8 @@ int choose(const GroupedParams& q) {
         if (*s && c >= 0 && c < kNumInt4Cfg) return c;
     }
     const int64_t runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
-    if (mean > 16) return 9;
-    return runs * cdiv(q.g.N, 64) >= 512 ? 2 : runs * cdiv(q.g.N, 32) >= 512 ? 1 : 0;
+    if (mean > 16) return 10;
+    return runs * cdiv(q.g.N, 64) >= 512 ? 3 : runs * cdiv(q.g.N, 32) >= 512 ? 1 : 0;
 }
 
 int run_product(const char* what, int64_t experts, const int32_t* offsets, const int32_t* order,

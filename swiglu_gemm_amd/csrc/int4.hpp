@@ -9,13 +9,15 @@
 // The codes meet the activations unscaled: a group's sum over k of a * (code - zero) is taken in
 // fp32 accumulators, then multiplied by the group's scale and added to the running sum, so
 // neither the weights nor the groups' sums are rounded to 16 bits.
-//   fp16: 0x6400 | code is 1024 + code; subtracting 1024 + zero leaves code - zero exactly.
+//   fp16: 0x6400 | code is 1024 + code; adding -(1024 + zero) leaves code - zero exactly.
 //   bf16: there is no packed bf16 subtraction, so 0x4180 | code << 3, which is 16 + code, goes
 //         into the product as it is, and (16 + zero) * sum of a is taken out afterwards, the sum
 //         of a from a product with ones (it stands in the same registers as the group's sums).
 //         The fp32 sums then hold numbers up to 31 / |code - zero| times larger: still 2^-24 of
 //         them, far below the 2^-9 of a bf16 output.
 #pragma once
+
+#include <type_traits>
 
 #include "grouped.hpp"
 #include "sg_device.hpp"
@@ -52,22 +54,49 @@ __device__ __forceinline__ f32x4 mfma_16x16x32(const u32x4& a, const u32x4& b, c
                                                        __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// Eight codes as an operand: fp16: code - zero, with zero packed twice as 1024 + zero; bf16: 16 +
-// code.
+// x & mask | magic in one instruction: kept in registers, the two constants leave it the one form
+// that takes both.  fp16 has a second mask, for the codes in the upper halves of bytes: 0x6400 |
+// code << 4 is 1024 + 16 code, of which one multiply-add makes code - zero, without a shift.
+struct Int4Magic {
+    uint32_t mask, high, magic;
+};
 template <int DT>
-__device__ __forceinline__ u32x4 int4_operand(uint32_t w, uint32_t zero2) {
+__device__ __forceinline__ Int4Magic int4_magic() {
+    Int4Magic m = {DT == DT_F16 ? 0x000F000Fu : 0x00780078u, 0x00F000F0u,
+                   DT == DT_F16 ? 0x64006400u : 0x41804180u};
+    asm("" : "+v"(m.mask));
+    if constexpr (DT == DT_F16) asm("" : "+v"(m.high));
+    asm("" : "+s"(m.magic));
+    return m;
+}
+
+// The zero point as int4_operand takes it: fp16: -(1024 + zero) and -(64 + zero), both twice, and
+// 2^-4 twice.  All three are exact, and so is code - zero.
+struct Int4Zero {
+    f16x2 low, high, scale;
+};
+__device__ __forceinline__ Int4Zero int4_zero(float z) {
+    const _Float16 l = (_Float16)(-1024.0f - z), h = (_Float16)(-64.0f - z), f = (_Float16)0.0625f;
+    return Int4Zero{{l, l}, {h, h}, {f, f}};
+}
+
+// Eight codes as an operand: fp16: code - zero; bf16: 16 + code.
+template <int DT>
+__device__ __forceinline__ u32x4 int4_operand(uint32_t w, const Int4Zero& z, const Int4Magic& m) {
     u32x4 o;
     if constexpr (DT == DT_F16) {
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            const uint32_t v = (w >> (4 * p) & 0x000F000Fu) | 0x64006400u;
-            o[p] = __builtin_bit_cast(
-                uint32_t, __builtin_bit_cast(f16x2, v) - __builtin_bit_cast(f16x2, zero2));
+        for (int p = 0; p < 4; p += 2) {
+            const uint32_t v = w >> (4 * p);
+            const uint32_t a = (v & m.mask) | m.magic, b = (v & m.high) | m.magic;
+            o[p] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, a) + z.low);
+            o[p + 1] = __builtin_bit_cast(
+                uint32_t, __builtin_elementwise_fma(__builtin_bit_cast(f16x2, b), z.scale, z.high));
         }
     } else {
-        o[0] = (w << 3 & 0x00780078u) | 0x41804180u;
+        o[0] = (w << 3 & m.mask) | m.magic;
 #pragma unroll
-        for (int p = 1; p < 4; ++p) o[p] = (w >> (4 * p - 3) & 0x00780078u) | 0x41804180u;
+        for (int p = 1; p < 4; ++p) o[p] = (w >> (4 * p - 3) & m.mask) | m.magic;
     }
     return o;
 }
@@ -90,19 +119,21 @@ struct Int4Tile {
     uint16_t f[PER];
     uint8_t z[PER];
 };
-// The addresses of a strip of 16 columns.
+// A strip of 16 columns: the same addresses in every lane, so that a load takes its base from
+// scalar registers and only the lane's offset from a vector one.
 struct Int4Strip {
     const uint8_t *codes, *zeros;
     const uint16_t* scales;
 };
 template <int GROUP, bool ZEROS>
-__device__ __forceinline__ void int4_load(Int4Tile<GROUP, ZEROS>& t, const Int4Strip& s, int lane,
-                                          int kt) {
+__device__ __forceinline__ void int4_load(Int4Tile<GROUP, ZEROS>& t, const Int4Strip& s,
+                                          uint32_t lane, int kt) {
     constexpr int PER = 128 / GROUP;
-    const int g = kt * PER, at = g / 4 * 64 + g % 4 + 4 * (lane & 15);
+    const int g = kt * PER, at = g / 4 * 64 + g % 4;
+    const uint32_t l = 4 * (lane & 15);
     t.w = *reinterpret_cast<const u32x4*>(s.codes + (int64_t)kt * 1024 + 16 * lane);
-    __builtin_memcpy(t.f, __builtin_assume_aligned(s.scales + at, 2 * PER), 2 * PER);
-    if constexpr (ZEROS) __builtin_memcpy(t.z, __builtin_assume_aligned(s.zeros + at, PER), PER);
+    __builtin_memcpy(t.f, __builtin_assume_aligned(s.scales + at + l, 2 * PER), 2 * PER);
+    if constexpr (ZEROS) __builtin_memcpy(t.z, __builtin_assume_aligned(s.zeros + at + l, PER), PER);
 }
 
 // The activations of 16 MT rows and 128 columns from tile kt on.
@@ -143,23 +174,21 @@ __device__ __forceinline__ void int4_row_sums(f32x4 (&asum)[MT][128 / GROUP],
 template <int DT, int GROUP, bool ZEROS, int MT>
 __device__ __forceinline__ void int4_add(f32x4 (&sum)[MT], const u32x4 (&a)[MT][4],
                                          const f32x4 (&asum)[MT][128 / GROUP],
-                                         const Int4Tile<GROUP, ZEROS>& t) {
+                                         const Int4Tile<GROUP, ZEROS>& t,
+                                         const Int4Magic& magic) {
     constexpr int STEPS = GROUP / 32;
 #pragma unroll
     for (int p = 0; p < 128 / GROUP; ++p) {
         const float f = to_f32<DT>(t.f[p]);
         const float z = ZEROS ? (float)t.z[p] : 8.0f;
-        uint32_t zero2 = 0;
-        if constexpr (DT == DT_F16) {
-            const uint32_t h = from_f32<DT_F16>(1024.0f + z);
-            zero2 = h | h << 16;
-        }
+        Int4Zero zero{};
+        if constexpr (DT == DT_F16) zero = int4_zero(z);
         f32x4 acc[MT];
 #pragma unroll
         for (int i = 0; i < MT; ++i) acc[i] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
-            const u32x4 b = int4_operand<DT>(t.w[p * STEPS + s], zero2);
+            const u32x4 b = int4_operand<DT>(t.w[p * STEPS + s], zero, magic);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
                 acc[i] = mfma_16x16x32<DT>(a[i][p * STEPS + s], b, acc[i]);
@@ -191,18 +220,19 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
     Int4Strip strip[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-        const int tn = min(it.tn * NT + j, (N + 15) / 16 - 1);
+        const int tn = __builtin_amdgcn_readfirstlane(min(it.tn * NT + j, (N + 15) / 16 - 1));
         const int64_t at = it.e * x.s_scales + (int64_t)tn * x.tiles_g * 64;
         strip[j].codes = x.codes + it.e * x.s_codes + (int64_t)tn * x.tiles_k * 1024;
         strip[j].scales = x.scales + at;
         strip[j].zeros = x.zeros + at;
     }
+    const Int4Magic magic = int4_magic<DT>();
     const int full = K / 128;
     int kt = wave;
-    Int4Tile<GROUP, ZEROS> t[NT];
+    Int4Tile<GROUP, ZEROS> t[2][NT];
     if (kt < full)
 #pragma unroll
-        for (int j = 0; j < NT; ++j) int4_load(t[j], strip[j], lane, kt);
+        for (int j = 0; j < NT; ++j) int4_load(t[0][j], strip[j], lane, kt);
     const uint16_t* row[MT];
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -216,39 +246,52 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
     for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int i = 0; i < MT; ++i) sum[j][i] = f32x4{0, 0, 0, 0};
-    u32x4 a[MT][4];
+    u32x4 a[2][MT][4];
     f32x4 asum[MT][PER];
-    if (kt < full) {
-        int4_rows<MT, false>(a, row, lane, kt, K);
-        for (; kt + NW < full; kt += NW) {
-            u32x4 next[MT][4];
-            int4_rows<MT, false>(next, row, lane, kt + NW, K);
-            int4_row_sums<DT, GROUP, MT>(asum, a);
+    // One tile of 128 along K: everything of the next one is loaded first, into registers of its
+    // own.  The barrier keeps the loads there; the compiler would gather them at the end, with
+    // nothing left to cover them.
+    auto step = [&](auto from, auto more) {
+        if constexpr (more) {
+            int4_rows<MT, false>(a[1 - from], row, lane, kt + NW, K);
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                int4_add<DT, GROUP, ZEROS, MT>(sum[j], a, asum, t[j]);
-                int4_load(t[j], strip[j], lane, kt + NW);
-            }
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) a[i][s] = next[i][s];
+            for (int j = 0; j < NT; ++j) int4_load(t[1 - from][j], strip[j], lane, kt + NW);
+            __builtin_amdgcn_sched_barrier(0);
         }
-        int4_row_sums<DT, GROUP, MT>(asum, a);
+        int4_row_sums<DT, GROUP, MT>(asum, a[from]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) int4_add<DT, GROUP, ZEROS, MT>(sum[j], a, asum, t[j]);
+        for (int j = 0; j < NT; ++j)
+            int4_add<DT, GROUP, ZEROS, MT>(sum[j], a[from], asum, t[from][j], magic);
+        kt += NW;
+    };
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
+    constexpr std::true_type more{};
+    constexpr std::false_type last{};
+    if (kt < full) {
+        int4_rows<MT, false>(a[0], row, lane, kt, K);
+        while (kt + 2 * NW < full) {
+            step(even, more);
+            step(odd, more);
+        }
+        if (kt + NW < full) {
+            step(even, more);
+            step(odd, last);
+        } else {
+            step(even, last);
+        }
     }
     if (K % 128 != 0 && wave == full % NW) {
-        int4_rows<MT, true>(a, row, lane, full, K);
-        int4_row_sums<DT, GROUP, MT>(asum, a);
+        int4_rows<MT, true>(a[0], row, lane, full, K);
+        int4_row_sums<DT, GROUP, MT>(asum, a[0]);
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            int4_load(t[j], strip[j], lane, full);
+            int4_load(t[0][j], strip[j], lane, full);
             // groups wholly behind K have no scale
 #pragma unroll
             for (int p = 1; p < PER; ++p)
-                if (full * 128 + p * GROUP >= K) t[j].f[p] = 0;
-            int4_add<DT, GROUP, ZEROS, MT>(sum[j], a, asum, t[j]);
+                if (full * 128 + p * GROUP >= K) t[0][j].f[p] = 0;
+            int4_add<DT, GROUP, ZEROS, MT>(sum[j], a[0], asum, t[0][j], magic);
         }
     }
     // D[m][n]: lane 16 q + r holds rows 4 q .. 4 q + 3 of column r
@@ -411,7 +454,7 @@ __global__ void __launch_bounds__(256) int4_dequantize_kernel(const Int4PackPara
     }
 }
 
-// Configurations of the product: rows and columns of a work-group in tiles of 16, its waves.
+// Configurations of the product: rows and columns of a work-group in tiles of 16, and its waves.
 // Index = configuration id (SG_FORCE_INT4=<id> overrides the choice).
 struct Int4Cfg {
     int MT, NT, NW;
@@ -420,16 +463,16 @@ struct Int4Cfg {
 #define SG_INT4_CONFIGS(X) \
     X(0, 1, 1, 8)          \
     X(1, 1, 2, 8)          \
-    X(2, 1, 4, 8)          \
-    X(3, 1, 8, 8)          \
-    X(4, 1, 1, 16)         \
+    X(2, 1, 3, 8)          \
+    X(3, 1, 4, 8)          \
+    X(4, 1, 6, 8)          \
     X(5, 1, 2, 4)          \
     X(6, 1, 4, 4)          \
-    X(7, 1, 8, 4)          \
-    X(8, 2, 2, 8)          \
-    X(9, 2, 4, 8)          \
+    X(7, 1, 6, 4)          \
+    X(8, 1, 1, 16)          \
+    X(9, 2, 2, 8)          \
     X(10, 2, 4, 4)         \
-    X(11, 4, 4, 4)
+    X(11, 2, 2, 4)
 #define SG_INT4_ROW(ID, MT, NT, NW) {MT, NT, NW, #MT "x" #NT " " #NW "w"},
 constexpr Int4Cfg kInt4Cfg[] = {SG_INT4_CONFIGS(SG_INT4_ROW)};
 #undef SG_INT4_ROW
