@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdlib>
 
 #include "abi_checks.hpp"
@@ -17,14 +18,38 @@ namespace {
 bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128; }
 bool half_type(int dtype) { return dtype == SG_F16 || dtype == SG_BF16; }
 
+// The tiles go by the 16 x 16 columns-by-rows pieces of the product (the rows of each expert are not
+// known here: their mean stands for them, a run of n rows making n / 16 + 1/2 pieces, at least one).
+// Measured with every tile forced (MI355X, bf16, groups of 128, weights cold):
+//   up to 256 pieces, one to a work-group of 8 waves: 1 row, 4096 x 4096: 4.9 us, 5.8 us two by two;
+//   up to 512, two: 32 rows, 4096 x 4096: 8.2 against 11.6 us one by one and 8.7 us by threes;
+//   up to 768, three: 1 row, 11008 x 4096: 7.2 against 7.9 us one by one and 8.2 us by twos;
+//   up to 1024, four to 4 waves: 8 rows, 16384 x 2048: 6.6 against 7.7 us by twos;
+//   up to 4096, six to 4 waves: 16 rows, 22016 x 4096: 14.7 against 18.6 us by fours and 19.0 us by
+//   twos; then four again: 256 rows of 64 experts, 2816 x 2048: 47.0 against 51.2 us by sixes.
+// 64-row tiles take 1 us for each 128 along K while they have a CU each, 0.65 us where they share
+// one; a piece takes a SIMD 0.165 us.  That puts them ahead from about 160 rows of one weight
+// (11008 x 4096: 128 rows 33.2 against 33.8 us, 256 rows 44.8 against 61 us; 4096 x 4096: 256 rows
+// 33.8 against 28.5 us, 512 rows 34.7 against 47.7 us) and 32 rows of each of 64 experts (2816 x
+// 2048: 74.8 against 85.1 us; 16 rows each: 67 against 56 us).
 int choose(const GroupedParams& q) {
     if (const char* s = std::getenv("SG_FORCE_INT4")) {
         const int c = std::atoi(s);
         if (*s && c >= 0 && c < kNumInt4Cfg) return c;
     }
-    const int64_t runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
-    if (mean > 16) return 10;
-    return runs * cdiv(q.g.N, 64) >= 512 ? 3 : runs * cdiv(q.g.N, 32) >= 512 ? 1 : 0;
+    const double runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
+    const double strips = (double)cdiv(q.g.N, 16), tiles_k = (double)cdiv(q.g.K, 128);
+    auto high = [&](int bm) {
+        return q.experts == 1 ? (double)cdiv(q.rows, bm) : runs * std::fmax(1.0, mean / bm + 0.5);
+    };
+    const double pieces = high(16) * strips;
+    const double rounds = std::ceil(high(64) * cdiv(q.g.N, 128) / 256.0);
+    const double many = 2.0 + tiles_k * (rounds > 1.0 ? 0.65 * rounds + 0.05 : 1.0);
+    if (mean > 16.0 && many < 4.0 + 0.165 * tiles_k * pieces / 1024.0) return 5;
+    if (pieces <= 256.0) return 0;
+    if (pieces <= 512.0) return 1;
+    if (pieces <= 768.0) return 2;
+    return pieces <= 1024.0 || pieces > 4096.0 ? 3 : 4;
 }
 
 int run_product(const char* what, int64_t experts, const int32_t* offsets, const int32_t* order,

@@ -111,13 +111,27 @@ __device__ __forceinline__ u32x4 int4_act(const uint16_t* row, int k, int K) {
     return v;
 }
 
-// One tile of 16 x 128 codes with its scales and zeros (PER groups of a row side by side).
+// One tile of 16 x 128 codes with its scales and zeros (PER groups of a row side by side), as
+// loaded.
 template <int GROUP, bool ZEROS>
 struct Int4Tile {
     static constexpr int PER = 128 / GROUP;
     u32x4 w;
-    uint16_t f[PER];
-    uint8_t z[PER];
+    uint32_t f[PER == 4 ? 2 : 1], z;
+
+    template <int DT>
+    __device__ __forceinline__ float scale(int p) const {
+        return to_f32<DT>((uint16_t)(f[p / 2] >> (16 * (p % 2))));
+    }
+    __device__ __forceinline__ float zero(int p) const {
+        return ZEROS ? (float)(z >> (8 * p) & 0xFFu) : 8.0f;
+    }
+    // the tile that holds column K of a row: groups wholly behind it have no scale
+    __device__ __forceinline__ void cut(int columns) {
+#pragma unroll
+        for (int p = 1; p < PER; ++p)
+            if (p * GROUP >= columns) f[p / 2] &= p % 2 ? 0x0000FFFFu : 0u;
+    }
 };
 // A strip of 16 columns: the same addresses in every lane, so that a load takes its base from
 // scalar registers and only the lane's offset from a vector one.
@@ -132,8 +146,22 @@ __device__ __forceinline__ void int4_load(Int4Tile<GROUP, ZEROS>& t, const Int4S
     const int g = kt * PER, at = g / 4 * 64 + g % 4;
     const uint32_t l = 4 * (lane & 15);
     t.w = *reinterpret_cast<const u32x4*>(s.codes + (int64_t)kt * 1024 + 16 * lane);
-    __builtin_memcpy(t.f, __builtin_assume_aligned(s.scales + at + l, 2 * PER), 2 * PER);
-    if constexpr (ZEROS) __builtin_memcpy(t.z, __builtin_assume_aligned(s.zeros + at + l, PER), PER);
+    const uint16_t* f = s.scales + at + l;
+    if constexpr (PER == 4) {
+        const u32x2 v = *reinterpret_cast<const u32x2*>(f);
+        t.f[0] = v.x;
+        t.f[1] = v.y;
+    } else if constexpr (PER == 2) {
+        t.f[0] = *reinterpret_cast<const uint32_t*>(f);
+    } else {
+        t.f[0] = *f;
+    }
+    if constexpr (ZEROS) {
+        const uint8_t* z = s.zeros + at + l;
+        t.z = PER == 4   ? *reinterpret_cast<const uint32_t*>(z)
+              : PER == 2 ? *reinterpret_cast<const uint16_t*>(z)
+                         : *z;
+    }
 }
 
 // The activations of 16 MT rows and 128 columns from tile kt on.
@@ -179,8 +207,7 @@ __device__ __forceinline__ void int4_add(f32x4 (&sum)[MT], const u32x4 (&a)[MT][
     constexpr int STEPS = GROUP / 32;
 #pragma unroll
     for (int p = 0; p < 128 / GROUP; ++p) {
-        const float f = to_f32<DT>(t.f[p]);
-        const float z = ZEROS ? (float)t.z[p] : 8.0f;
+        const float f = t.template scale<DT>(p), z = t.zero(p);
         Int4Zero zero{};
         if constexpr (DT == DT_F16) zero = int4_zero(z);
         f32x4 acc[MT];
@@ -201,6 +228,23 @@ __device__ __forceinline__ void int4_add(f32x4 (&sum)[MT], const u32x4 (&a)[MT][
                 if constexpr (DT == DT_BF16) v = __builtin_fmaf(-16.0f - z, asum[i][p][r], v);
                 sum[i][r] = __builtin_fmaf(f, v, sum[i][r]);
             }
+    }
+}
+
+// Stores columns n (even) and n + 1 of the row that starts `row` elements into C.
+template <int DT>
+__device__ __forceinline__ void int4_put(const Int4Params& x, int64_t row, int n, float u, float v) {
+    const Gemm16Params& g = x.q.g;
+    if (x.swiglu) {
+        reinterpret_cast<uint16_t*>(g.C)[row + n / 2] = from_f32<DT>(silu(u) * v);
+    } else if (x.c_f32) {
+        float* c = reinterpret_cast<float*>(g.C) + row + n;
+        c[0] = g.alpha * u;
+        if (n + 1 < g.N) c[1] = g.alpha * v;
+    } else {
+        uint16_t* c = reinterpret_cast<uint16_t*>(g.C) + row + n;
+        c[0] = from_f32<DT>(g.alpha * u);
+        if (n + 1 < g.N) c[1] = from_f32<DT>(g.alpha * v);
     }
 }
 
@@ -287,10 +331,7 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             int4_load(t[0][j], strip[j], lane, full);
-            // groups wholly behind K have no scale
-#pragma unroll
-            for (int p = 1; p < PER; ++p)
-                if (full * 128 + p * GROUP >= K) t[0][j].f[p] = 0;
+            t[0][j].cut(K - full * 128);
             int4_add<DT, GROUP, ZEROS, MT>(sum[j], a[0], asum, t[0][j], magic);
         }
     }
@@ -313,18 +354,234 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
         const int m = it.m0 + o / BN, n = n0 + o % BN;
         if (m >= it.rows || n >= N) continue;
         const int64_t r = (int64_t)(it.row0 + m) * q.g.ldc;
-        if (x.swiglu) {
-            reinterpret_cast<uint16_t*>(q.g.C)[r + n / 2] = from_f32<DT>(silu(u) * v);
-        } else if (x.c_f32) {
-            float* c = reinterpret_cast<float*>(q.g.C) + r + n;
-            c[0] = q.g.alpha * u;
-            if (n + 1 < N) c[1] = q.g.alpha * v;
-        } else {
-            uint16_t* c = reinterpret_cast<uint16_t*>(q.g.C) + r + n;
-            c[0] = from_f32<DT>(q.g.alpha * u);
-            if (n + 1 < N) c[1] = from_f32<DT>(q.g.alpha * v);
-        }
+        int4_put<DT>(x, r, n, u, v);
     }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows: 64 rows x 128 NP columns a work-group, the columns divided over its four waves, so that
+// each code is loaded and widened once and meets 64 rows, on 32 x 32 x 16 products: their operands
+// keep the vector unit, which widens the codes, from issuing for less time than those of four times
+// as many 16 x 16 x 32 ones.  A wave takes two strips of 16 columns together: lane 32 h + n loads
+// the pieces q = h and q = 2 + h of row n of the two.  The activations pass through LDS, three tiles
+// of 128 along K with one barrier a tile, their 16-byte pieces XOR-swizzled by row.  bf16: the sums
+// of the activations over a group are taken one tile ahead, 16 rows by each wave, and enter the
+// group's products as their initial accumulators; without zero points they are taken times -(16 + 8)
+// at once.
+// ---------------------------------------------------------------------------
+template <int DT, int GROUP, bool ZEROS, int NP>
+__global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
+    constexpr int MT = 2, BM = 64, BN = 128 * NP, PER = 128 / GROUP, STEPS = 2 * GROUP / 32;
+    constexpr bool SUMS = DT == DT_BF16;
+    typedef Int4Tile<GROUP, ZEROS> Tile;
+    __shared__ u32x4 lds[3][BM * 16];
+    __shared__ f32x4 sums[SUMS ? 2 : 1][SUMS ? PER * BM / 4 : 1];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const GroupedParams& q = x.q;
+    GroupItem it;
+    if (!find_rows<BM>(q, blockIdx.x, lane, it)) return;
+    const int N = q.g.N, K = q.g.K, lr = lane & 15, ln = lane & 31, lh = lane >> 5;
+    const int n0 = it.tn * BN + wave * 32 * NP;
+    const uint8_t *codes[NP], *zeros[NP];
+    const uint16_t* scales[NP];
+#pragma unroll
+    for (int j = 0; j < NP; ++j) {
+        const int tn = min(n0 / 16 + 2 * j + (ln >> 4), (N + 15) / 16 - 1);
+        const int64_t at = it.e * x.s_scales + (int64_t)tn * x.tiles_g * 64 + 4 * lr;
+        codes[j] = x.codes + it.e * x.s_codes + (int64_t)tn * x.tiles_k * 1024 + 16 * (16 * lh + lr);
+        scales[j] = x.scales + at;
+        zeros[j] = x.zeros + at;
+    }
+    // this thread's piece of 8 columns in rows srow, srow + 16, srow + 32 and srow + 48
+    const int srow = threadIdx.x >> 4, spiece = threadIdx.x & 15;
+    const uint16_t* row[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        int r = it.row0 + min(it.m0 + 16 * i + srow, it.rows - 1);
+        if (x.order) r = min(max(x.order[r] / x.top_k, 0), x.T - 1);
+        row[i] = q.g.A + (int64_t)r * q.g.lda + 8 * spiece;
+    }
+    const int spot = srow * 16 + (spiece ^ srow);
+    const Int4Magic magic = int4_magic<DT>();
+    f32x16 sum[NP][MT];
+#pragma unroll
+    for (int j = 0; j < NP; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) sum[j][i][r] = 0.0f;
+    u32x4 stage[4];
+    auto load_stage = [&](int kt) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            stage[i] = *reinterpret_cast<const u32x4_a2*>(row[i] + (int64_t)kt * 128);
+    };
+    auto store_stage = [&](u32x4* buf) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) buf[spot + 256 * i] = stage[i];
+    };
+    // w: pieces q = h; more: pieces q = 2 + h
+    Tile t[2][NP];
+    u32x4 more[2][NP];
+    auto load_codes = [&](Tile(&tile)[NP], u32x4(&second)[NP], int kt) {
+#pragma unroll
+        for (int j = 0; j < NP; ++j) {
+            const Int4Strip s = {codes[j], zeros[j], scales[j]};
+            int4_load(tile[j], s, 0, kt);
+            second[j] = *reinterpret_cast<const u32x4*>(codes[j] + (int64_t)kt * 1024 + 512);
+        }
+    };
+    // The group sums of this wave's 16 rows.
+    auto add_up = [&](f32x4* to, const u32x4* buf) {
+        const uint32_t c = ZEROS ? 0x3F803F80u : 0xC1C0C1C0u;     // 1, or -24, twice
+#pragma unroll
+        for (int p = 0; p < PER; ++p) {
+            f32x4 d = {0, 0, 0, 0};
+#pragma unroll
+            for (int s = p * GROUP / 32; s < (p + 1) * GROUP / 32; ++s)
+                d = mfma_16x16x32<DT>(buf[(16 * wave + lr) * 16 + ((4 * s + (lane >> 4)) ^ lr)],
+                                      u32x4{c, c, c, c}, d);
+            if (lr == 0) to[p * (BM / 4) + 4 * wave + (lane >> 4)] = d;
+        }
+    };
+    // Eight steps of 16 along K.  While a step's products run, the next one's activations are read
+    // and its codes widened; the barriers between steps keep the compiler from reading all of them
+    // at once, which spills.
+    auto compute = [&](const u32x4* buf, const f32x4* group_sums, const Tile(&tile)[NP],
+                       const u32x4(&second)[NP]) {
+        f32x16 acc[NP][MT];
+        u32x4 a[2][MT], b[2][NP];
+        auto ready = [&](auto uc) {
+            constexpr int u = uc, s = u / 2, p = u / STEPS;
+            const int piece = (4 * s + 2 * (u % 2) + lh) ^ lr;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) a[u % 2][i] = buf[(32 * i + ln) * 16 + piece];
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                Int4Zero zero{};
+                if constexpr (DT == DT_F16) zero = int4_zero(tile[j].zero(p));
+                b[u % 2][j] =
+                    int4_operand<DT>(u % 2 ? second[j][s] : tile[j].w[s], zero, magic);
+            }
+        };
+        auto eighth = [&](auto uc) {
+            constexpr int u = uc, p = u / STEPS;
+            if constexpr (u % STEPS == 0)
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    const float off = -16.0f - tile[j].zero(p);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+                            f32x4 d = {0, 0, 0, 0};
+                            if constexpr (SUMS) d = group_sums[p * (BM / 4) + 8 * i + 2 * g + lh];
+#pragma unroll
+                            for (int r = 0; r < 4; ++r)
+                                acc[j][i][4 * g + r] = SUMS && ZEROS ? off * d[r] : d[r];
+                        }
+                }
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    acc[j][i] = mfma16<DT>(a[u % 2][i], b[u % 2][j], acc[j][i]);
+            if constexpr (u < 7) ready(std::integral_constant<int, u + 1>{});
+            if constexpr (u % STEPS == STEPS - 1)
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    const float f = tile[j].template scale<DT>(p);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+                        for (int r = 0; r < 16; ++r)
+                            sum[j][i][r] = __builtin_fmaf(f, acc[j][i][r], sum[j][i][r]);
+                        // here, not a tile later with both tiles' accumulators alive
+                        asm volatile("" : "+v"(sum[j][i]));
+                    }
+                }
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        ready(std::integral_constant<int, 0>{});
+        eighth(std::integral_constant<int, 0>{});
+        eighth(std::integral_constant<int, 1>{});
+        eighth(std::integral_constant<int, 2>{});
+        eighth(std::integral_constant<int, 3>{});
+        eighth(std::integral_constant<int, 4>{});
+        eighth(std::integral_constant<int, 5>{});
+        eighth(std::integral_constant<int, 6>{});
+        eighth(std::integral_constant<int, 7>{});
+    };
+    // Step kt computes on buffer kt % 3 while the sums of tile kt + 1, whose activations are in LDS,
+    // are taken.  At its end the codes of tile kt + 2 take the registers of tile kt's, tile kt + 2 of
+    // the activations goes to LDS, and its registers get tile kt + 3.  Tiles past the last whole one
+    // are that one again: a load behind a branch would make the compiler wait for all of them.  A
+    // partial tile comes last, by itself.
+    const int full = K / 128, last = full - 1;
+    int cur = 0;
+    auto after = [](int i) { return i == 2 ? 0 : i + 1; };
+    auto step = [&](auto from, int kt) {
+        const int next = after(cur), free = after(next);
+        compute(lds[cur], sums[SUMS ? from : 0], t[from], more[from]);
+        if constexpr (SUMS) add_up(sums[1 - from], lds[next]);
+        load_codes(t[from], more[from], min(kt + 2, last));
+        store_stage(lds[free]);
+        load_stage(min(kt + 3, last));
+        __syncthreads();
+        cur = next;
+    };
+    if (full > 0) {
+        load_stage(0);
+        load_codes(t[0], more[0], 0);
+        store_stage(lds[0]);
+        load_stage(min(1, last));
+        load_codes(t[1], more[1], min(1, last));
+        store_stage(lds[1]);
+        load_stage(min(2, last));
+        __syncthreads();
+        if constexpr (SUMS) {
+            add_up(sums[0], lds[0]);
+            __syncthreads();
+        }
+        int kt = 0;
+        for (; kt + 1 < full; kt += 2) {
+            step(std::integral_constant<int, 0>{}, kt);
+            step(std::integral_constant<int, 1>{}, kt + 1);
+        }
+        if (kt < full) step(std::integral_constant<int, 0>{}, kt);
+    }
+    if (K % 128 != 0) {
+        load_codes(t[0], more[0], full);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            stage[i] = int4_act(row[i] - 8 * spiece, full * 128 + 8 * spiece, K);
+#pragma unroll
+        for (int j = 0; j < NP; ++j) t[0][j].cut(K - full * 128);
+        // the last whole step ended with a barrier
+        store_stage(lds[0]);
+        __syncthreads();
+        if constexpr (SUMS) {
+            add_up(sums[0], lds[0]);
+            __syncthreads();
+        }
+        compute(lds[0], sums[0], t[0], more[0]);
+    }
+    // lane 32 h + n holds rows 8 g + 4 h .. + 3 of column n of each 32 x 32 tile; even columns and
+    // the ones behind them meet in the even lanes
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NP; ++j)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float u = sum[j][i][r];
+                const float v = __builtin_bit_cast(
+                    float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, u), 0xB1, 0xf, 0xf, true));
+                const int m = it.m0 + 32 * i + 8 * (r / 4) + 4 * lh + r % 4;
+                const int n = n0 + 32 * j + ln;
+                if ((ln & 1) || m >= it.rows || n >= N) continue;
+                int4_put<DT>(x, (int64_t)(it.row0 + m) * q.g.ldc, n, u, v);
+            }
 }
 
 // ---------------------------------------------------------------------------
@@ -460,21 +717,15 @@ struct Int4Cfg {
     int MT, NT, NW;
     const char* name;
 };
-#define SG_INT4_CONFIGS(X) \
-    X(0, 1, 1, 8)          \
-    X(1, 1, 2, 8)          \
-    X(2, 1, 3, 8)          \
-    X(3, 1, 4, 8)          \
-    X(4, 1, 6, 8)          \
-    X(5, 1, 2, 4)          \
-    X(6, 1, 4, 4)          \
-    X(7, 1, 6, 4)          \
-    X(8, 1, 1, 16)          \
-    X(9, 2, 2, 8)          \
-    X(10, 2, 4, 4)         \
-    X(11, 2, 2, 4)
+#define SG_INT4_FEW(X) \
+    X(0, 1, 1, 8)      \
+    X(1, 1, 2, 8)      \
+    X(2, 1, 3, 8)      \
+    X(3, 1, 4, 4)      \
+    X(4, 1, 6, 4)
+#define SG_INT4_MANY(X) X(5, 4, 8, 4)
 #define SG_INT4_ROW(ID, MT, NT, NW) {MT, NT, NW, #MT "x" #NT " " #NW "w"},
-constexpr Int4Cfg kInt4Cfg[] = {SG_INT4_CONFIGS(SG_INT4_ROW)};
+constexpr Int4Cfg kInt4Cfg[] = {SG_INT4_FEW(SG_INT4_ROW) SG_INT4_MANY(SG_INT4_ROW)};
 #undef SG_INT4_ROW
 constexpr int kNumInt4Cfg = sizeof(kInt4Cfg) / sizeof(kInt4Cfg[0]);
 
