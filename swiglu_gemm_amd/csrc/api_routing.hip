@@ -14,27 +14,54 @@ namespace {
 #define SG_LAUNCH(KERNEL, GRID, BLOCK, ST, P) hipLaunchKernelGGL((KERNEL), GRID, BLOCK, 0, ST, P)
 
 template <int DT>
-void launch_route(bool bwd, const RouteParams& p, hipStream_t st) {
+void launch_route(const RouteParams& p, hipStream_t st) {
+    const dim3 block(256);
+    auto waves = [&](int64_t tokens) { return dim3((unsigned)cdiv(p.T, 4 * tokens)); };
+    if (p.E <= 256 && p.top_k <= 8) {
+#define SG_ROUTE_LANES(L, V)                                                     \
+    if (p.E <= L * V) {                                                          \
+        SG_LAUNCH((route_lanes_kernel<DT, L, V>), waves(64 / L), block, st, p);  \
+        return;                                                                  \
+    }
+        SG_ROUTE_LANES(1, 8)
+        SG_ROUTE_LANES(2, 8)
+        SG_ROUTE_LANES(4, 8)
+        SG_ROUTE_LANES(8, 8)
+        SG_ROUTE_LANES(16, 8)
+        SG_ROUTE_LANES(16, 16)
+#undef SG_ROUTE_LANES
+    }
+#define SG_ROUTE(NV)                                                     \
+    if (p.E <= 64 * NV) {                                                \
+        SG_LAUNCH((route_kernel<DT, NV>), waves(1), block, st, p);       \
+        return;                                                          \
+    }
+    SG_ROUTE(1)
+    SG_ROUTE(4)
+    SG_ROUTE(16)
+#undef SG_ROUTE
+}
+
+template <int DT>
+void launch_route_bwd(const RouteParams& p, hipStream_t st) {
     const dim3 grid((unsigned)cdiv(p.T, 4)), block(256);
-#define SG_ROUTE(NV)                                                            \
-    if (p.E <= 64 * NV) {                                                       \
-        if (bwd) SG_LAUNCH((route_bwd_kernel<DT, NV>), grid, block, st, p);     \
-        else SG_LAUNCH((route_kernel<DT, NV>), grid, block, st, p);             \
-        return;                                                                 \
+#define SG_ROUTE(NV)                                                     \
+    if (p.E <= 64 * NV) {                                                \
+        SG_LAUNCH((route_bwd_kernel<DT, NV>), grid, block, st, p);       \
+        return;                                                          \
     }
     SG_ROUTE(1)
     SG_ROUTE(2)
     SG_ROUTE(4)
-    SG_ROUTE(8)
     SG_ROUTE(16)
 #undef SG_ROUTE
 }
 
 int run_route(bool bwd, int dtype, const RouteParams& p, hipStream_t st) {
     describe(bwd ? "route_experts_bwd" : "route_experts", -2, "");
-    if (dtype == SG_F32) launch_route<DT_F32>(bwd, p, st);
-    else if (dtype == SG_F16) launch_route<DT_F16>(bwd, p, st);
-    else launch_route<DT_BF16>(bwd, p, st);
+    if (dtype == SG_F32) bwd ? launch_route_bwd<DT_F32>(p, st) : launch_route<DT_F32>(p, st);
+    else if (dtype == SG_F16) bwd ? launch_route_bwd<DT_F16>(p, st) : launch_route<DT_F16>(p, st);
+    else bwd ? launch_route_bwd<DT_BF16>(p, st) : launch_route<DT_BF16>(p, st);
     return status_of(hipGetLastError());
 }
 

@@ -25,20 +25,115 @@ struct RouteParams {
     int64_t lddx;
 };
 
-template <typename T, typename F>
-__device__ __forceinline__ T wave_reduce(T x, F f) {
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight elements from column c of a row of D, as loaded; zeros behind the row.
+template <int DT>
+struct Raw8 {
+    u32x4 a;
+    __device__ __forceinline__ void load(const char* row, int c, int D) {
+        if (c + 8 <= D) {
+            a = *reinterpret_cast<const u32x4_any*>(row + (int64_t)c * 2);
+        } else {
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) x = f(x, __shfl_xor(x, d));
-    return x;
+            for (int i = 0; i < 4; ++i)
+                a[i] = (c + 2 * i < D ? p[2 * i] : 0u) |
+                       (c + 2 * i + 1 < D ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = to_f32<DT>((uint16_t)a[i]);
+            v[2 * i + 1] = to_f32<DT>((uint16_t)(a[i] >> 16));
+        }
+    }
+};
+template <>
+struct Raw8<DT_F32> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const char* row, int c, int D) {
+        const float* p = reinterpret_cast<const float*>(row) + c;
+        if (c + 8 <= D) {
+            a = *reinterpret_cast<const f32x4_any*>(p);
+            b = *reinterpret_cast<const f32x4_any*>(p + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = c + i < D ? p[i] : 0.0f;
+                b[i] = c + 4 + i < D ? p[4 + i] : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    }
+};
+// x moved between lanes by a data-parallel move; lanes without a source (rows left out) get `none`.
+// Every lane of the wave takes part: none of these may stand in an operand that only some evaluate.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t x, uint32_t none) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)none, (int)x, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int moved(int x, int none) {
+    return (int)moved<CTRL, ROWS>((uint32_t)x, (uint32_t)none);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float moved(float x, float none) {
+    return __builtin_bit_cast(float, moved<CTRL, ROWS>(__builtin_bit_cast(uint32_t, x),
+                                                       __builtin_bit_cast(uint32_t, none)));
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double moved(double x, double none) {
+    const u32x2 v = __builtin_bit_cast(u32x2, x), n = __builtin_bit_cast(u32x2, none);
+    return __builtin_bit_cast(
+        double, u32x2{moved<CTRL, ROWS>((uint32_t)v.x, (uint32_t)n.x),
+                      moved<CTRL, ROWS>((uint32_t)v.y, (uint32_t)n.y)});
+}
+__device__ __forceinline__ int from_lane(int x, int lane) {
+    return __builtin_amdgcn_readlane(x, lane);
+}
+__device__ __forceinline__ float from_lane(float x, int lane) {
+    return __builtin_bit_cast(float, from_lane(__builtin_bit_cast(int, x), lane));
+}
+__device__ __forceinline__ double from_lane(double x, int lane) {
+    const u32x2 v = __builtin_bit_cast(u32x2, x);
+    return __builtin_bit_cast(double, u32x2{(uint32_t)from_lane((int)v.x, lane),
+                                            (uint32_t)from_lane((int)v.y, lane)});
+}
+// f over the lanes of a wave, the same in every lane: neighbours, pairs, mirrored halves of a row of
+// 16, then the rows' last lanes to the rows behind.
+template <typename T, typename F>
+__device__ __forceinline__ T wave_reduce(T x, T none, F f) {
+    x = f(x, moved<0xB1, 0xf>(x, none));         // quad_perm 1 0 3 2
+    x = f(x, moved<0x4E, 0xf>(x, none));         // quad_perm 2 3 0 1
+    x = f(x, moved<0x141, 0xf>(x, none));        // row_half_mirror
+    x = f(x, moved<0x140, 0xf>(x, none));        // row_mirror
+    x = f(x, moved<0x142, 0xa>(x, none));        // row_bcast:15
+    x = f(x, moved<0x143, 0xc>(x, none));        // row_bcast:31
+    return from_lane(x, 63);
 }
 __device__ __forceinline__ float wave_sum(float x) {
-    return wave_reduce(x, [](float a, float b) { return a + b; });
+    return wave_reduce(x, 0.0f, [](float a, float b) { return a + b; });
 }
 __device__ __forceinline__ double wave_sum(double x) {
-    return wave_reduce(x, [](double a, double b) { return a + b; });
+    return wave_reduce(x, 0.0, [](double a, double b) { return a + b; });
 }
 __device__ __forceinline__ float wave_max(float x) {
-    return wave_reduce(x, [](float a, float b) { return fmaxf(a, b); });
+    return wave_reduce(x, -__builtin_huge_valf(), [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ double wave_max(double x) {
+    return wave_reduce(x, -__builtin_huge_val(), [](double a, double b) { return fmax(a, b); });
+}
+__device__ __forceinline__ int wave_min(int x) {
+    return wave_reduce(x, 0x7FFFFFFF, [](int a, int b) { return min(a, b); });
 }
 
 // log of a score, up to what renormalising over the chosen cancels
@@ -50,13 +145,29 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-
 constexpr double kNone = -__builtin_huge_val();
 constexpr double kNanKey = -1e300;        // a NaN logit: behind every number
 
-// One wave a token; lane l holds experts l, l + 64, ...
+// Lane j < top_k holds place j of token t: its expert (-1: none) and logit x; top and total: the row's
+// largest logit and the sum of e^(x - top), where softmax is not renormalised.
+__device__ __forceinline__ void route_finish(const RouteParams& p, int t, int lane, int id, float x,
+                                             float top, float total, bool bad) {
+    float w;
+    if (p.renormalize) {
+        const float inf = __builtin_huge_valf(), l = id < 0 ? -inf : log_score(p.scoring, x);
+        const float most = wave_max(l);
+        const float a = id < 0 ? 0.0f : expf(l - most);
+        w = a / wave_sum(a);
+    } else {
+        w = p.scoring == ROUTE_SOFTMAX ? expf(x - top) / total : sigmoid(x);
+    }
+    if (lane < p.top_k) {
+        p.ids[(int64_t)t * p.top_k + lane] = id;
+        p.weights[(int64_t)t * p.top_k + lane] = id < 0 ? 0.0f : bad ? __builtin_nanf("") : p.scale * w;
+    }
+}
+
+// One token by one wave, every comparison in 64 bits; lane l holds experts l, l + 64, ...
+// lds: 64 NV values for this wave.
 template <int DT, int NV>
-__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
-    __shared__ double lds[4][NV * 64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int t = blockIdx.x * 4 + wave;
-    if (t >= p.T) return;
+__device__ __forceinline__ void route_token(const RouteParams& p, int t, int lane, double* lds) {
     int32_t* ids = p.ids + (int64_t)t * p.top_k;
     float* weights = p.weights + (int64_t)t * p.top_k;
     if (p.mask && p.mask[t] == 0) {
@@ -116,7 +227,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
         }
         if (p.groups > 1) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) lds[wave][lane + 64 * i] = c[i];
+            for (int i = 0; i < NV; ++i) lds[lane + 64 * i] = c[i];
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             __builtin_amdgcn_wave_barrier();
             const int per = p.E / p.groups;
@@ -124,7 +235,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
             if (lane < p.groups) {
                 double a = kNone, b = kNone;          // the two best
                 for (int i = 0; i < per; ++i) {
-                    const double v = lds[wave][lane * per + i];
+                    const double v = lds[lane * per + i];
                     b = fmax(b, fmin(a, v));
                     a = fmax(a, v);
                 }
@@ -132,7 +243,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
             }
             int rank = 0;
             for (int g = 0; g < p.groups; ++g) {
-                const double v = __shfl(value, g);
+                const double v = from_lane(value, g);
                 rank += v > value || (v == value && g < lane);
             }
             const uint64_t kept = __ballot(lane < p.groups && rank < p.top_groups);
@@ -155,18 +266,10 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
                 e = lane + 64 * i;
                 v = x[i];
             }
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const double b = __shfl_xor(best, d);
-            const int f = __shfl_xor(e, d);
-            const float w = __shfl_xor(v, d);
-            if (b > best || (b == best && f < e)) {
-                best = b;
-                e = f;
-                v = w;
-            }
-        }
-        if (best == kNone) break;
+        const double most = wave_max(best);
+        if (most == kNone) break;
+        e = wave_min(best == most ? e : 1 << 20);
+        v = from_lane(v, e & 63);
         if (lane == j) {
             id = e;
             mine = v;
@@ -175,23 +278,388 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
         for (int i = 0; i < NV; ++i)
             if (lane + 64 * i == e) key[i] = kNone;
     }
-    float w;
+    float total = 0.0f;
+    if (!p.renormalize && p.scoring == ROUTE_SOFTMAX) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) total += x[i] == -inf ? 0.0f : expf(x[i] - top);
+        total = wave_sum(total);
+    }
+    route_finish(p, t, lane, id, mine, top, total, bad);
+}
+
+template <int DT, int NV>
+__global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
+    __shared__ double lds[4][NV * 64];
+    const int wave = threadIdx.x >> 6;
+    const int t = blockIdx.x * 4 + wave;
+    if (t < p.T) route_token<DT, NV>(p, t, threadIdx.x & 63, lds[wave]);
+}
+
+// ---------------------------------------------------------------------------
+// The usual case, at most 256 experts and 8 choices: L lanes a token (64 / L tokens a wave) hold V
+// neighbouring experts each.  Keys of 32 bits carry the value in front of the inverted index, so
+// the eight largest come out of sorting networks of integer maxima and minima: within a lane, then
+// between lanes, whose sorted lists a and b join as max(a[i], b[7 - i]).
+//   16-bit logits without a bias: the value is the logit itself, in an order of unsigned numbers.
+//   Otherwise 24 bits from the row's largest value down to its smallest (at most 64 below), of
+//   scores in fp32.  Where two values that decide are closer than what they may be off by (of the
+//   scores 2^-20 for sigmoid and 2^-18 for softmax, beside the 24 bits), the few that are in question
+//   are compared in 64 bits, one a lane (0.1 % of tokens with random logits).  Groups that close and
+//   everything unusual (NaN, too few experts left) go through route_token.
+// 16384 tokens, 256 experts in 8 groups, top 8, sigmoid and bias: ROUTE_NOW (one wave a token in 64
+// bits: 53 us).
+// ---------------------------------------------------------------------------
+template <int S>
+__device__ __forceinline__ uint32_t lane_swap(uint32_t x) {
+    constexpr int ctrl = S == 1 ? 0xB1 : S == 2 ? 0x4E : S == 4 ? 0x141 : 0x140;
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)x, ctrl, 0xf, 0xf, true);
+}
+template <int S>
+__device__ __forceinline__ float lane_swap(float x) {
+    return __builtin_bit_cast(float, lane_swap<S>(__builtin_bit_cast(uint32_t, x)));
+}
+// f over the L lanes of a token; every lane gets the result.  (Lanes of a half that S = 4 or 8 mirrors
+// onto hold the same value already.)
+template <int L, typename T, typename F>
+__device__ __forceinline__ T lanes_reduce(T x, F f) {
+    if constexpr (L > 1) x = f(x, lane_swap<1>(x));
+    if constexpr (L > 2) x = f(x, lane_swap<2>(x));
+    if constexpr (L > 4) x = f(x, lane_swap<4>(x));
+    if constexpr (L > 8) x = f(x, lane_swap<8>(x));
+    return x;
+}
+
+__device__ __forceinline__ void order_pair(uint32_t& a, uint32_t& b) {
+    const uint32_t hi = max(a, b);
+    b = min(a, b);
+    a = hi;
+}
+// Eight values, the largest first: Batcher's odd-even merge sort.
+__device__ __forceinline__ void sort8(uint32_t (&v)[8]) {
+    order_pair(v[0], v[1]), order_pair(v[2], v[3]), order_pair(v[4], v[5]), order_pair(v[6], v[7]);
+    order_pair(v[0], v[2]), order_pair(v[1], v[3]), order_pair(v[4], v[6]), order_pair(v[5], v[7]);
+    order_pair(v[1], v[2]), order_pair(v[5], v[6]);
+    order_pair(v[0], v[4]), order_pair(v[1], v[5]), order_pair(v[2], v[6]), order_pair(v[3], v[7]);
+    order_pair(v[2], v[4]), order_pair(v[3], v[5]);
+    order_pair(v[1], v[2]), order_pair(v[3], v[4]), order_pair(v[5], v[6]);
+}
+// The eight largest of two sorted lists (b the other one, its last first): bitonic, then sorted.
+__device__ __forceinline__ void join8(uint32_t (&v)[8], const uint32_t (&b)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = max(v[i], b[i]);
+#pragma unroll
+    for (int d = 4; d > 0; d /= 2)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (!(i & d)) order_pair(v[i], v[i + d]);
+}
+template <int S>
+__device__ __forceinline__ void join_lanes(uint32_t (&v)[8]) {
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) b[i] = lane_swap<S>(v[7 - i]);
+    join8(v, b);
+}
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+// e^d and 1 / (1 + e^-x) from the hardware's exp2 and reciprocal
+__device__ __forceinline__ float fast_exp(float d) {
+    return __builtin_amdgcn_exp2f(d * 1.44269504088896341f);
+}
+
+template <int DT, int L, int V>
+__global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
+    constexpr int TOKENS = 64 / L, NV = L * V > 64 ? L * V / 64 : 1;
+    constexpr int ROW = L * V + 1;                      // odd: tokens' rows start in other banks
+    struct Wave {
+        union {
+            float c[TOKENS * ROW];
+            double exact[NV * 64];
+        };
+        float value[64 * V];
+        uint8_t kept[64 * V];
+        float edge[TOKENS][2];                          // the lowest group kept, the best one not
+        uint16_t list[64];                              // candidates, then the chosen ones
+        double exact_value[64];
+    };
+    __shared__ Wave lds[4];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, li = lane % L, lt = lane / L;
+    Wave& w = lds[wave];
+    const int t0 = (blockIdx.x * 4 + wave) * TOKENS, t = t0 + lt;
+    if (t0 >= p.T) return;
+    const float inf = __builtin_huge_valf();
+    const bool here = t < p.T, live = here && !(p.mask && p.mask[t] == 0);
+    const char* row = reinterpret_cast<const char*>(p.X) +
+                      (int64_t)(here ? t : t0) * p.ldx * (DT == DT_F32 ? 4 : 2);
+    const int e0 = li * V;
+    float x[V];
+    if (live && e0 + V <= p.E) {
+#pragma unroll
+        for (int i = 0; i < V; i += 8) {
+            Raw8<DT> raw;
+            float v[8];
+            raw.load(row, e0 + i, p.E);
+            raw.get(v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[i + j] = v[j];
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) x[i] = live && e0 + i < p.E ? load_elem<DT>(row, e0 + i) : -inf;
+    }
+    float top = -inf;
+    // unusual: for route_token; unsure: the order of a few has to be looked at in 64 bits
+    bool unusual = false, unsure = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        top = fmaxf(top, x[i]);
+        unusual |= x[i] != x[i];
+    }
+    top = lanes_reduce<L>(top, [](float a, float b) { return fmaxf(a, b); });
+    unusual |= p.scoring == ROUTE_SOFTMAX && top == inf;
+    const bool softmax = p.scoring == ROUTE_SOFTMAX, groups = p.groups > 1;
+    // scores, where they decide or are needed for the weights
+    float c[V], total = 0.0f, off = 0.0f;
+    if (softmax && (p.bias || groups || !p.renormalize)) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            c[i] = x[i] == -inf ? 0.0f : fast_exp(x[i] - top);
+            total += c[i];
+        }
+        total = lanes_reduce<L>(total, [](float a, float b) { return a + b; });
+        const float f = __builtin_amdgcn_rcpf(total);
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] *= f;
+        off = 0x1p-18f;
+    } else if (p.bias || groups) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-x[i]));
+        off = 0x1p-20f;
+    }
+    float hi = -inf, lo = inf;
+    if (p.bias || groups) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if (p.bias && e0 + i < p.E) c[i] += p.bias[e0 + i];
+            if (x[i] == -inf || c[i] != c[i]) c[i] = -inf;
+            hi = fmaxf(hi, c[i]);
+            lo = fminf(lo, c[i] == -inf ? inf : c[i]);
+        }
+        hi = lanes_reduce<L>(hi, [](float a, float b) { return fmaxf(a, b); });
+        lo = lanes_reduce<L>(lo, [](float a, float b) { return fminf(a, b); });
+        off += 0x1p-23f * fmaxf(fabsf(hi), fabsf(lo));
+    }
+    bool in[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) in[i] = p.bias ? c[i] != -inf : x[i] != -inf;
+    if (groups) {
+        const int per = p.E / p.groups, work = TOKENS * p.groups;
+#pragma unroll
+        for (int i = 0; i < V; ++i) w.c[lt * ROW + e0 + i] = c[i];
+        wave_sync();
+        // one lane a token's group: its best two; each starts elsewhere, for the banks
+        for (int k = lane; k < work; k += 64) {
+            const int tt = k / p.groups, g = k - tt * p.groups;
+            const float* from = w.c + tt * ROW + g * per;
+            float a = -inf, b = -inf;
+            for (int i = 0, j = g % per; i < per; ++i) {
+                const float v = from[j];
+                b = fmaxf(b, fminf(a, v));
+                a = fmaxf(a, v);
+                j = j + 1 == per ? 0 : j + 1;
+            }
+            w.value[k] = p.group_top == 2 && b != -inf ? a + b : a;
+        }
+        wave_sync();
+        for (int k = lane; k < work; k += 64) {
+            const int tt = k / p.groups, g = k - tt * p.groups;
+            const float v = w.value[k];
+            int rank = 0;
+            for (int h = 0; h < p.groups; ++h) {
+                const float o = w.value[tt * p.groups + h];
+                rank += o > v || (o == v && h < g);
+            }
+            w.kept[k] = rank < p.top_groups;
+            if (rank == p.top_groups - 1) w.edge[tt][0] = v;
+            if (rank == p.top_groups) w.edge[tt][1] = v;
+        }
+        wave_sync();
+        // a sum of two is off by twice what a score is, and so is the other
+        unusual |= w.edge[lt][0] - w.edge[lt][1] <= 5.0f * off;
+        int g = e0 / per, r = e0 - g * per;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            in[i] = in[i] && g < p.groups && w.kept[lt * p.groups + min(g, p.groups - 1)];
+            if (++r == per) {
+                r = 0;
+                ++g;
+            }
+        }
+    }
+    // keys
+    const bool whole = DT != DT_F32 && !p.bias;          // a 16-bit logit whole
+    uint32_t key[V], band = 0;
+    if (whole) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            uint32_t h = __builtin_bit_cast(uint32_t, x[i]);
+            if constexpr (DT == DT_F16) h = (uint32_t)from_f32<DT_F16>(x[i]) << 16;
+            if (h == 0x80000000u) h = 0;                 // -0 is 0
+            h = (h ^ (h >> 31 ? 0xFFFF0000u : 0x80000000u)) & 0xFFFF0000u;
+            key[i] = in[i] ? h | (0xFFFFu - (e0 + i)) : 0;
+        }
+    } else {
+        if (!p.bias) {
+            hi = top;
+            lo = inf;
+#pragma unroll
+            for (int i = 0; i < V; ++i) lo = fminf(lo, x[i] == -inf ? inf : x[i]);
+            lo = lanes_reduce<L>(lo, [](float a, float b) { return fminf(a, b); });
+            off = 0.0f;
+        }
+        lo = fmaxf(lo, hi - 64.0f);
+        const float scale = hi > lo ? 16770000.0f / (hi - lo) : 0.0f;
+        // both ends of a difference: twice what a value is off by, and the steps lost in rounding
+        const float wide = 8.0f + 2.0f * off * scale;
+        unusual |= !(wide < 4000.0f);
+        band = (uint32_t)fminf(wide, 4000.0f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float d = fmaxf((p.bias ? c[i] : x[i]) - lo, 0.0f);
+            key[i] = in[i] ? (4096u + (uint32_t)fminf(d * scale, 16770000.0f)) << 8 | (255u - (e0 + i)) : 0;
+        }
+    }
+    uint32_t best[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) best[i] = key[i];
+    sort8(best);
+    if constexpr (V == 16) {
+        uint32_t more[8], back[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) more[i] = key[8 + i];
+        sort8(more);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) back[i] = more[7 - i];
+        join8(best, back);
+    }
+    if constexpr (L > 1) join_lanes<1>(best);
+    if constexpr (L > 2) join_lanes<2>(best);
+    if constexpr (L > 4) join_lanes<4>(best);
+    if constexpr (L > 8) join_lanes<8>(best);
+    // the last one chosen, and how far behind it the next key is
+    uint32_t end = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (j == p.top_k - 1) end = best[j];
+    unusual |= end == 0;
+    if (!whole) {
+        uint32_t gap = ~0u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) gap = min(gap, end - 1 - key[i]);
+        gap = lanes_reduce<L>(gap, [](uint32_t a, uint32_t b) { return min(a, b); });
+        unsure |= gap >> 8 <= band + 1;
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+            if (j + 1 < p.top_k) unsure |= (best[j] >> 8) - (best[j + 1] >> 8) <= band;
+    }
+    const uint64_t mine = ((uint64_t)1 << L) - 1;         // the lanes of the token at bit 0
+    const uint64_t fully = __ballot(unusual && live), closely = __ballot(unsure && live);
+    const bool redo = ((fully | closely) >> (lt * L) & mine) != 0;
+    // weights: lane li has places li, li + L, ...
+    constexpr int PLACES = L < 8 ? 8 / L : 1;
+    int id[PLACES];
+    float v[PLACES], most = -inf;
+#pragma unroll
+    for (int k = 0; k < PLACES; ++k) {
+        uint32_t kk = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (li + L * k == j && j < p.top_k) kk = best[j];
+        id[k] = kk == 0 ? -1 : (int)(whole ? 0xFFFFu - (kk & 0xFFFFu) : 255u - (kk & 255u));
+        v[k] = id[k] < 0 ? -inf : load_elem<DT>(row, id[k]);
+    }
     if (p.renormalize) {
-        const float l = id < 0 ? -inf : log_score(p.scoring, mine);
-        const float m = wave_max(l);
-        const float a = id < 0 ? 0.0f : expf(l - m);
-        w = a / wave_sum(a);
-    } else if (p.scoring == ROUTE_SOFTMAX) {
+#pragma unroll
+        for (int k = 0; k < PLACES; ++k) {
+            v[k] = id[k] < 0 ? -inf : log_score(p.scoring, v[k]);
+            most = fmaxf(most, v[k]);
+        }
+        most = lanes_reduce<L>(most, [](float a, float b) { return fmaxf(a, b); });
         float sum = 0.0f;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) sum += x[i] == -inf ? 0.0f : expf(x[i] - top);
-        w = expf(mine - top) / wave_sum(sum);
+        for (int k = 0; k < PLACES; ++k) {
+            v[k] = id[k] < 0 ? 0.0f : expf(v[k] - most);
+            sum += v[k];
+        }
+        sum = lanes_reduce<L>(sum, [](float a, float b) { return a + b; });
+#pragma unroll
+        for (int k = 0; k < PLACES; ++k) v[k] /= sum;
     } else {
-        w = sigmoid(mine);
+#pragma unroll
+        for (int k = 0; k < PLACES; ++k) v[k] = softmax ? expf(v[k] - top) / total : sigmoid(v[k]);
     }
-    if (lane < p.top_k) {
-        ids[lane] = id;
-        weights[lane] = id < 0 ? 0.0f : bad ? __builtin_nanf("") : p.scale * w;
+    if (here && !redo)
+#pragma unroll
+        for (int k = 0; k < PLACES; ++k) {
+            const int j = li + L * k;
+            if (j < p.top_k) {
+                p.ids[(int64_t)t * p.top_k + j] = live ? id[k] : -1;
+                p.weights[(int64_t)t * p.top_k + j] = live ? p.scale * v[k] : 0.0f;
+            }
+        }
+    for (uint64_t left = fully | closely; left;) {
+        const int tt = __builtin_ctzll(left) / L;
+        left &= ~(mine << (tt * L));
+        wave_sync();
+        // every key that may belong in front of the last one chosen, one a lane, in 64 bits
+        int n = 64 + 1;
+        if ((fully >> (tt * L) & mine) == 0) {
+            const uint32_t from = (end >> 8) - min(end >> 8, band + 2);
+            n = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const bool is = lt == tt && key[i] != 0 && key[i] >> 8 >= from;
+                const uint64_t all = __ballot(is);
+                const int at = n + __popcll(all & (((uint64_t)1 << lane) - 1));
+                if (is && at < 64) w.list[at] = (uint16_t)(e0 + i);
+                n += __popcll(all);
+            }
+        }
+        if (n > 64) {
+            route_token<DT, NV>(p, t0 + tt, lane, w.exact);
+            continue;
+        }
+        wave_sync();
+        const char* its = reinterpret_cast<const char*>(p.X) +
+                          (int64_t)(t0 + tt) * p.ldx * (DT == DT_F32 ? 4 : 2);
+        const float its_top = from_lane(top, tt * L), its_total = from_lane(total, tt * L);
+        const int e = lane < n ? w.list[lane] : 0;
+        const float its_x = load_elem<DT>(its, e);
+        double exact = its_x;
+        if (p.bias) {
+            if (softmax) {
+                double sum = 0.0;
+                for (int i = lane; i < p.E; i += 64) sum += exp((double)load_elem<DT>(its, i) - (double)its_top);
+                exact = exp(exact - (double)its_top) / wave_sum(sum);
+            } else {
+                exact = 1.0 / (1.0 + exp(-exact));
+            }
+            exact += (double)p.bias[e];
+        }
+        w.exact_value[lane] = exact;
+        wave_sync();
+        int rank = 0;
+        for (int j = 0; j < n; ++j) {
+            const double o = w.exact_value[j];
+            rank += o > exact || (o == exact && w.list[j] < e);
+        }
+        wave_sync();
+        if (lane < n && rank < p.top_k) w.list[rank] = (uint16_t)e;
+        wave_sync();
+        const int id = lane < p.top_k ? w.list[lane] : -1;
+        route_finish(p, t0 + tt, lane, id, id < 0 ? 0.0f : load_elem<DT>(its, id), its_top, its_total, false);
     }
 }
 
@@ -219,7 +687,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
         if (p.renormalize) {
             const float x = id < 0 ? 0.0f : load_elem<DT>(row, id);
             const float l = id < 0 ? -inf : log_score(p.scoring, x);
-            const float a = id < 0 ? 0.0f : expf(l - wave_max(l));
+            const float most = wave_max(l);
+            const float a = id < 0 ? 0.0f : expf(l - most);
             const float q = a / wave_sum(a);
             v = q * (G - wave_sum(G * q));
             if (p.scoring == ROUTE_SIGMOID) v *= sigmoid(-x);
@@ -230,8 +699,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
             v = G;
         }
         for (int j = 0; j < p.top_k; ++j) {
-            const int e = __shfl(id, j);
-            const float g = __shfl(v, j);
+            const int e = from_lane(id, j);
+            const float g = from_lane(v, j);
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 if (lane + 64 * i == e) d[i] += g;
@@ -402,56 +871,6 @@ struct RowsParams {
     float* dweights;
 };
 
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-
-// Eight elements from column c of a row of D, as loaded; zeros behind the row.
-template <int DT>
-struct Raw8 {
-    u32x4 a;
-    __device__ __forceinline__ void load(const char* row, int c, int D) {
-        if (c + 8 <= D) {
-            a = *reinterpret_cast<const u32x4_any*>(row + (int64_t)c * 2);
-        } else {
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[i] = (c + 2 * i < D ? p[2 * i] : 0u) |
-                       (c + 2 * i + 1 < D ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-        }
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = to_f32<DT>((uint16_t)a[i]);
-            v[2 * i + 1] = to_f32<DT>((uint16_t)(a[i] >> 16));
-        }
-    }
-};
-template <>
-struct Raw8<DT_F32> {
-    f32x4 a, b;
-    __device__ __forceinline__ void load(const char* row, int c, int D) {
-        const float* p = reinterpret_cast<const float*>(row) + c;
-        if (c + 8 <= D) {
-            a = *reinterpret_cast<const f32x4_any*>(p);
-            b = *reinterpret_cast<const f32x4_any*>(p + 4);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = c + i < D ? p[i] : 0.0f;
-                b[i] = c + 4 + i < D ? p[4 + i] : 0.0f;
-            }
-        }
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    }
-};
 template <int DT>
 __device__ __forceinline__ void load8(const char* row, int c, int D, float (&v)[8]) {
     Raw8<DT> raw;

@@ -211,6 +211,22 @@ def test_route_gradient_against_differences(scoring, renormalize):
         assert ((diff - dX[:, e]).abs() <= bound).all(), e
 
 
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+def test_route_of_negative_logits(scoring):
+    """Logits all far below zero: what a lane without a place holds must not pass for a logit."""
+    import swiglu_gemm_amd as sg
+    for T, E, k in ((5, 16, 4), (3, 64, 8), (4, 256, 8), (3, 300, 20)):
+        X, g = logits(T, E, "f32", E)
+        X -= 300.0 if scoring == "softmax" else 60.0
+        dw = torch.randn(T, k, generator=g)
+        for renormalize in (False, True):
+            ids, _ = check_route(X, k, scoring=scoring, renormalize=renormalize)
+            want, tol = ref.route_bwd(X, ids, dw, scoring, renormalize, 1.0)
+            dX = sg.route_experts_bwd(X.cuda(), ids.cuda(), dw.cuda(), torch.empty(T, E, device="cuda:0"),
+                                      scoring=scoring, renormalize=renormalize)
+            check(dX, want, tol)
+
+
 def test_route_backward_of_odd_ids():
     """The same expert twice, ids outside the experts, and a row that no place reads."""
     import swiglu_gemm_amd as sg
