@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
 //   16-bit logits without a bias: the value is the logit itself, in an order of unsigned numbers.
 //   Otherwise 24 bits from the row's largest value down to its smallest (at most 64 below), of
 //   scores in fp32.  Where two values that decide are closer than what they may be off by (of the
-//   scores 2^-20 for sigmoid and 2^-18 for softmax, beside the 24 bits), the few that are in question
+//   scores 2^-21 for sigmoid and 2^-18 of the largest for softmax), the few that are in question
 //   are compared in 64 bits, one a lane (0.1 % of tokens with random logits).  Groups that close and
 //   everything unusual (NaN, too few experts left) go through route_token.
 // 16384 tokens, 256 experts in 8 groups, top 8, sigmoid and bias: ROUTE_NOW (one wave a token in 64
@@ -373,15 +373,17 @@ template <int DT, int L, int V>
 __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
     constexpr int TOKENS = 64 / L, NV = L * V > 64 ? L * V / 64 : 1;
     constexpr int ROW = L * V + 1;                      // odd: tokens' rows start in other banks
+    constexpr int GROUPS = L * V < 64 ? L * V : 64;
     struct Wave {
         union {
             float c[TOKENS * ROW];
             double exact[NV * 64];
         };
-        float value[64 * V];
-        uint8_t kept[64 * V];
+        float value[TOKENS * GROUPS];
+        uint8_t kept[TOKENS * GROUPS];
         float edge[TOKENS][2];                          // the lowest group kept, the best one not
         uint16_t list[64];                              // candidates, then the chosen ones
+        float logit[64];
         double exact_value[64];
     };
     __shared__ Wave lds[4];
@@ -409,6 +411,20 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) x[i] = live && e0 + i < p.E ? load_elem<DT>(row, e0 + i) : -inf;
     }
+    float bias[V];
+    if (p.bias) {
+        if (e0 + V <= p.E) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                const f32x4 b = *reinterpret_cast<const f32x4_any*>(p.bias + e0 + i);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) bias[i + j] = b[j];
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) bias[i] = e0 + i < p.E ? p.bias[e0 + i] : 0.0f;
+        }
+    }
     float top = -inf;
     // unusual: for route_token; unsure: the order of a few has to be looked at in 64 bits
     bool unusual = false, unsure = false;
@@ -432,17 +448,17 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
         const float f = __builtin_amdgcn_rcpf(total);
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] *= f;
-        off = 0x1p-18f;
+        off = 0x1p-23f + 0x1p-18f * f;                  // f: the largest score
     } else if (p.bias || groups) {
 #pragma unroll
         for (int i = 0; i < V; ++i) c[i] = __builtin_amdgcn_rcpf(1.0f + fast_exp(-x[i]));
-        off = 0x1p-20f;
+        off = 0x1p-21f;
     }
     float hi = -inf, lo = inf;
     if (p.bias || groups) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            if (p.bias && e0 + i < p.E) c[i] += p.bias[e0 + i];
+            if (p.bias) c[i] += bias[i];
             if (x[i] == -inf || c[i] != c[i]) c[i] = -inf;
             hi = fmaxf(hi, c[i]);
             lo = fminf(lo, c[i] == -inf ? inf : c[i]);
@@ -455,46 +471,82 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
 #pragma unroll
     for (int i = 0; i < V; ++i) in[i] = p.bias ? c[i] != -inf : x[i] != -inf;
     if (groups) {
-        const int per = p.E / p.groups, work = TOKENS * p.groups;
-#pragma unroll
-        for (int i = 0; i < V; ++i) w.c[lt * ROW + e0 + i] = c[i];
-        wave_sync();
-        // one lane a token's group: its best two; each starts elsewhere, for the banks
-        for (int k = lane; k < work; k += 64) {
-            const int tt = k / p.groups, g = k - tt * p.groups;
-            const float* from = w.c + tt * ROW + g * per;
+        const int per = p.E / p.groups, work = TOKENS * p.groups, wide = per / V;
+        if (per % V == 0 && (wide == 1 || wide == 2 || wide == 4 || wide == 8)) {
+            // a group is 1, 2, 4 or 8 lanes: its best two by data-parallel moves
             float a = -inf, b = -inf;
-            for (int i = 0, j = g % per; i < per; ++i) {
-                const float v = from[j];
-                b = fmaxf(b, fminf(a, v));
-                a = fmaxf(a, v);
-                j = j + 1 == per ? 0 : j + 1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                b = fmaxf(b, fminf(a, c[i]));
+                a = fmaxf(a, c[i]);
             }
-            w.value[k] = p.group_top == 2 && b != -inf ? a + b : a;
-        }
-        wave_sync();
-        for (int k = lane; k < work; k += 64) {
-            const int tt = k / p.groups, g = k - tt * p.groups;
-            const float v = w.value[k];
+            auto with = [&](float a2, float b2) {
+                b = fmaxf(fminf(a, a2), fmaxf(b, b2));
+                a = fmaxf(a, a2);
+            };
+            if (wide > 1) with(lane_swap<1>(a), lane_swap<1>(b));
+            if (wide > 2) with(lane_swap<2>(a), lane_swap<2>(b));
+            if (wide > 4) with(lane_swap<4>(a), lane_swap<4>(b));
+            const float v = p.group_top == 2 && b != -inf ? a + b : a;
+            const int g = li / wide;
+            if (li % wide == 0 && g < p.groups) w.value[lt * p.groups + g] = v;
+            wave_sync();
             int rank = 0;
+#pragma unroll 8
             for (int h = 0; h < p.groups; ++h) {
-                const float o = w.value[tt * p.groups + h];
+                const float o = w.value[lt * p.groups + h];
                 rank += o > v || (o == v && h < g);
             }
-            w.kept[k] = rank < p.top_groups;
-            if (rank == p.top_groups - 1) w.edge[tt][0] = v;
-            if (rank == p.top_groups) w.edge[tt][1] = v;
-        }
-        wave_sync();
-        // a sum of two is off by twice what a score is, and so is the other
-        unusual |= w.edge[lt][0] - w.edge[lt][1] <= 5.0f * off;
-        int g = e0 / per, r = e0 - g * per;
+            const bool is = g < p.groups, keep = is && rank < p.top_groups;
+            const float low = lanes_reduce<L>(keep ? v : inf, [](float a, float b) { return fminf(a, b); });
+            const float high = lanes_reduce<L>(is && !keep ? v : -inf,
+                                               [](float a, float b) { return fmaxf(a, b); });
+            // a sum of two is off by twice what a score is, and so is the other
+            unusual |= low - high <= 5.0f * off;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            in[i] = in[i] && g < p.groups && w.kept[lt * p.groups + min(g, p.groups - 1)];
-            if (++r == per) {
-                r = 0;
-                ++g;
+            for (int i = 0; i < V; ++i) in[i] = in[i] && keep;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) w.c[lt * ROW + e0 + i] = c[i];
+            wave_sync();
+            // one lane a token's group: its best two; each starts elsewhere, for the banks
+            for (int k = lane; k < work; k += 64) {
+                const int tt = k / p.groups, g = k - tt * p.groups;
+                const float* from = w.c + tt * ROW + g * per;
+                float a = -inf, b = -inf;
+#pragma unroll 8
+                for (int i = 0, j = g % per; i < per; ++i) {
+                    const float v = from[j];
+                    b = fmaxf(b, fminf(a, v));
+                    a = fmaxf(a, v);
+                    j = j + 1 == per ? 0 : j + 1;
+                }
+                w.value[k] = p.group_top == 2 && b != -inf ? a + b : a;
+            }
+            wave_sync();
+            for (int k = lane; k < work; k += 64) {
+                const int tt = k / p.groups, g = k - tt * p.groups;
+                const float v = w.value[k];
+                int rank = 0;
+#pragma unroll 4
+                for (int h = 0; h < p.groups; ++h) {
+                    const float o = w.value[tt * p.groups + h];
+                    rank += o > v || (o == v && h < g);
+                }
+                w.kept[k] = rank < p.top_groups;
+                if (rank == p.top_groups - 1) w.edge[tt][0] = v;
+                if (rank == p.top_groups) w.edge[tt][1] = v;
+            }
+            wave_sync();
+            unusual |= w.edge[lt][0] - w.edge[lt][1] <= 5.0f * off;
+            int g = e0 / per, r = e0 - g * per;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                in[i] = in[i] && g < p.groups && w.kept[lt * p.groups + min(g, p.groups - 1)];
+                if (++r == per) {
+                    r = 0;
+                    ++g;
+                }
             }
         }
     }
@@ -521,8 +573,9 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
         }
         lo = fmaxf(lo, hi - 64.0f);
         const float scale = hi > lo ? 16770000.0f / (hi - lo) : 0.0f;
-        // both ends of a difference: twice what a value is off by, and the steps lost in rounding
-        const float wide = 8.0f + 2.0f * off * scale;
+        // The steps from value to key keep the order, so of exact values only equal keys are in
+        // doubt; else both ends of a difference may be off, and the key by a step of rounding each.
+        const float wide = off > 0.0f ? 2.0f + 2.0f * off * scale : 0.0f;
         unusual |= !(wide < 4000.0f);
         band = (uint32_t)fminf(wide, 4000.0f);
 #pragma unroll
@@ -559,7 +612,7 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) gap = min(gap, end - 1 - key[i]);
         gap = lanes_reduce<L>(gap, [](uint32_t a, uint32_t b) { return min(a, b); });
-        unsure |= gap >> 8 <= band + 1;
+        unsure |= gap >> 8 <= band;
 #pragma unroll
         for (int j = 0; j < 7; ++j)
             if (j + 1 < p.top_k) unsure |= (best[j] >> 8) - (best[j + 1] >> 8) <= band;
@@ -651,15 +704,19 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
         w.exact_value[lane] = exact;
         wave_sync();
         int rank = 0;
+#pragma unroll 4
         for (int j = 0; j < n; ++j) {
             const double o = w.exact_value[j];
-            rank += o > exact || (o == exact && w.list[j] < e);
+            rank += (int)(o > exact) | ((int)(o == exact) & (int)(w.list[j] < e));
         }
         wave_sync();
-        if (lane < n && rank < p.top_k) w.list[rank] = (uint16_t)e;
+        if (lane < n && rank < p.top_k) {
+            w.list[rank] = (uint16_t)e;
+            w.logit[rank] = its_x;
+        }
         wave_sync();
         const int id = lane < p.top_k ? w.list[lane] : -1;
-        route_finish(p, t0 + tt, lane, id, id < 0 ? 0.0f : load_elem<DT>(its, id), its_top, its_total, false);
+        route_finish(p, t0 + tt, lane, id, w.logit[lane], its_top, its_total, false);
     }
 }
 
