@@ -280,3 +280,34 @@ def test_no_depth_and_no_rows():
     assert (C == 0).all()
     sg.int4_gemm(torch.empty(0, 128, **dev), codes, scales, torch.empty(0, 16, **dev))
     sg.int4_swiglu_gemm(torch.empty(0, 128, **dev), codes, scales, torch.empty(0, 8, **dev))
+
+
+@pytest.mark.parametrize("cfg", range(6))
+@pytest.mark.parametrize("dtype", sorted(HALF))
+def test_every_tile(dtype, cfg, monkeypatch):
+    """Each tile forced on sizes that end inside it: rows, columns, depth, runs and groups."""
+    import swiglu_gemm_amd as sg
+    monkeypatch.setenv("SG_FORCE_INT4", str(cfg))
+    for M, N, K, group, zeros in ((1, 16, 128, 128, False), (70, 210, 1100, 64, True), (65, 130, 2304, 128, True),
+                                  (16, 98, 4000, 32, False), (3, 34, 40, 32, True)):
+        g = torch.Generator().manual_seed(M + N + K)
+        A = torch.randn(M, K, generator=g).to(HALF[dtype])
+        print("int4 tile %d %s %d x %d x %d" % (cfg, dtype, M, N, K), flush=True)
+        check_product(A, [weight(g, N, K, group, HALF[dtype], zeros)], group)
+        assert "cfg=%d" % cfg in sg.last_config()
+    offsets, M = runs([5, 0, 64, 1, 130, 16], 2, 3)
+    A = torch.randn(M, 200, generator=g).to(HALF[dtype])
+    ws = [weight(g, 150, 200, 64, HALF[dtype], True) for _ in range(6)]
+    check_product(A, ws, 64, offsets)
+
+
+def test_the_choice_of_tiles():
+    """One piece to a work-group, then more columns, then 64-row tiles, as the products grow."""
+    import swiglu_gemm_amd as sg
+    dev = dict(device="cuda:0", dtype=torch.bfloat16)
+    for M, N, want in ((1, 4096, 0), (1, 8192, 1), (1, 11008, 2), (1, 16384, 3), (16, 22016, 4), (1, 70000, 3),
+                       (512, 4096, 5), (32, 1024, 0)):
+        nc, ns = sg.int4_shapes(N, 4096)
+        sg.int4_gemm(torch.zeros(M, 4096, **dev), torch.zeros(nc, device="cuda:0", dtype=U8), torch.zeros(ns, **dev),
+                     torch.empty(M, N, **dev))
+        assert "cfg=%d " % want in sg.last_config(), (M, N, sg.last_config())
