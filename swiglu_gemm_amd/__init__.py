@@ -234,12 +234,16 @@ def _stream(t):
     """Handle (an int) of torch's current HIP stream on t's device.  torch's raw-stream
     query skips building a Stream object (about 2 us a call); older builds without it
     take the public route."""
+    return (_RAW_STREAM or _stream_of)(t.get_device())
+
+
+def _stream_of(device: int):
     global _RAW_STREAM
     if _RAW_STREAM is None:
         import torch
         _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
             (lambda d: torch.cuda.current_stream(d).cuda_stream)
-    return _RAW_STREAM(t.get_device())
+    return _RAW_STREAM(device)
 
 
 def _ld(t) -> int:
@@ -569,23 +573,22 @@ def _launch(what: str, fn, tensors, *args) -> None:
     """Calls the library on the tensors' device and torch's current stream there.  Every tensor
     (None: an argument left out) must be on one GPU; where that is not the current device it is
     made so for the call."""
-    device = -1
+    device = tensors[0].get_device()
     for t in tensors:
-        if t is not None:
-            d = t.get_device()
-            if d < 0:
+        if t is not None and t.get_device() != device:
+            devices = [u.get_device() for u in tensors if u is not None]
+            if min(devices) < 0:
                 raise ValueError("every tensor must be on the GPU")
-            if device < 0:
-                device = d
-            elif d != device:
-                raise ValueError("every tensor must be on one device, got cuda:%d and cuda:%d"
-                                 % (device, d))
-    torch, current = _torch()
+            raise ValueError("every tensor must be on one device, got cuda:%d and cuda:%d"
+                             % (device, t.get_device()))
+    if device < 0:
+        raise ValueError("every tensor must be on the GPU")
+    torch, current = _TORCH or _torch()
     if current() != device:
         with torch.cuda.device(device):
             status = fn(*args, _stream(tensors[0]))
     else:
-        status = fn(*args, _stream(tensors[0]))
+        status = fn(*args, (_RAW_STREAM or _stream_of)(device))
     if status != 0:
         _check(status, what)
 
@@ -922,7 +925,7 @@ def mxfp4_swiglu_gemm(A, As, W, Ws, Y, offsets=None):
 
 # ------------------------------------------------- routing to experts
 def _ints(t, name: str, shape) -> int:
-    if t.dtype is not _torch()[0].int32:
+    if t.dtype is not (_TORCH or _torch())[0].int32:
         raise TypeError("%s must be int32, not %s" % (name, t.dtype))
     if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous of shape %s, not %s" % (name, tuple(shape),
@@ -931,7 +934,7 @@ def _ints(t, name: str, shape) -> int:
 
 
 def _floats(t, name: str, shape) -> int:
-    if t.dtype is not _torch()[0].float32:
+    if t.dtype is not (_TORCH or _torch())[0].float32:
         raise TypeError("%s must be float32, not %s" % (name, t.dtype))
     if t.shape != shape or not t.is_contiguous():
         raise ValueError("%s must be contiguous of shape %s, not %s" % (name, tuple(shape),
@@ -940,10 +943,10 @@ def _floats(t, name: str, shape) -> int:
 
 
 def _row_type(t, name: str) -> int:
-    code = _dtype_code(t)
-    if code == SG_F8E4M3:
-        raise TypeError("%s must be fp32, fp16 or bf16" % name)
-    if len(t.shape) != 2:
+    code = (_TABLES or _tables())[0].get(t.dtype)
+    if code is None or code == SG_F8E4M3:
+        raise TypeError("%s has dtype %s, must be fp32, fp16 or bf16" % (name, t.dtype))
+    if t.dim() != 2:
         raise ValueError("%s must be 2-D" % name)
     return code
 
@@ -966,36 +969,40 @@ def route_experts(X, top_k: int, scoring: str = "softmax", bias=None, groups: in
     where it is False get id -1 and weight 0 and are not read; so do places for which no expert is
     left (a logit of -inf takes one out).  ids, weights: tensors to write."""
     code = _row_type(X, "X")
-    if scoring not in SCORINGS:
+    how = SCORINGS.get(scoring)
+    if how is None:
         raise ValueError("scoring must be one of %s" % ", ".join(SCORINGS))
     T, E = X.shape
-    ldx = _rows(X, "X", E)
-    top_k, groups, top_groups = int(top_k), int(groups), int(top_groups)
-    if not 1 <= top_k <= min(E, 64):
-        raise ValueError("top_k must be 1 to %d, not %d" % (min(E, 64), top_k))
+    ldx = E if X.is_contiguous() and E > 0 else _rows(X, "X", E)
+    if not 1 <= top_k <= 64 or top_k > E:
+        raise ValueError("top_k must be 1 to %d, not %r" % (min(E, 64), top_k))
     if E > 1024:
         raise ValueError("X has %d experts, at most 1024 are supported" % E)
-    if not 1 <= groups <= 64 or E % groups or not 1 <= top_groups <= groups:
+    if groups != 1 and (not 1 <= groups <= 64 or E % groups) or not 1 <= top_groups <= groups:
         raise ValueError("groups (1 to 64) must divide the %d experts, top_groups be 1 to groups" % E)
     if group_top not in (1, 2):
         raise ValueError("group_top must be 1 or 2")
-    bp = None if bias is None else _floats(bias, "bias", (E,))
-    torch = _torch()[0]
-    mp = None
+    torch = (_TORCH or _torch())[0]
+    bp = mp = None
+    if bias is not None:
+        bp = _floats(bias, "bias", (E,))
     if mask is not None:
         if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
             raise TypeError("mask must be bool")
         if mask.shape != (T,) or not mask.is_contiguous():
             raise ValueError("mask must be a contiguous vector of %d tokens" % T)
         mp = mask.data_ptr()
-    if ids is None:
-        ids = X.new_empty((T, top_k), dtype=torch.int32)
     if weights is None:
         weights = X.new_empty((T, top_k), dtype=torch.float32)
-    ip, wp = _ints(ids, "ids", (T, top_k)), _floats(weights, "weights", (T, top_k))
-    _launch("sg_route_experts", lib().sg_route_experts, (ids, X, bias, mask, weights), X.data_ptr(),
-            ldx, T, E, code, top_k, SCORINGS[scoring], bp, groups, top_groups, group_top,
-            int(bool(renormalize)), float(scale), mp, ip, wp)
+    else:
+        _floats(weights, "weights", (T, top_k))
+    if ids is None:
+        ids = torch.empty_like(weights, dtype=torch.int32)
+    else:
+        _ints(ids, "ids", (T, top_k))
+    _launch("sg_route_experts", lib().sg_route_experts, (X, ids, weights, bias, mask), X.data_ptr(),
+            ldx, T, E, code, top_k, how, bp, groups, top_groups, group_top, 1 if renormalize else 0,
+            scale, mp, ids.data_ptr(), weights.data_ptr())
     return ids, weights
 
 
@@ -1031,15 +1038,14 @@ def sort_experts(ids, experts: int):
     int32.  offsets is the table of the grouped products; order[r] is the flat place that is row r,
     place[t, j] the row of place (t, j).  Places of no expert (id -1) come last in order, as -1, and
     have place -1."""
-    torch = _torch()[0]
-    experts = int(experts)
+    torch = (_TORCH or _torch())[0]
     if not 1 <= experts <= 65536:
-        raise ValueError("experts must be 1 to 65536, not %d" % experts)
+        raise ValueError("experts must be 1 to 65536, not %r" % (experts,))
     ip = _ints(ids, "ids", ids.shape)
     n = ids.numel()
-    offsets = ids.new_empty((experts + 1,))
-    order, place = ids.new_empty((n,)), torch.empty_like(ids)
-    _launch("sg_sort_experts", lib().sg_sort_experts, (ids, offsets), ip, n, experts,
+    offsets, order = ids.new_empty(experts + 1), ids.new_empty(n)
+    place = torch.empty_like(ids)
+    _launch("sg_sort_experts", lib().sg_sort_experts, (ids,), ip, n, experts,
             offsets.data_ptr(), order.data_ptr(), place.data_ptr())
     return offsets, order, place
 
@@ -1130,7 +1136,7 @@ def int4_shapes(rows: int, cols: int, group: int = 128):
 def _int4_group(group) -> int:
     if group not in (32, 64, 128):
         raise ValueError("group must be 32, 64 or 128, not %r" % (group,))
-    return int(group)
+    return group
 
 
 def _int4_scale(t, name: str) -> int:
@@ -1142,8 +1148,12 @@ def _int4_scale(t, name: str) -> int:
 
 def _int4_held(codes, scales, zeros, lead, N, K, group) -> None:
     nc, ns = int4_shapes(N, K, group)
-    _mx_bytes(codes, "codes", lead + (nc,))
-    _contig(scales, "scales", lead + (ns,))
+    if codes.dtype is not (_TORCH or _torch())[0].uint8:
+        raise TypeError("codes must be uint8")
+    if codes.shape != lead + (nc,) or not codes.is_contiguous():
+        _contig(codes, "codes", lead + (nc,))
+    if scales.shape != lead + (ns,) or not scales.is_contiguous():
+        _contig(scales, "scales", lead + (ns,))
     if zeros is not None:
         _mx_bytes(zeros, "zeros", lead + (ns,))
 
@@ -1219,24 +1229,23 @@ def int4_dequantize(codes, scales, W, zeros=None, group: int = 128):
 
 def _int4_product(A, codes, scales, zeros, group, offsets, order, top_k, out, rows_of_w):
     """Checks of a product: the arguments up to K in the library's order."""
-    code = _dtype_code(A)
-    if code not in (SG_F16, SG_BF16):
+    dtype = A.dtype
+    code = (_TABLES or _tables())[0].get(dtype)
+    if code != SG_BF16 and code != SG_F16:
         raise TypeError("A must be fp16 or bf16")
-    if scales.dtype != A.dtype:
-        raise TypeError("scales have dtype %s, expected A's %s" % (scales.dtype, A.dtype))
-    if len(A.shape) != 2 or len(out.shape) != 2:
+    if scales.dtype is not dtype:
+        raise TypeError("scales have dtype %s, expected A's %s" % (scales.dtype, dtype))
+    if A.dim() != 2 or out.dim() != 2:
         raise ValueError("A and the output must be 2-D")
-    group = _int4_group(group)
     T, K = A.shape
     M = out.shape[0]
     E, op, lead = 1, None, ()
     if offsets is not None:
-        if len(codes.shape) != 2 or codes.shape[0] < 1:
+        if codes.dim() != 2 or codes.shape[0] < 1:
             raise ValueError("with offsets the codes must be 2-D, one weight for each expert")
         E = codes.shape[0]
         lead = (E,)
         op = _experts(offsets, E)
-    top_k = int(top_k)
     rp = None
     if order is not None:
         rp = _ints(order, "order", (M,))
@@ -1248,8 +1257,8 @@ def _int4_product(A, codes, scales, zeros, group, offsets, order, top_k, out, ro
         top_k = 1
         if T != M:
             raise ValueError("the output has %d rows, A %d" % (M, T))
-    _int4_held(codes, scales, zeros, lead, rows_of_w, K, group)
-    return code, (E, op, rp, top_k, T, M), K, group
+    _int4_held(codes, scales, zeros, lead, rows_of_w, K, _int4_group(group))
+    return code, (E, op, rp, top_k, T, M), K
 
 
 def int4_gemm(A, codes, scales, C, zeros=None, group: int = 128, offsets=None, order=None,
@@ -1260,7 +1269,7 @@ def int4_gemm(A, codes, scales, C, zeros=None, group: int = 128, offsets=None, o
     rows of no expert stay as they are.  With order (sort_experts'), row r of C is computed from row
     order[r] // top_k of A, so that the tokens' rows need not be spread first."""
     N = C.shape[-1]
-    code, head, K, group = _int4_product(A, codes, scales, zeros, group, offsets, order, top_k, C, N)
+    code, head, K = _int4_product(A, codes, scales, zeros, group, offsets, order, top_k, C, N)
     if C.dtype != A.dtype and C.dtype is not _torch()[0].float32:
         raise TypeError("C has dtype %s, expected %s or float32" % (C.dtype, A.dtype))
     lda, ldc = _rows(A, "A", K), _rows(C, "C", N)
@@ -1277,7 +1286,7 @@ def int4_swiglu_gemm(A, codes, scales, Y, zeros=None, group: int = 128, offsets=
     rows interleaved (torch.stack((W1, W2), 1).flatten(0, 1) before quantising); Y [M, N] of A's
     dtype.  The rest as int4_gemm."""
     N = Y.shape[-1]
-    code, head, K, group = _int4_product(A, codes, scales, zeros, group, offsets, order, top_k, Y,
+    code, head, K = _int4_product(A, codes, scales, zeros, group, offsets, order, top_k, Y,
                                          2 * N)
     if Y.dtype != A.dtype:
         raise TypeError("Y has dtype %s, expected %s" % (Y.dtype, A.dtype))
