@@ -364,10 +364,13 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
 // keep the vector unit, which widens the codes, from issuing for less time than those of four times
 // as many 16 x 16 x 32 ones.  A wave takes two strips of 16 columns together: lane 32 h + n loads
 // the pieces q = h and q = 2 + h of row n of the two.  The activations pass through LDS, three tiles
-// of 128 along K with one barrier a tile, their 16-byte pieces XOR-swizzled by row.  bf16: the sums
-// of the activations over a group are taken one tile ahead, 16 rows by each wave, and enter the
-// group's products as their initial accumulators; without zero points they are taken times -(16 + 8)
-// at once.
+// of 128 along K with one barrier a tile, their 16-byte pieces XOR-swizzled by row.  bf16: minus the
+// sums of the activations over each group are taken one tile ahead, 16 rows by each wave; times
+// scale * (16 + zero) they are a product along the groups, two at a time on the fp32 32 x 32 x 2
+// matrix instruction.  (As the initial accumulators of each group's products they cost a read of LDS
+// by every lane and, with zero points, a multiplication for each value: 256 x 4096 by 11008, groups
+// of 64 with zero points, 57.6 us so and 52.3 us this way; 128 x 4096 by 11008, groups of 128, 33.2
+// and 32.2; 512 rows of the latter and groups of 32 the same both ways.)
 // ---------------------------------------------------------------------------
 template <int DT, int GROUP, bool ZEROS, int NP>
 __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
@@ -375,7 +378,7 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
     constexpr bool SUMS = DT == DT_BF16;
     typedef Int4Tile<GROUP, ZEROS> Tile;
     __shared__ u32x4 lds[3][BM * 16];
-    __shared__ f32x4 sums[SUMS ? 2 : 1][SUMS ? PER * BM / 4 : 1];
+    __shared__ f32x4 sums[SUMS ? 4 : 1][SUMS ? PER * BM / 4 : 1];     // of tile kt at kt % 4
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const GroupedParams& q = x.q;
     GroupItem it;
@@ -431,9 +434,9 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
             second[j] = *reinterpret_cast<const u32x4*>(codes[j] + (int64_t)kt * 1024 + 512);
         }
     };
-    // The group sums of this wave's 16 rows.
+    // Minus the group sums of this wave's 16 rows.
     auto add_up = [&](f32x4* to, const u32x4* buf) {
-        const uint32_t c = ZEROS ? 0x3F803F80u : 0xC1C0C1C0u;     // 1, or -24, twice
+        const uint32_t c = 0xBF80BF80u;                          // -1, twice
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
             f32x4 d = {0, 0, 0, 0};
@@ -447,8 +450,7 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
     // Eight steps of 16 along K.  While a step's products run, the next one's activations are read
     // and its codes widened; the barriers between steps keep the compiler from reading all of them
     // at once, which spills.
-    auto compute = [&](const u32x4* buf, const f32x4* group_sums, const Tile(&tile)[NP],
-                       const u32x4(&second)[NP]) {
+    auto compute = [&](const u32x4* buf, const Tile(&tile)[NP], const u32x4(&second)[NP]) {
         f32x16 acc[NP][MT];
         u32x4 a[2][MT], b[2][NP];
         auto ready = [&](auto uc) {
@@ -466,26 +468,12 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
         };
         auto eighth = [&](auto uc) {
             constexpr int u = uc, p = u / STEPS;
-            if constexpr (u % STEPS == 0)
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    const float off = -16.0f - tile[j].zero(p);
-#pragma unroll
-                    for (int i = 0; i < MT; ++i)
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            f32x4 d = {0, 0, 0, 0};
-                            if constexpr (SUMS) d = group_sums[p * (BM / 4) + 8 * i + 2 * g + lh];
-#pragma unroll
-                            for (int r = 0; r < 4; ++r)
-                                acc[j][i][4 * g + r] = SUMS && ZEROS ? off * d[r] : d[r];
-                        }
-                }
 #pragma unroll
             for (int j = 0; j < NP; ++j)
 #pragma unroll
                 for (int i = 0; i < MT; ++i)
-                    acc[j][i] = mfma16<DT>(a[u % 2][i], b[u % 2][j], acc[j][i]);
+                    acc[j][i] = mfma16<DT>(a[u % 2][i], b[u % 2][j],
+                                           u % STEPS == 0 ? f32x16{} : acc[j][i]);
             if constexpr (u < 7) ready(std::integral_constant<int, u + 1>{});
             if constexpr (u % STEPS == STEPS - 1)
 #pragma unroll
@@ -512,6 +500,32 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
         eighth(std::integral_constant<int, 6>{});
         eighth(std::integral_constant<int, 7>{});
     };
+    // Takes scale * (16 + zero) * the sums of two groups out of the sums of the products: lanes h of
+    // `offset` hold it for the group whose sums are at of[h].
+    auto take_out = [&](const float(&offset)[NP], const f32x4* first, const f32x4* second, bool both) {
+        const float* of = reinterpret_cast<const float*>(lh ? second : first);
+#pragma unroll
+        for (int i = 0; i < MT; ++i) {
+            const float s = both || lh == 0 ? of[32 * i + ln] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < NP; ++j)
+                sum[j][i] = __builtin_amdgcn_mfma_f32_32x32x2f32(s, offset[j], sum[j][i], 0, 0, 0);
+        }
+    };
+    // ... of a tile's own groups, where it has more than one
+    auto take_out_pairs = [&](const Tile(&tile)[NP], const f32x4* of) {
+#pragma unroll
+        for (int p = 0; p + 1 < PER; p += 2) {
+            float offset[NP];
+#pragma unroll
+            for (int j = 0; j < NP; ++j) {
+                const float lo = tile[j].template scale<DT>(p) * (16.0f + tile[j].zero(p));
+                const float hi = tile[j].template scale<DT>(p + 1) * (16.0f + tile[j].zero(p + 1));
+                offset[j] = lh ? hi : lo;
+            }
+            take_out(offset, of + p * (BM / 4), of + (p + 1) * (BM / 4), true);
+        }
+    };
     // Step kt computes on buffer kt % 3 while the sums of tile kt + 1, whose activations are in LDS,
     // are taken.  At its end the codes of tile kt + 2 take the registers of tile kt's, tile kt + 2 of
     // the activations goes to LDS, and its registers get tile kt + 3.  Tiles past the last whole one
@@ -519,17 +533,34 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
     // partial tile comes last, by itself.
     const int full = K / 128, last = full - 1;
     int cur = 0;
+    float before[NP] = {};                              // the even tile's offset (one group a tile)
     auto after = [](int i) { return i == 2 ? 0 : i + 1; };
     auto step = [&](auto from, int kt) {
         const int next = after(cur), free = after(next);
-        compute(lds[cur], sums[SUMS ? from : 0], t[from], more[from]);
-        if constexpr (SUMS) add_up(sums[1 - from], lds[next]);
+        compute(lds[cur], t[from], more[from]);
+        if constexpr (SUMS) {
+            add_up(sums[(kt + 1) % 4], lds[next]);
+            if constexpr (PER > 1) {
+                take_out_pairs(t[from], sums[kt % 4]);
+            } else {
+                float offset[NP];
+#pragma unroll
+                for (int j = 0; j < NP; ++j) {
+                    const float c = t[from][j].template scale<DT>(0) * (16.0f + t[from][j].zero(0));
+                    if constexpr (from == 0) before[j] = c;
+                    else offset[j] = lh ? c : before[j];
+                }
+                if constexpr (from == 1) take_out(offset, sums[(kt + 3) % 4], sums[kt % 4], true);
+            }
+        }
         load_codes(t[from], more[from], min(kt + 2, last));
         store_stage(lds[free]);
         load_stage(min(kt + 3, last));
         __syncthreads();
         cur = next;
     };
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
     if (full > 0) {
         load_stage(0);
         load_codes(t[0], more[0], 0);
@@ -545,10 +576,18 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
         }
         int kt = 0;
         for (; kt + 1 < full; kt += 2) {
-            step(std::integral_constant<int, 0>{}, kt);
-            step(std::integral_constant<int, 1>{}, kt + 1);
+            step(even, kt);
+            step(odd, kt + 1);
         }
-        if (kt < full) step(std::integral_constant<int, 0>{}, kt);
+        if (kt < full) {
+            step(even, kt);
+            if constexpr (SUMS && PER == 1) {
+                float offset[NP];
+#pragma unroll
+                for (int j = 0; j < NP; ++j) offset[j] = lh ? 0.0f : before[j];
+                take_out(offset, sums[kt % 4], sums[kt % 4], false);
+            }
+        }
     }
     if (K % 128 != 0) {
         load_codes(t[0], more[0], full);
@@ -557,14 +596,23 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
             stage[i] = int4_act(row[i] - 8 * spiece, full * 128 + 8 * spiece, K);
 #pragma unroll
         for (int j = 0; j < NP; ++j) t[0][j].cut(K - full * 128);
-        // the last whole step ended with a barrier
+        __syncthreads();                  // the sums of the last whole tile are read
         store_stage(lds[0]);
         __syncthreads();
         if constexpr (SUMS) {
             add_up(sums[0], lds[0]);
             __syncthreads();
+            if constexpr (PER > 1) {
+                take_out_pairs(t[0], sums[0]);
+            } else {
+                float offset[NP];
+#pragma unroll
+                for (int j = 0; j < NP; ++j)
+                    offset[j] = lh ? 0.0f : t[0][j].template scale<DT>(0) * (16.0f + t[0][j].zero(0));
+                take_out(offset, sums[0], sums[0], false);
+            }
         }
-        compute(lds[0], sums[0], t[0], more[0]);
+        compute(lds[0], t[0], more[0]);
     }
     // lane 32 h + n holds rows 8 g + 4 h .. + 3 of column n of each 32 x 32 tile; even columns and
     // the ones behind them meet in the even lanes
