@@ -25,13 +25,17 @@ bool half_type(int dtype) { return dtype == SG_F16 || dtype == SG_BF16; }
 //   up to 512, two: 32 rows, 4096 x 4096: 8.2 against 11.6 us one by one and 8.7 us by threes;
 //   up to 768, three: 1 row, 11008 x 4096: 7.2 against 7.9 us one by one and 8.2 us by twos;
 //   up to 1024, four to 4 waves: 8 rows, 16384 x 2048: 6.6 against 7.7 us by twos;
-//   up to 4096, six to 4 waves: 16 rows, 22016 x 4096: 14.7 against 18.6 us by fours and 19.0 us by
-//   twos; then four again: 256 rows of 64 experts, 2816 x 2048: 47.0 against 51.2 us by sixes.
-// 64-row tiles take 1 us for each 128 along K while they have a CU each, 0.65 us where they share
-// one; a piece takes a SIMD 0.165 us.  That puts them ahead from about 160 rows of one weight
-// (11008 x 4096: 128 rows 33.2 against 33.8 us, 256 rows 44.8 against 61 us; 4096 x 4096: 256 rows
-// 33.8 against 28.5 us, 512 rows 34.7 against 47.7 us) and 32 rows of each of 64 experts (2816 x
-// 2048: 74.8 against 85.1 us; 16 rows each: 67 against 56 us).
+//   up to 8192, six to 4 waves: 16 rows, 22016 x 4096: 14.7 against 18.6 us by fours and 19.0 us by
+//   twos; 96 rows, 11008 x 4096: 26.8 against 32.1 us by fours; then four again: 256 rows of 64
+//   experts, 2816 x 2048: 47.0 against 51.2 us by sixes.
+// From K = 512 on, 64-row tiles that have a CU each are divided in two along K: 512 rows, 4096 x
+// 4096: 28.2 against 33.0 us; K = 1024: 13.9 and 14.5 us; K = 256: 9.6 and 9.1 us; where tiles share
+// a CU it only costs (256 rows, 11008 x 4096: 51.6 against 44.9 us).
+// What decides between 16-row pieces and 64-row tiles are the times fitted to such runs, which stay
+// within a tenth of them for K from 128 to 11008.  They put 64-row tiles ahead from about 100 rows
+// of one weight (11008 x 4096: 96 rows 27.2 against 26.8 us, 128 rows 27.2 against 33.0 us; 4096 x
+// 4096: 256 rows 27.1 against 26.9 us, 320 rows 27.1 against 32.8 us) and 32 rows of each of 64
+// experts (2816 x 2048: 74.2 against 83.7 us; 16 rows each: 67 against 56 us).
 int choose(const GroupedParams& q) {
     if (const char* s = std::getenv("SG_FORCE_INT4")) {
         const int c = std::atoi(s);
@@ -44,12 +48,16 @@ int choose(const GroupedParams& q) {
     };
     const double pieces = high(16) * strips;
     const double rounds = std::ceil(high(64) * cdiv(q.g.N, 128) / 256.0);
-    const double many = 2.0 + tiles_k * (rounds > 1.0 ? 0.65 * rounds + 0.05 : 1.0);
-    if (mean > 16.0 && many < 4.0 + 0.165 * tiles_k * pieces / 1024.0) return 5;
+    const bool parts = rounds <= 1.0 && tiles_k >= 4.0;
+    const double many = parts          ? 8.5 + 0.6 * tiles_k
+                        : rounds > 1.0 ? 6.0 + tiles_k * (0.62 * rounds - 0.05)
+                                       : 7.0 + 0.8 * tiles_k;
+    const double few = 3.9 + (0.6 + 0.155 * tiles_k) * pieces / 1024.0;
+    if (mean > 16.0 && many < few) return parts ? 6 : 5;
     if (pieces <= 256.0) return 0;
     if (pieces <= 512.0) return 1;
     if (pieces <= 768.0) return 2;
-    return pieces <= 1024.0 || pieces > 4096.0 ? 3 : 4;
+    return pieces <= 1024.0 || pieces > 8192.0 ? 3 : 4;
 }
 
 int run_product(const char* what, int64_t experts, const int32_t* offsets, const int32_t* order,

@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: 64 rows x 128 NP columns a work-group, the columns divided over its four waves, so that
+// Many rows: 64 rows x 128 columns a work-group, the columns divided over its four waves, so that
 // each code is loaded and widened once and meets 64 rows, on 32 x 32 x 16 products: their operands
 // keep the vector unit, which widens the codes, from issuing for less time than those of four times
 // as many 16 x 16 x 32 ones.  A wave takes two strips of 16 columns together: lane 32 h + n loads
@@ -371,32 +371,39 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
 // by every lane and, with zero points, a multiplication for each value: 256 x 4096 by 11008, groups
 // of 64 with zero points, 57.6 us so and 52.3 us this way; 128 x 4096 by 11008, groups of 128, 33.2
 // and 32.2; 512 rows of the latter and groups of 32 the same both ways.)
+// KS = 2: eight waves, four for each half of K, joined through LDS, for grids that leave a CU one
+// work-group, whose waves would wait for their own operands: 1.0 us a step of 128 along K alone, 1.4
+// us for two work-groups' or two halves' steps.
+// Measured (MI355X, bf16, groups of 128): 512 x 4096 by 11008 63.8 us, 720 TFLOP/s, against 140 us
+// with 16-row pieces.  What bounds it is issue, not memory or the matrix unit: a wave's step is 18
+// products of 16 ns and 140 vector instructions, each of which the SIMD's other wave waits for.
+// Longer look-ahead on the codes and activations (2 tiles more: 5% faster alone on a CU, 8% slower
+// shared), on LDS (3 products: slower) and 256 columns (spills) did not pay.
 // ---------------------------------------------------------------------------
-template <int DT, int GROUP, bool ZEROS, int NP>
-__global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
-    constexpr int MT = 2, BM = 64, BN = 128 * NP, PER = 128 / GROUP, STEPS = 2 * GROUP / 32;
+template <int DT, int GROUP, bool ZEROS, int KS>
+__global__ void __launch_bounds__(256 * KS, 2) int4_tile_kernel(const Int4Params x) {
+    constexpr int MT = 2, BM = 64, BN = 128, PER = 128 / GROUP, STEPS = 2 * GROUP / 32;
     constexpr bool SUMS = DT == DT_BF16;
     typedef Int4Tile<GROUP, ZEROS> Tile;
-    __shared__ u32x4 lds[3][BM * 16];
-    __shared__ f32x4 sums[SUMS ? 4 : 1][SUMS ? PER * BM / 4 : 1];     // of tile kt at kt % 4
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    __shared__ u32x4 all_lds[KS][3][BM * 16];
+    __shared__ f32x4 all_sums[KS][SUMS ? 4 : 1][SUMS ? PER * BM / 4 : 1];     // of tile kt at kt % 4
+    const int lane = threadIdx.x & 63, tid = threadIdx.x & 255;
+    const int part = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8);
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    auto& lds = all_lds[part];
+    auto& sums = all_sums[part];
     const GroupedParams& q = x.q;
     GroupItem it;
     if (!find_rows<BM>(q, blockIdx.x, lane, it)) return;
     const int N = q.g.N, K = q.g.K, lr = lane & 15, ln = lane & 31, lh = lane >> 5;
-    const int n0 = it.tn * BN + wave * 32 * NP;
-    const uint8_t *codes[NP], *zeros[NP];
-    const uint16_t* scales[NP];
-#pragma unroll
-    for (int j = 0; j < NP; ++j) {
-        const int tn = min(n0 / 16 + 2 * j + (ln >> 4), (N + 15) / 16 - 1);
-        const int64_t at = it.e * x.s_scales + (int64_t)tn * x.tiles_g * 64 + 4 * lr;
-        codes[j] = x.codes + it.e * x.s_codes + (int64_t)tn * x.tiles_k * 1024 + 16 * (16 * lh + lr);
-        scales[j] = x.scales + at;
-        zeros[j] = x.zeros + at;
-    }
+    const int n0 = it.tn * BN + wave * 32;
+    const int tn = min(n0 / 16 + (ln >> 4), (N + 15) / 16 - 1);
+    const int64_t at = it.e * x.s_scales + (int64_t)tn * x.tiles_g * 64 + 4 * lr;
+    const Int4Strip strip = {
+        x.codes + it.e * x.s_codes + (int64_t)tn * x.tiles_k * 1024 + 16 * (16 * lh + lr),
+        x.zeros + at, x.scales + at};
     // this thread's piece of 8 columns in rows srow, srow + 16, srow + 32 and srow + 48
-    const int srow = threadIdx.x >> 4, spiece = threadIdx.x & 15;
+    const int srow = tid >> 4, spiece = tid & 15;
     const uint16_t* row[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -406,13 +413,7 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
     }
     const int spot = srow * 16 + (spiece ^ srow);
     const Int4Magic magic = int4_magic<DT>();
-    f32x16 sum[NP][MT];
-#pragma unroll
-    for (int j = 0; j < NP; ++j)
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) sum[j][i][r] = 0.0f;
+    f32x16 sum[MT] = {};
     u32x4 stage[4];
     auto load_stage = [&](int kt) {
 #pragma unroll
@@ -423,16 +424,12 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) buf[spot + 256 * i] = stage[i];
     };
-    // w: pieces q = h; more: pieces q = 2 + h
-    Tile t[2][NP];
-    u32x4 more[2][NP];
-    auto load_codes = [&](Tile(&tile)[NP], u32x4(&second)[NP], int kt) {
-#pragma unroll
-        for (int j = 0; j < NP; ++j) {
-            const Int4Strip s = {codes[j], zeros[j], scales[j]};
-            int4_load(tile[j], s, 0, kt);
-            second[j] = *reinterpret_cast<const u32x4*>(codes[j] + (int64_t)kt * 1024 + 512);
-        }
+    // t: pieces q = h; more: pieces q = 2 + h
+    Tile t[2];
+    u32x4 more[2];
+    auto load_codes = [&](auto to, int kt) {
+        int4_load(t[to], strip, 0, kt);
+        more[to] = *reinterpret_cast<const u32x4*>(strip.codes + (int64_t)kt * 1024 + 512);
     };
     // Minus the group sums of this wave's 16 rows.
     auto add_up = [&](f32x4* to, const u32x4* buf) {
@@ -450,44 +447,36 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
     // Eight steps of 16 along K.  While a step's products run, the next one's activations are read
     // and its codes widened; the barriers between steps keep the compiler from reading all of them
     // at once, which spills.
-    auto compute = [&](const u32x4* buf, const Tile(&tile)[NP], const u32x4(&second)[NP]) {
-        f32x16 acc[NP][MT];
-        u32x4 a[2][MT], b[2][NP];
+    auto compute = [&](const u32x4* buf, auto from) {
+        const Tile& tile = t[from];
+        f32x16 acc[MT];
+        u32x4 a[2][MT], b[2];
         auto ready = [&](auto uc) {
             constexpr int u = uc, s = u / 2, p = u / STEPS;
             const int piece = (4 * s + 2 * (u % 2) + lh) ^ lr;
 #pragma unroll
             for (int i = 0; i < MT; ++i) a[u % 2][i] = buf[(32 * i + ln) * 16 + piece];
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                Int4Zero zero{};
-                if constexpr (DT == DT_F16) zero = int4_zero(tile[j].zero(p));
-                b[u % 2][j] =
-                    int4_operand<DT>(u % 2 ? second[j][s] : tile[j].w[s], zero, magic);
-            }
+            Int4Zero zero{};
+            if constexpr (DT == DT_F16) zero = int4_zero(tile.zero(p));
+            b[u % 2] = int4_operand<DT>(u % 2 ? more[from][s] : tile.w[s], zero, magic);
         };
         auto eighth = [&](auto uc) {
             constexpr int u = uc, p = u / STEPS;
 #pragma unroll
-            for (int j = 0; j < NP; ++j)
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    acc[j][i] = mfma16<DT>(a[u % 2][i], b[u % 2][j],
-                                           u % STEPS == 0 ? f32x16{} : acc[j][i]);
+            for (int i = 0; i < MT; ++i)
+                acc[i] = mfma16<DT>(a[u % 2][i], b[u % 2], u % STEPS == 0 ? f32x16{} : acc[i]);
             if constexpr (u < 7) ready(std::integral_constant<int, u + 1>{});
-            if constexpr (u % STEPS == STEPS - 1)
+            if constexpr (u % STEPS == STEPS - 1) {
+                const float f = tile.template scale<DT>(p);
 #pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    const float f = tile[j].template scale<DT>(p);
+                for (int i = 0; i < MT; ++i) {
 #pragma unroll
-                    for (int i = 0; i < MT; ++i) {
-#pragma unroll
-                        for (int r = 0; r < 16; ++r)
-                            sum[j][i][r] = __builtin_fmaf(f, acc[j][i][r], sum[j][i][r]);
-                        // here, not a tile later with both tiles' accumulators alive
-                        asm volatile("" : "+v"(sum[j][i]));
-                    }
+                    for (int r = 0; r < 16; ++r)
+                        sum[i][r] = __builtin_fmaf(f, acc[i][r], sum[i][r]);
+                    // here, not a tile later with both tiles' accumulators alive
+                    asm volatile("" : "+v"(sum[i]));
                 }
+            }
             __builtin_amdgcn_sched_barrier(0);
         };
         ready(std::integral_constant<int, 0>{});
@@ -502,134 +491,138 @@ __global__ void __launch_bounds__(256, 2) int4_tile_kernel(const Int4Params x) {
     };
     // Takes scale * (16 + zero) * the sums of two groups out of the sums of the products: lanes h of
     // `offset` hold it for the group whose sums are at of[h].
-    auto take_out = [&](const float(&offset)[NP], const f32x4* first, const f32x4* second, bool both) {
+    auto offset_of = [&](const Tile& tile, int p) {
+        return tile.template scale<DT>(p) * (16.0f + tile.zero(p));
+    };
+    auto take_out = [&](float offset, const f32x4* first, const f32x4* second, bool both) {
         const float* of = reinterpret_cast<const float*>(lh ? second : first);
 #pragma unroll
         for (int i = 0; i < MT; ++i) {
             const float s = both || lh == 0 ? of[32 * i + ln] : 0.0f;
-#pragma unroll
-            for (int j = 0; j < NP; ++j)
-                sum[j][i] = __builtin_amdgcn_mfma_f32_32x32x2f32(s, offset[j], sum[j][i], 0, 0, 0);
+            sum[i] = __builtin_amdgcn_mfma_f32_32x32x2f32(s, offset, sum[i], 0, 0, 0);
         }
     };
     // ... of a tile's own groups, where it has more than one
-    auto take_out_pairs = [&](const Tile(&tile)[NP], const f32x4* of) {
+    auto take_out_pairs = [&](const Tile& tile, const f32x4* of) {
 #pragma unroll
         for (int p = 0; p + 1 < PER; p += 2) {
-            float offset[NP];
-#pragma unroll
-            for (int j = 0; j < NP; ++j) {
-                const float lo = tile[j].template scale<DT>(p) * (16.0f + tile[j].zero(p));
-                const float hi = tile[j].template scale<DT>(p + 1) * (16.0f + tile[j].zero(p + 1));
-                offset[j] = lh ? hi : lo;
-            }
-            take_out(offset, of + p * (BM / 4), of + (p + 1) * (BM / 4), true);
+            const float lo = offset_of(tile, p), hi = offset_of(tile, p + 1);
+            take_out(lh ? hi : lo, of + p * (BM / 4), of + (p + 1) * (BM / 4), true);
         }
     };
-    // Step kt computes on buffer kt % 3 while the sums of tile kt + 1, whose activations are in LDS,
-    // are taken.  At its end the codes of tile kt + 2 take the registers of tile kt's, tile kt + 2 of
-    // the activations goes to LDS, and its registers get tile kt + 3.  Tiles past the last whole one
-    // are that one again: a load behind a branch would make the compiler wait for all of them.  A
-    // partial tile comes last, by itself.
-    const int full = K / 128, last = full - 1;
+    // The whole tiles along K: `most` for the first part, `mine` for this one, of which `common` are
+    // every part's.  Step kt computes on buffer kt % 3 while the sums of tile kt + 1, whose
+    // activations are in LDS, are taken.  At its end the codes of tile kt + 2 take the registers of
+    // tile kt's, tile kt + 2 of the activations goes to LDS, and its registers get tile kt + 3.
+    // Tiles past the last whole one are that one again: a load behind a branch would make the
+    // compiler wait for all of them.  A partial tile comes last, by itself.
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
+    const int full = K / 128, common = full / KS, most = (full + KS - 1) / KS, base = part * most;
+    const int mine = KS == 1 || part == 0 ? most : full - most;
+    auto tile_at = [&](int kt) { return min(base + kt, full - 1); };
     int cur = 0;
-    float before[NP] = {};                              // the even tile's offset (one group a tile)
+    float before = 0.0f;                                // the even tile's offset (one group a tile)
     auto after = [](int i) { return i == 2 ? 0 : i + 1; };
-    auto step = [&](auto from, int kt) {
+    auto step = [&](auto from, int kt, bool active) {
         const int next = after(cur), free = after(next);
-        compute(lds[cur], t[from], more[from]);
+        if (active) compute(lds[cur], from);
         if constexpr (SUMS) {
             add_up(sums[(kt + 1) % 4], lds[next]);
-            if constexpr (PER > 1) {
-                take_out_pairs(t[from], sums[kt % 4]);
-            } else {
-                float offset[NP];
-#pragma unroll
-                for (int j = 0; j < NP; ++j) {
-                    const float c = t[from][j].template scale<DT>(0) * (16.0f + t[from][j].zero(0));
-                    if constexpr (from == 0) before[j] = c;
-                    else offset[j] = lh ? c : before[j];
+            if (active) {
+                if constexpr (PER > 1) {
+                    take_out_pairs(t[from], sums[kt % 4]);
+                } else if constexpr (from == 0) {
+                    before = offset_of(t[0], 0);
+                } else {
+                    const float here = offset_of(t[1], 0);
+                    take_out(lh ? here : before, sums[(kt + 3) % 4], sums[kt % 4], true);
                 }
-                if constexpr (from == 1) take_out(offset, sums[(kt + 3) % 4], sums[kt % 4], true);
             }
         }
-        load_codes(t[from], more[from], min(kt + 2, last));
+        load_codes(from, tile_at(kt + 2));
         store_stage(lds[free]);
-        load_stage(min(kt + 3, last));
+        load_stage(tile_at(kt + 3));
         __syncthreads();
         cur = next;
     };
-    constexpr std::integral_constant<int, 0> even{};
-    constexpr std::integral_constant<int, 1> odd{};
     if (full > 0) {
-        load_stage(0);
-        load_codes(t[0], more[0], 0);
+        load_stage(tile_at(0));
+        load_codes(even, tile_at(0));
         store_stage(lds[0]);
-        load_stage(min(1, last));
-        load_codes(t[1], more[1], min(1, last));
+        load_stage(tile_at(1));
+        load_codes(odd, tile_at(1));
         store_stage(lds[1]);
-        load_stage(min(2, last));
+        load_stage(tile_at(2));
         __syncthreads();
         if constexpr (SUMS) {
             add_up(sums[0], lds[0]);
             __syncthreads();
         }
         int kt = 0;
-        for (; kt + 1 < full; kt += 2) {
-            step(even, kt);
-            step(odd, kt + 1);
+        for (; kt + 1 < common; kt += 2) {
+            step(even, kt, true);
+            step(odd, kt + 1, true);
         }
-        if (kt < full) {
-            step(even, kt);
-            if constexpr (SUMS && PER == 1) {
-                float offset[NP];
-#pragma unroll
-                for (int j = 0; j < NP; ++j) offset[j] = lh ? 0.0f : before[j];
-                take_out(offset, sums[kt % 4], sums[kt % 4], false);
-            }
-        }
+        if (kt < most) step(even, kt, kt < mine);
+        if (KS > 1 && kt + 1 < most) step(odd, kt + 1, kt + 1 < mine);
+        if constexpr (SUMS && PER == 1)
+            if (mine % 2)
+                take_out(lh ? 0.0f : before, sums[(mine - 1) % 4], sums[(mine - 1) % 4], false);
     }
     if (K % 128 != 0) {
-        load_codes(t[0], more[0], full);
+        load_codes(even, full);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             stage[i] = int4_act(row[i] - 8 * spiece, full * 128 + 8 * spiece, K);
-#pragma unroll
-        for (int j = 0; j < NP; ++j) t[0][j].cut(K - full * 128);
+        t[0].cut(K - full * 128);
         __syncthreads();                  // the sums of the last whole tile are read
         store_stage(lds[0]);
         __syncthreads();
         if constexpr (SUMS) {
             add_up(sums[0], lds[0]);
             __syncthreads();
-            if constexpr (PER > 1) {
-                take_out_pairs(t[0], sums[0]);
-            } else {
-                float offset[NP];
-#pragma unroll
-                for (int j = 0; j < NP; ++j)
-                    offset[j] = lh ? 0.0f : t[0][j].template scale<DT>(0) * (16.0f + t[0][j].zero(0));
-                take_out(offset, sums[0], sums[0], false);
-            }
         }
-        compute(lds[0], t[0], more[0]);
+        if (part == KS - 1) {
+            if constexpr (SUMS) {
+                if constexpr (PER > 1) take_out_pairs(t[0], sums[0]);
+                else take_out(lh ? 0.0f : offset_of(t[0], 0), sums[0], sums[0], false);
+            }
+            compute(lds[0], even);
+        }
+    }
+    if constexpr (KS > 1) {
+        // the second part's sums reach the first through LDS
+        f32x4* pass = reinterpret_cast<f32x4*>(all_lds) + 8 * (wave * 64) + lane;
+        __syncthreads();
+        if (part == 1)
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+                pass[64 * v] = f32x4{sum[v / 4][4 * (v % 4)], sum[v / 4][4 * (v % 4) + 1],
+                                     sum[v / 4][4 * (v % 4) + 2], sum[v / 4][4 * (v % 4) + 3]};
+        __syncthreads();
+        if (part == 1) return;
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+            const f32x4 d = pass[64 * v];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sum[v / 4][4 * (v % 4) + r] += d[r];
+        }
     }
     // lane 32 h + n holds rows 8 g + 4 h .. + 3 of column n of each 32 x 32 tile; even columns and
     // the ones behind them meet in the even lanes
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int j = 0; j < NP; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float u = sum[j][i][r];
-                const float v = __builtin_bit_cast(
-                    float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, u), 0xB1, 0xf, 0xf, true));
-                const int m = it.m0 + 32 * i + 8 * (r / 4) + 4 * lh + r % 4;
-                const int n = n0 + 32 * j + ln;
-                if ((ln & 1) || m >= it.rows || n >= N) continue;
-                int4_put<DT>(x, (int64_t)(it.row0 + m) * q.g.ldc, n, u, v);
-            }
+        for (int r = 0; r < 16; ++r) {
+            const float u = sum[i][r];
+            const float v = __builtin_bit_cast(
+                float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, u), 0xB1, 0xf, 0xf, true));
+            const int m = it.m0 + 32 * i + 8 * (r / 4) + 4 * lh + r % 4;
+            const int n = n0 + ln;
+            if ((ln & 1) || m >= it.rows || n >= N) continue;
+            int4_put<DT>(x, (int64_t)(it.row0 + m) * q.g.ldc, n, u, v);
+        }
 }
 
 // ---------------------------------------------------------------------------
@@ -771,7 +764,9 @@ struct Int4Cfg {
     X(2, 1, 3, 8)      \
     X(3, 1, 4, 4)      \
     X(4, 1, 6, 4)
-#define SG_INT4_MANY(X) X(5, 4, 8, 4)
+#define SG_INT4_MANY(X) \
+    X(5, 4, 8, 4)       \
+    X(6, 4, 8, 8)
 #define SG_INT4_ROW(ID, MT, NT, NW) {MT, NT, NW, #MT "x" #NT " " #NW "w"},
 constexpr Int4Cfg kInt4Cfg[] = {SG_INT4_FEW(SG_INT4_ROW) SG_INT4_MANY(SG_INT4_ROW)};
 #undef SG_INT4_ROW

@@ -15,7 +15,7 @@ hipError_t launch_int4_group(int cfg, const Int4Params& x, unsigned blocks, hipS
         return hipGetLastError();
 #define SG_INT4_TILE(ID, MT, NT, NW)                                                   \
     case ID:                                                                           \
-        hipLaunchKernelGGL((int4_tile_kernel<DT, GROUP, ZEROS, NT / 8>), dim3(blocks),  \
+        hipLaunchKernelGGL((int4_tile_kernel<DT, GROUP, ZEROS, NW / 4>), dim3(blocks),  \
                            dim3(64 * NW), 0, st, x);                                   \
         return hipGetLastError();
     switch (cfg) {

@@ -282,14 +282,15 @@ def test_no_depth_and_no_rows():
     sg.int4_swiglu_gemm(torch.empty(0, 128, **dev), codes, scales, torch.empty(0, 8, **dev))
 
 
-@pytest.mark.parametrize("cfg", range(6))
+@pytest.mark.parametrize("cfg", range(7))
 @pytest.mark.parametrize("dtype", sorted(HALF))
 def test_every_tile(dtype, cfg, monkeypatch):
     """Each tile forced on sizes that end inside it: rows, columns, depth, runs and groups."""
     import swiglu_gemm_amd as sg
     monkeypatch.setenv("SG_FORCE_INT4", str(cfg))
     for M, N, K, group, zeros in ((1, 16, 128, 128, False), (70, 210, 1100, 64, True), (65, 130, 2304, 128, True),
-                                  (16, 98, 4000, 32, False), (3, 34, 40, 32, True)):
+                                  (16, 98, 4000, 32, False), (3, 34, 40, 32, True),
+                                  (40, 50, 640, 128, True), (33, 60, 384, 64, False)):
         g = torch.Generator().manual_seed(M + N + K)
         A = torch.randn(M, K, generator=g).to(HALF[dtype])
         print("int4 tile %d %s %d x %d x %d" % (cfg, dtype, M, N, K), flush=True)
@@ -302,11 +303,12 @@ def test_every_tile(dtype, cfg, monkeypatch):
 
 
 def test_the_choice_of_tiles():
-    """One piece to a work-group, then more columns, then 64-row tiles, as the products grow."""
+    """One piece to a work-group, then more columns, then 64-row tiles, in two parts along K while each
+    has a CU, as the products grow."""
     import swiglu_gemm_amd as sg
     dev = dict(device="cuda:0", dtype=torch.bfloat16)
-    for M, N, want in ((1, 4096, 0), (1, 8192, 1), (1, 11008, 2), (1, 16384, 3), (16, 22016, 4), (1, 70000, 3),
-                       (512, 4096, 5), (32, 1024, 0)):
+    for M, N, want in ((1, 4096, 0), (1, 8192, 1), (1, 11008, 2), (1, 16384, 3), (16, 22016, 4), (1, 140000, 3),
+                       (512, 4096, 6), (512, 11008, 5), (32, 1024, 0)):
         nc, ns = sg.int4_shapes(N, 4096)
         sg.int4_gemm(torch.zeros(M, 4096, **dev), torch.zeros(nc, device="cuda:0", dtype=U8), torch.zeros(ns, **dev),
                      torch.empty(M, N, **dev))
