@@ -98,19 +98,34 @@ int run_product(const char* what, int64_t experts, const int32_t* offsets, const
                                      : launch_int4<DT_BF16, false>(g, cfg, x, b, st));
 }
 
-void launch_pack(const Int4PackParams& p, bool pack, int dtype, unsigned batch, hipStream_t st) {
-    const int64_t rows = cdiv(p.N, 16) * 16;
-    const int64_t groups = std::max<int64_t>((int64_t)p.tiles_k * 128 / p.group, p.tiles_g * 4);
-    const int64_t blocks = cdiv(rows * groups, 256);
-    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536), 1, batch);
-    if (pack)
-        hipLaunchKernelGGL((int4_pack_kernel<DT_F32, true>), grid, dim3(256), 0, st, p);
-    else if (dtype == SG_F32)
-        hipLaunchKernelGGL((int4_pack_kernel<DT_F32, false>), grid, dim3(256), 0, st, p);
-    else if (dtype == SG_F16)
-        hipLaunchKernelGGL((int4_pack_kernel<DT_F16, false>), grid, dim3(256), 0, st, p);
-    else
-        hipLaunchKernelGGL((int4_pack_kernel<DT_BF16, false>), grid, dim3(256), 0, st, p);
+enum { QUANTIZE, PACK, DEQUANTIZE };
+template <int DT, int GROUP>
+void launch_tiles(int what, const Int4PackParams& p, const dim3& grid, hipStream_t st) {
+    const dim3 block(256);
+    if (what == DEQUANTIZE)
+        hipLaunchKernelGGL((int4_dequantize_kernel<DT, GROUP>), grid, block, 0, st, p);
+    else if (what == QUANTIZE)
+        hipLaunchKernelGGL((int4_pack_kernel<DT, GROUP, false>), grid, block, 0, st, p);
+    else if constexpr (DT == DT_F32)                       // (packing reads no floats)
+        hipLaunchKernelGGL((int4_pack_kernel<DT, GROUP, true>), grid, block, 0, st, p);
+}
+template <int DT>
+void launch_tiles(int what, const Int4PackParams& p, const dim3& grid, hipStream_t st) {
+    if (p.group == 32) launch_tiles<DT, 32>(what, p, grid, st);
+    else if (p.group == 64) launch_tiles<DT, 64>(what, p, grid, st);
+    else launch_tiles<DT, 128>(what, p, grid, st);
+}
+int run_tiles(const char* name, int what, Int4PackParams& p, int dtype, int64_t batch, void* stream) {
+    // quantising and packing fill whole tiles of scales, which may reach past those of codes
+    p.across = what == DEQUANTIZE ? p.tiles_k : p.tiles_g * 4 * p.group / 128;
+    const int64_t blocks = cdiv(cdiv(p.N, 16) * p.across, 4);
+    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536), 1, (unsigned)batch);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    describe(name, -2, "");
+    if (dtype == SG_F32) launch_tiles<DT_F32>(what, p, grid, st);
+    else if (dtype == SG_F16) launch_tiles<DT_F16>(what, p, grid, st);
+    else launch_tiles<DT_BF16>(what, p, grid, st);
+    return status_of(hipGetLastError());
 }
 
 Int4PackParams pack_params(int64_t N, int64_t K, int64_t group, const void* codes,
@@ -155,9 +170,7 @@ int sg_int4_quantize(const void* W, int64_t ldw, int64_t strideW, int64_t batch,
     p.ldw = ldw;
     p.sW = batch > 1 ? strideW : 0;
     p.scale_bf16 = scale_dtype == SG_BF16;
-    describe("int4_quantize", -2, "");
-    launch_pack(p, false, dtype, (unsigned)batch, static_cast<hipStream_t>(stream));
-    return status_of(hipGetLastError());
+    return run_tiles("int4_quantize", QUANTIZE, p, dtype, batch, stream);
 }
 
 int sg_int4_pack(const void* src, const void* src_scales, const void* src_zeros, int64_t batch,
@@ -179,9 +192,7 @@ int sg_int4_pack(const void* src, const void* src_scales, const void* src_zeros,
     p.src = static_cast<const uint8_t*>(src);
     p.src_scales = static_cast<const uint16_t*>(src_scales);
     p.src_zeros = static_cast<const uint8_t*>(src_zeros);
-    describe("int4_pack", -2, "");
-    launch_pack(p, true, SG_F32, (unsigned)batch, static_cast<hipStream_t>(stream));
-    return status_of(hipGetLastError());
+    return run_tiles("int4_pack", PACK, p, SG_F32, batch, stream);
 }
 
 int sg_int4_dequantize(const void* codes, const void* scales, const void* zeros, int scale_dtype,
@@ -207,17 +218,7 @@ int sg_int4_dequantize(const void* codes, const void* scales, const void* zeros,
     p.ldw = ldw;
     p.sW = batch > 1 ? strideW : 0;
     p.scale_bf16 = scale_dtype == SG_BF16;
-    const int64_t blocks = cdiv(N * cdiv(K, 8), 256);
-    const dim3 grid((unsigned)(blocks < 65536 ? blocks : 65536), 1, (unsigned)batch);
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    describe("int4_dequantize", -2, "");
-    if (dtype == SG_F32)
-        hipLaunchKernelGGL(int4_dequantize_kernel<DT_F32>, grid, dim3(256), 0, st, p);
-    else if (dtype == SG_F16)
-        hipLaunchKernelGGL(int4_dequantize_kernel<DT_F16>, grid, dim3(256), 0, st, p);
-    else
-        hipLaunchKernelGGL(int4_dequantize_kernel<DT_BF16>, grid, dim3(256), 0, st, p);
-    return status_of(hipGetLastError());
+    return run_tiles("int4_dequantize", DEQUANTIZE, p, dtype, batch, stream);
 }
 
 int sg_int4_gemm(int64_t experts, const int32_t* offsets, const int32_t* order, int64_t top_k,

@@ -11,8 +11,14 @@ using namespace sg;
 
 namespace {
 
+// Work-groups of 256 threads along one side of a grid: a launch has fewer than 2^32 threads there.
+constexpr int64_t kMaxSide = ((int64_t)1 << 24) - 1;
+
 #define SG_LAUNCH(KERNEL, GRID, BLOCK, ST, P) hipLaunchKernelGGL((KERNEL), GRID, BLOCK, 0, ST, P)
 
+// Up to 256 experts and 8 choices several tokens share a wave; else each has one.  fp32 logits, 8
+// choices: 1 token of 64 experts 3.4 against 3.5 us for one wave each, 16384 tokens 4.5 against 14.5
+// us (6 choices), of 256 experts 10.0 against 21.6 us.
 template <int DT>
 void launch_route(const RouteParams& p, hipStream_t st) {
     const dim3 block(256);
@@ -37,7 +43,9 @@ void launch_route(const RouteParams& p, hipStream_t st) {
         return;                                                          \
     }
     SG_ROUTE(1)
+    SG_ROUTE(2)
     SG_ROUTE(4)
+    SG_ROUTE(8)
     SG_ROUTE(16)
 #undef SG_ROUTE
 }
@@ -53,11 +61,13 @@ void launch_route_bwd(const RouteParams& p, hipStream_t st) {
     SG_ROUTE(1)
     SG_ROUTE(2)
     SG_ROUTE(4)
+    SG_ROUTE(8)
     SG_ROUTE(16)
 #undef SG_ROUTE
 }
 
 int run_route(bool bwd, int dtype, const RouteParams& p, hipStream_t st) {
+    if (cdiv(p.T, 4) > kMaxSide) return status_of(hipErrorInvalidConfiguration);
     describe(bwd ? "route_experts_bwd" : "route_experts", -2, "");
     if (dtype == SG_F32) bwd ? launch_route_bwd<DT_F32>(p, st) : launch_route<DT_F32>(p, st);
     else if (dtype == SG_F16) bwd ? launch_route_bwd<DT_F16>(p, st) : launch_route<DT_F16>(p, st);
@@ -67,16 +77,15 @@ int run_route(bool bwd, int dtype, const RouteParams& p, hipStream_t st) {
 
 bool float_type(int dtype) { return dtype == SG_F32 || dtype == SG_F16 || dtype == SG_BF16; }
 
-// Threads of a row and the grid: rows of up to 2048 elements share a work-group, and where
-// there are few tokens their rows are divided over grid y.
+// Threads of a row and the grid: rows of up to 2048 elements share a work-group, longer ones are
+// divided over grid y (bf16, 8 places: spreading 1 row of 4096 4.8 us, 6.4 us by one work-group; 4096
+// rows of 4096 61.4 and 66.1 us; 4096 elements by 64 threads 76.9 us).
 dim3 rows_grid(RowsParams& p) {
     const int64_t pieces = cdiv(p.D, 8);
     p.lanes = 1;
     while (p.lanes < 256 && p.lanes < pieces) p.lanes *= 2;
-    const int64_t x = cdiv(p.T, 256 / p.lanes);
-    int64_t y = cdiv(pieces, p.lanes), most = cdiv(2048, x);
-    if (y > most) y = most;
-    return dim3((unsigned)x, (unsigned)y);
+    const int64_t x = cdiv(p.T, 256 / p.lanes), y = cdiv(pieces, p.lanes);
+    return dim3((unsigned)x, (unsigned)(y < 65535 ? y : 65535));
 }
 
 enum { SPREAD, COMBINE, COMBINE_BWD };
@@ -179,11 +188,14 @@ int sg_sort_experts(const int32_t* ids, int64_t n, int64_t experts, int32_t* off
     if (!offsets) return -4;
     SortParams p{ids, (int)n, (int)experts, offsets, order, place};
     hipStream_t st = static_cast<hipStream_t>(stream);
-    // the walk that writes is divided while the work-groups fit the CUs one each
+    // Four waves up to 4096 ids (64 experts, 1024 ids: 2.9 us, 4.1 us with 16 waves; 4096: 4.7 and 5.6
+    // us; 8192: 7.2 and 5.7 us).  The walk that writes is divided from 16384 ids on while the
+    // work-groups fit the CUs one each (65536 ids of 8 experts in 8 parts 8.3 us, in one 15.2 us; of
+    // 64 experts in 3 parts 9.9 us, in one 13.3 us, in 8 14.6 us; 16384 ids: no part helps).
     const int64_t fit = 256 / (experts + 1), parts = n <= 16384 || fit < 1 ? 1 : fit < 8 ? fit : 8;
     const dim3 grid((unsigned)experts + 1, (unsigned)parts);
     describe("sort_experts", -2, "");
-    if (n <= 1024) SG_LAUNCH((sort_kernel<4, 1>), grid, dim3(256), st, p);
+    if (n <= 4096) SG_LAUNCH((sort_kernel<4, 1>), grid, dim3(256), st, p);
     else SG_LAUNCH((sort_kernel<16, 4>), grid, dim3(1024), st, p);
     return status_of(hipGetLastError());
 }
@@ -215,6 +227,7 @@ int sg_spread_rows(const void* X, int64_t ldx, int64_t T, int64_t D, int dtype,
     p.Y = Y;
     p.ldy = ldy;
     const dim3 grid = rows_grid(p);
+    if (grid.x > kMaxSide) return status_of(hipErrorInvalidConfiguration);
     return run_rows("spread_rows", SPREAD, dtype, grid, p, static_cast<hipStream_t>(stream));
 }
 
@@ -249,6 +262,7 @@ int sg_combine_rows(const void* Z, int64_t ldz, int64_t M, int64_t D, int64_t T,
     p.Y = out;
     p.ldy = ldo;
     const dim3 grid = rows_grid(p);
+    if (grid.x > kMaxSide) return status_of(hipErrorInvalidConfiguration);
     return run_rows("combine_rows", COMBINE, dtype, grid, p, static_cast<hipStream_t>(stream));
 }
 
@@ -273,7 +287,7 @@ int sg_combine_rows_bwd(const void* dOut, int64_t lddo, const void* Z, int64_t l
     if (dZ && lddz < row) return -13;
     if (!any) return 0;
     const int64_t blocks = cdiv(T * top_k, 4);
-    if (blocks > (int64_t)1 << 24) return status_of(hipErrorInvalidConfiguration);
+    if (blocks > kMaxSide) return status_of(hipErrorInvalidConfiguration);
     RowsParams p{};
     p.X = dOut;
     p.ldx = lddo;

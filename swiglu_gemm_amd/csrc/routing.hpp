@@ -25,56 +25,6 @@ struct RouteParams {
     int64_t lddx;
 };
 
-typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
-
-// Eight elements from column c of a row of D, as loaded; zeros behind the row.
-template <int DT>
-struct Raw8 {
-    u32x4 a;
-    __device__ __forceinline__ void load(const char* row, int c, int D) {
-        if (c + 8 <= D) {
-            a = *reinterpret_cast<const u32x4_any*>(row + (int64_t)c * 2);
-        } else {
-            const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[i] = (c + 2 * i < D ? p[2 * i] : 0u) |
-                       (c + 2 * i + 1 < D ? (uint32_t)p[2 * i + 1] << 16 : 0u);
-        }
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = to_f32<DT>((uint16_t)a[i]);
-            v[2 * i + 1] = to_f32<DT>((uint16_t)(a[i] >> 16));
-        }
-    }
-};
-template <>
-struct Raw8<DT_F32> {
-    f32x4 a, b;
-    __device__ __forceinline__ void load(const char* row, int c, int D) {
-        const float* p = reinterpret_cast<const float*>(row) + c;
-        if (c + 8 <= D) {
-            a = *reinterpret_cast<const f32x4_any*>(p);
-            b = *reinterpret_cast<const f32x4_any*>(p + 4);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                a[i] = c + i < D ? p[i] : 0.0f;
-                b[i] = c + 4 + i < D ? p[4 + i] : 0.0f;
-            }
-        }
-    }
-    __device__ __forceinline__ void get(float (&v)[8]) const {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = a[i];
-            v[4 + i] = b[i];
-        }
-    }
-};
 // x moved between lanes by a data-parallel move; lanes without a source (rows left out) get `none`.
 // Every lane of the wave takes part: none of these may stand in an operand that only some evaluate.
 template <int CTRL, int ROWS>
@@ -160,11 +110,14 @@ __device__ __forceinline__ void route_finish(const RouteParams& p, int t, int la
     }
     if (lane < p.top_k) {
         p.ids[(int64_t)t * p.top_k + lane] = id;
-        p.weights[(int64_t)t * p.top_k + lane] = id < 0 ? 0.0f : bad ? __builtin_nanf("") : p.scale * w;
+        p.weights[(int64_t)t * p.top_k + lane] =
+            id < 0 ? 0.0f : bad ? __builtin_nanf("") : p.scale * w;
     }
 }
 
-// One token by one wave, every comparison in 64 bits; lane l holds experts l, l + 64, ...
+// One token by one wave, every comparison in 64 bits; lane l holds experts l, l + 64, ...  The choices
+// follow one another, each a maximum over the wave, which bounds it: 16384 tokens of 512 experts, 10
+// choices 35 us; of 1024, 32 choices 161 us (fp32, MI355X).
 // lds: 64 NV values for this wave.
 template <int DT, int NV>
 __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lane, double* lds) {
@@ -306,8 +259,10 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
 //   scores 2^-21 for sigmoid and 2^-18 of the largest for softmax), the few that are in question
 //   are compared in 64 bits, one a lane (0.1 % of tokens with random logits).  Groups that close and
 //   everything unusual (NaN, too few experts left) go through route_token.
-// 16384 tokens, 256 experts in 8 groups, top 8, sigmoid and bias: ROUTE_NOW (one wave a token in 64
-// bits: 53 us).
+// What bounds it is the vector unit, not memory: 16384 tokens, top 8 (MI355X, in a graph), fp32 logits:
+//   64 experts (6 choices) 4.5 us, 0.9 TB/s; 256 experts 8.0 us, 2.1 TB/s;
+//   256 experts in 8 groups, sigmoid and bias 14.5 us (one wave a token in 64 bits 35 us).
+// 1 token of 64 experts 3.4 us, nearly all of it the launch.
 // ---------------------------------------------------------------------------
 template <int S>
 __device__ __forceinline__ uint32_t lane_swap(uint32_t x) {
@@ -498,7 +453,8 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
                 rank += o > v || (o == v && h < g);
             }
             const bool is = g < p.groups, keep = is && rank < p.top_groups;
-            const float low = lanes_reduce<L>(keep ? v : inf, [](float a, float b) { return fminf(a, b); });
+            const float low = lanes_reduce<L>(keep ? v : inf,
+                                              [](float a, float b) { return fminf(a, b); });
             const float high = lanes_reduce<L>(is && !keep ? v : -inf,
                                                [](float a, float b) { return fmaxf(a, b); });
             // a sum of two is off by twice what a score is, and so is the other
@@ -581,7 +537,8 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float d = fmaxf((p.bias ? c[i] : x[i]) - lo, 0.0f);
-            key[i] = in[i] ? (4096u + (uint32_t)fminf(d * scale, 16770000.0f)) << 8 | (255u - (e0 + i)) : 0;
+            key[i] = in[i] ? (4096u + (uint32_t)fminf(d * scale, 16770000.0f)) << 8 | (255u - (e0 + i))
+                           : 0;
         }
     }
     uint32_t best[8];
@@ -694,7 +651,8 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
         if (p.bias) {
             if (softmax) {
                 double sum = 0.0;
-                for (int i = lane; i < p.E; i += 64) sum += exp((double)load_elem<DT>(its, i) - (double)its_top);
+                for (int i = lane; i < p.E; i += 64)
+                    sum += exp((double)load_elem<DT>(its, i) - (double)its_top);
                 exact = exp(exact - (double)its_top) / wave_sum(sum);
             } else {
                 exact = 1.0 / (1.0 + exp(-exact));
@@ -720,6 +678,15 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
     }
 }
 
+// ---------------------------------------------------------------------------
+// dX of a token by one wave, from the choice: with l the chosen logs of scores, q = softmax(l) and
+// G = scale * dweights, dl = q (G - sum G q) (for sigmoid times dl/dx = 1 - s); not renormalised, the
+// softmax's own product dx = s (G - sum G s) over the row, or G s (1 - s).  One read of what it needs
+// of X (renormalised: the chosen alone), one write of dX.  A lane has NV experts in registers and the
+// choices are added to them in order, so that the same expert twice adds up the same each time.
+// Measured (MI355X, bf16, 16384 tokens, top 8): 64 experts 6.0 us, softmax not renormalised 6.3 us;
+// 256 experts 8.9 and 11.7 us (8 MB written; 17 MB moved, 1.4 TB/s): the walk over the choices bounds it.
+// ---------------------------------------------------------------------------
 template <int DT, int NV>
 __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -793,6 +760,8 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
 // expert, which behave as expert `experts`.  Every work-group reads all ids: no second launch, no
 // table between work-groups and no atomics.  Wave w owns one run of the ids, in order, so the
 // ranks are the order of the places.  Grid y divides the second walk, the one that writes.
+// What bounds it is the walk of one work-group over all ids: 64 experts (MI355X): 1024 ids 2.9 us,
+// 16384 5.7 us, 65536 10.0 us (1.3 us for the 0.8 MB at the rate of a copy, and the launch).
 // ---------------------------------------------------------------------------
 typedef int32_t i32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -916,7 +885,13 @@ __global__ void __launch_bounds__(64 * WAVES) sort_kernel(const SortParams p) {
 
 // ---------------------------------------------------------------------------
 // Rows to their places and back.  Eight elements a thread; `lanes` threads (a power of two up to
-// 256) walk a row, 256 / lanes tokens share a work-group, grid y divides long rows of few tokens.
+// 256) walk a row, 256 / lanes tokens share a work-group, grid y divides long rows.  Memory bounds
+// all three, and each byte is moved once: a token's row is read once for its top_k places, and its sum
+// stays in registers.  Measured (MI355X, bf16, memory cold, all bytes read and written):
+//   spread    4096 x 4096 to 8 places  302 MB  61.5 us  4.9 TB/s;  128 x 4096 5.8 us;  1 x 4096 4.7 us
+//   combine   4096 x 4096 of 8 places  302 MB  62 us    4.9 TB/s;  128 x 4096 5.5 us;  1 x 4096 4.3 us
+//   combine's gradient, 16384 x 2048 of 4 places, 604 MB with Z read for the weights' dots: 131 us,
+//   4.6 TB/s (a copy of 4 GiB: 4.75 TB/s)
 // ---------------------------------------------------------------------------
 struct RowsParams {
     const void *X, *Z, *R;       // spread: X; combine: Z, R; backward: X = dOut, Z
@@ -927,32 +902,6 @@ struct RowsParams {
     const float* weights;
     float* dweights;
 };
-
-template <int DT>
-__device__ __forceinline__ void load8(const char* row, int c, int D, float (&v)[8]) {
-    Raw8<DT> raw;
-    raw.load(row, c, D);
-    raw.get(v);
-}
-template <int DT>
-__device__ __forceinline__ void store8(char* row, int c, int D, const float (&v)[8]) {
-    if (c + 8 <= D) {
-        if constexpr (DT == DT_F32) {
-            *reinterpret_cast<f32x4_any*>(row + (int64_t)c * 4) = f32x4{v[0], v[1], v[2], v[3]};
-            *reinterpret_cast<f32x4_any*>(row + (int64_t)c * 4 + 16) = f32x4{v[4], v[5], v[6], v[7]};
-        } else {
-            u32x4 a;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                a[i] = from_f32<DT>(v[2 * i]) | (uint32_t)from_f32<DT>(v[2 * i + 1]) << 16;
-            *reinterpret_cast<u32x4_any*>(row + (int64_t)c * 2) = a;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < D) put_elem<DT>(row, c + i, v[i]);
-    }
-}
 
 template <int DT>
 __global__ void __launch_bounds__(256) spread_kernel(const RowsParams p) {
@@ -1024,7 +973,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const RowsParams p) {
     }
 }
 
-// One wave a place: its row of dZ, and the dot product for its weight.
+// One wave a place: its row of dZ, and the dot product for its weight, whose order of summing is fixed.
 template <int DT>
 __global__ void __launch_bounds__(256) combine_bwd_kernel(const RowsParams p) {
     constexpr int ESZ = DT == DT_F32 ? 4 : 2;

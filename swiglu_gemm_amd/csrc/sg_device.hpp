@@ -58,6 +58,82 @@ __device__ __forceinline__ void put_elem(void* p, int64_t i, float x) {
     else reinterpret_cast<uint16_t*>(p)[i] = from_f32<DT>(x);
 }
 
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+
+// Eight elements from column c of a row of D, as loaded; zeros behind the row.
+template <int DT>
+struct Raw8 {
+    u32x4 a;
+    __device__ __forceinline__ void load(const char* row, int c, int D) {
+        if (c + 8 <= D) {
+            a = *reinterpret_cast<const u32x4_any*>(row + (int64_t)c * 2);
+        } else {
+            const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + c;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[i] = (c + 2 * i < D ? p[2 * i] : 0u) |
+                       (c + 2 * i + 1 < D ? (uint32_t)p[2 * i + 1] << 16 : 0u);
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = to_f32<DT>((uint16_t)a[i]);
+            v[2 * i + 1] = to_f32<DT>((uint16_t)(a[i] >> 16));
+        }
+    }
+};
+template <>
+struct Raw8<DT_F32> {
+    f32x4 a, b;
+    __device__ __forceinline__ void load(const char* row, int c, int D) {
+        const float* p = reinterpret_cast<const float*>(row) + c;
+        if (c + 8 <= D) {
+            a = *reinterpret_cast<const f32x4_any*>(p);
+            b = *reinterpret_cast<const f32x4_any*>(p + 4);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                a[i] = c + i < D ? p[i] : 0.0f;
+                b[i] = c + 4 + i < D ? p[4 + i] : 0.0f;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = a[i];
+            v[4 + i] = b[i];
+        }
+    }
+};
+template <int DT>
+__device__ __forceinline__ void load8(const char* row, int c, int D, float (&v)[8]) {
+    Raw8<DT> raw;
+    raw.load(row, c, D);
+    raw.get(v);
+}
+template <int DT>
+__device__ __forceinline__ void store8(char* row, int c, int D, const float (&v)[8]) {
+    if (c + 8 <= D) {
+        if constexpr (DT == DT_F32) {
+            *reinterpret_cast<f32x4_any*>(row + (int64_t)c * 4) = f32x4{v[0], v[1], v[2], v[3]};
+            *reinterpret_cast<f32x4_any*>(row + (int64_t)c * 4 + 16) = f32x4{v[4], v[5], v[6], v[7]};
+        } else {
+            u32x4 a;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                a[i] = from_f32<DT>(v[2 * i]) | (uint32_t)from_f32<DT>(v[2 * i + 1]) << 16;
+            *reinterpret_cast<u32x4_any*>(row + (int64_t)c * 2) = a;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < D) put_elem<DT>(row, c + i, v[i]);
+    }
+}
+
 // SiLU(x) = x / (1 + e^-x), evaluated as x * rcp(1 + 2^(-x*log2 e)) with the
 // hardware exp2 and reciprocal (about 1 ulp each in fp32, far below the bf16 /
 // fp16 output rounding).  e^-x -> +inf for very negative x gives rcp = 0 and

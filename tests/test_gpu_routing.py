@@ -43,7 +43,7 @@ def check_route(X, top_k, Xd=None, **how):
 
 
 SHAPES = [(1, 1, 1), (1, 8, 2), (3, 5, 5), (7, 60, 6), (130, 64, 8), (9, 128, 8), (5, 160, 6), (33, 256, 8),
-          (2, 500, 64), (3, 1024, 33)]
+          (2, 500, 64), (3, 1024, 33), (6, 100, 9), (5, 300, 17), (3, 200, 12)]
 
 
 @pytest.mark.parametrize("T,E,k", SHAPES)
@@ -245,7 +245,7 @@ def test_route_backward_of_odd_ids():
 
 # ------------------------------------------------------------------ sort
 @pytest.mark.parametrize("n,E", [(0, 3), (1, 1), (5, 4), (64, 64), (256, 64), (1000, 8), (1025, 300),
-                                 (5000, 60), (20000, 256), (70001, 7)])
+                                 (4096, 20), (5000, 60), (20000, 256), (70001, 7)])
 def test_sort(n, E):
     import swiglu_gemm_amd as sg
     g = torch.Generator().manual_seed(n + E)
@@ -334,6 +334,19 @@ def test_combine_and_backward(dtype, T, k, D):
         assert torch.equal(only, dZ)
         alone = sg.combine_rows_bwd(dO.cuda(), Zd, pd, cuda(wn), dweights=torch.empty_like(dw))[1]
         assert torch.equal(alone, dw)
+
+
+@pytest.mark.parametrize("dtype", sorted(FLOATS))
+def test_combine_onto_its_residual(dtype):
+    """out may be the residual itself."""
+    import swiglu_gemm_amd as sg
+    T, k, D, M = 37, 3, 2500, 90
+    place, g = places(T, k, M, 5)
+    Z, R = (torch.randn(n, D, generator=g).to(FLOATS[dtype]) for n in (M, T))
+    w = torch.randn(T, k, generator=g)
+    out = R.cuda()
+    sg.combine_rows(Z.cuda(), place.cuda(), out, w.cuda(), out)
+    check(out, *ref.combine(Z, place, w, R), "out")
 
 
 def test_rows_of_nothing():
