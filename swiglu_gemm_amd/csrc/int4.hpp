@@ -251,10 +251,11 @@ __device__ __forceinline__ void int4_put(const Int4Params& x, int64_t row, int n
 // One work-group: 16 MT rows x 16 NT columns of the product; its waves take every NW-th tile of
 // 128 along K and their sums meet in LDS, in the order of the waves.  A wave keeps a tile of codes
 // of each of its NT strips, and the activations of a tile, under way while it works on the one
-// before.  For few rows: what bounds it is the codes from memory.  Measured (MI355X, bf16, groups of
-// 128, weights cold, in a graph): 1 x 4096 by 4096 3.9 us, nearly all of it the launch and one trip
-// to memory; 16 x 4096 by 22016 (SwiGLU) 13.2 us, 47 MB, 3.6 TB/s; 256 rows of 64 experts, 2048 by
-// 2816 with zero points in groups of 64, 200 MB, 36.7 us, 5.4 TB/s (a plain read: 5.66 TB/s).
+// before.  For few rows: what bounds it is the codes from memory.  Measured (MI355X, kernel alone,
+// weights cold): bf16, 1 x 4096 by 4096 4.9 us, most of it launch and one trip to memory; fp16, 16 x
+// 4096 by 22016 (SwiGLU, groups of 128 with zero points) 14.5 us, 47 MB, 3.2 TB/s; bf16, 256 rows of
+// 64 experts, 2048 by 2816 with zero points in groups of 64, 200 MB, 48.6 us in the mean, 45.1 at best,
+// 4.4 TB/s (a plain read: 5.66 TB/s).
 template <int DT, int GROUP, bool ZEROS, int MT, int NT, int NW>
 __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
     constexpr int BM = 16 * MT, BN = 16 * NT, PER = 128 / GROUP;
