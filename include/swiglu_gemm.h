@@ -496,7 +496,7 @@ int sg_route_experts_bwd(const void* X, int64_t ldx, int64_t T, int64_t E, int d
  *     order[r]     the place that is row r, -1 from offsets[experts] on
  *     place[i]     the row of place i (order[place[i]] == i), -1 where ids[i] is outside
  *                  0..experts-1
- * Each expert's part of the work reads all ids: 64 experts' 65536 take 10 us, 4 n * experts bytes
+ * Each expert's part of the work reads all ids: 64 experts' 65536 take 9.4 us, 4 n * experts bytes
  * from the caches.
  *  1 ids, 2 n (0..2^30)   3 experts (1..65536)   4 offsets, 5 order, 6 place (order or place
  *  may be NULL)   7 stream.

@@ -189,14 +189,15 @@ int sg_sort_experts(const int32_t* ids, int64_t n, int64_t experts, int32_t* off
     SortParams p{ids, (int)n, (int)experts, offsets, order, place};
     hipStream_t st = static_cast<hipStream_t>(stream);
     // Four waves up to 4096 ids (64 experts, 1024 ids: 2.9 us, 4.1 us with 16 waves; 4096: 4.7 and 5.6
-    // us; 8192: 7.2 and 5.7 us).  The walk that writes is divided from 16384 ids on while the
-    // work-groups fit the CUs one each (65536 ids of 8 experts in 8 parts 8.3 us, in one 15.2 us; of
-    // 64 experts in 3 parts 9.9 us, in one 13.3 us, in 8 14.6 us; 16384 ids: no part helps).
-    const int64_t fit = 256 / (experts + 1), parts = n <= 16384 || fit < 1 ? 1 : fit < 8 ? fit : 8;
+    // us; 8192: 7.2 and 5.2 us).  The walk that writes is divided from 16384 ids on while the
+    // work-groups fit the CUs one each (64 experts, 16384 ids in 3 parts 5.0 us, in one 5.7 us; 65536
+    // in 3 parts 9.4 us, in one 13.8 us, in 4 12.0 us; of 8 experts in 8 parts 7.4 us, in one 15.4 us;
+    // 8192 ids: no part helps).
+    const int64_t fit = 256 / (experts + 1), parts = n < 16384 || fit < 1 ? 1 : fit < 8 ? fit : 8;
     const dim3 grid((unsigned)experts + 1, (unsigned)parts);
     describe("sort_experts", -2, "");
-    if (n <= 4096) SG_LAUNCH((sort_kernel<4, 1>), grid, dim3(256), st, p);
-    else SG_LAUNCH((sort_kernel<16, 4>), grid, dim3(1024), st, p);
+    if (n <= 4096) SG_LAUNCH((sort_kernel<4, 1, 1>), grid, dim3(256), st, p);
+    else SG_LAUNCH((sort_kernel<16, 2, 4>), grid, dim3(1024), st, p);
     return status_of(hipGetLastError());
 }
 

@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
 // table between work-groups and no atomics.  Wave w owns one run of the ids, in order, so the
 // ranks are the order of the places.  Grid y divides the second walk, the one that writes.
 // What bounds it is the walk of one work-group over all ids: 64 experts (MI355X): 1024 ids 2.9 us,
-// 16384 5.7 us, 65536 10.0 us (1.3 us for the 0.8 MB at the rate of a copy, and the launch).
+// 16384 5.0 us, 65536 9.4 us (0.2 us for the 0.8 MB at the rate of a copy, and the launch).
 // ---------------------------------------------------------------------------
 typedef int32_t i32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
@@ -805,8 +805,9 @@ __device__ __forceinline__ void sort_load(const SortParams& p, int i, int lane, 
             v[d][j] = at + 256 * d + j < last ? min((uint32_t)x[d][j], none) : ~0u;
 }
 
-// A wave takes DEEP pieces of 256 ids at a time, so that as many loads are under way.
-template <int WAVES, int DEEP>
+// A wave counts COUNT pieces of 256 ids at a time and writes DEEP, so that as many loads are under way
+// (65536 ids of 64 experts: 4 and 2 9.4 us, 4 and 4 10.1 us, 16 and 4 10.1 us).
+template <int WAVES, int DEEP, int COUNT>
 __global__ void __launch_bounds__(64 * WAVES) sort_kernel(const SortParams p) {
     __shared__ int below[WAVES], equal[WAVES];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -821,17 +822,18 @@ __global__ void __launch_bounds__(64 * WAVES) sort_kernel(const SortParams p) {
     // counts of each lane: two vector instructions an id and count, where a ballot and its bits
     // counted keep the scalar unit busy (65536 ids of 64 experts: 20.9 us)
     int lt = 0, eq = 0, ahead = 0;
-    for (int i = first; i < last; i += STEP) {
-        uint32_t v[DEEP][4];
-        if (i == begin) ahead = eq;
-        sort_load<DEEP>(p, i, lane, last, none, v);
+    for (int i = first; i < last; i += 256 * COUNT) {
+        uint32_t v[COUNT][4];
+        sort_load<COUNT>(p, i, lane, last, none, v);
 #pragma unroll
-        for (int d = 0; d < DEEP; ++d)
+        for (int d = 0; d < COUNT; ++d) {
+            if (d % DEEP == 0 && i + 256 * d == begin) ahead = eq;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 lt += v[d][j] < e;
                 eq += v[d][j] == e;
             }
+        }
     }
     lt = __builtin_amdgcn_readlane(lane_scan(lt), 63);
     eq = __builtin_amdgcn_readlane(lane_scan(eq), 63);
