@@ -268,6 +268,33 @@ def test_nan_stays_in_its_row_and_column():
         assert torch.isfinite(C[:, [c for c in range(40) if c != 7]]).all()
 
 
+@pytest.mark.parametrize("cfg", range(7))
+@pytest.mark.parametrize("group,K", [(128, 700), (32, 513), (64, 1280)])
+def test_nan_stays_in_its_row_and_column_of_every_tile(group, K, cfg, monkeypatch):
+    """Rows of NaN and infinity, a NaN scale in the last group: every other output is bit for bit what it
+    is without them."""
+    import swiglu_gemm_amd as sg
+    monkeypatch.setenv("SG_FORCE_INT4", str(cfg))
+    g = torch.Generator().manual_seed(K + cfg)
+    M, N = 67, 141
+    for dtype in HALF.values():
+        w = weight(g, N, K, group, dtype, True)
+        A = torch.randn(M, K, generator=g).to(dtype)
+        outs = []
+        for bad in (False, True):
+            if bad:
+                w[1][77, -1] = NAN
+                A[3, K - 1], A[30, 0], A[64, K // 2] = NAN, INF, -INF
+            codes, scales, zeros = layouts([w], group, False)
+            outs.append(sg.int4_gemm(A.cuda(), codes, scales, torch.empty(M, N, dtype=dtype, device="cuda:0"),
+                                     zeros=zeros, group=group).cpu())
+        clean, C = outs
+        rows = [r for r in range(M) if r not in (3, 30, 64)]
+        columns = [c for c in range(N) if c != 77]
+        assert torch.isnan(C[3]).all() and torch.isnan(C[:, 77]).all() and not torch.isfinite(C[[30, 64]]).any()
+        assert torch.equal(C[rows][:, columns], clean[rows][:, columns])
+
+
 def test_no_depth_and_no_rows():
     import swiglu_gemm_amd as sg
     dev = dict(device="cuda:0", dtype=torch.float16)
