@@ -18,46 +18,45 @@ namespace {
 bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128; }
 bool half_type(int dtype) { return dtype == SG_F16 || dtype == SG_BF16; }
 
-// The tiles go by the 16 x 16 columns-by-rows pieces of the product (the rows of each expert are not
-// known here: their mean stands for them, a run of n rows making n / 16 + 1/2 pieces, at least one).
-// Measured with every tile forced (MI355X, bf16, groups of 128, weights cold):
-//   up to 256 pieces, one to a work-group of 8 waves: 1 row, 4096 x 4096: 4.9 us, 5.8 us two by two;
-//   up to 512, two: 32 rows, 4096 x 4096: 8.2 against 11.6 us one by one and 8.7 us by threes;
-//   up to 768, three: 1 row, 11008 x 4096: 7.2 against 7.9 us one by one and 8.2 us by twos;
-//   up to 1024, four to 4 waves: 8 rows, 16384 x 2048: 6.6 against 7.7 us by twos;
-//   up to 8192, six to 4 waves: 16 rows, 22016 x 4096: 14.7 against 18.6 us by fours and 19.0 us by
-//   twos; 96 rows, 11008 x 4096: 26.8 against 32.1 us by fours; then four again: 256 rows of 64
-//   experts, 2816 x 2048: 47.0 against 51.2 us by sixes.
-// From K = 512 on, 64-row tiles that have a CU each are divided in two along K: 512 rows, 4096 x
-// 4096: 28.2 against 33.0 us; K = 1024: 13.9 and 14.5 us; K = 256: 9.6 and 9.1 us; where tiles share
-// a CU it only costs (256 rows, 11008 x 4096: 51.6 against 44.9 us).
-// What decides between 16-row pieces and 64-row tiles are the times fitted to such runs, which stay
-// within a tenth of them for K from 128 to 11008.  They put 64-row tiles ahead from about 100 rows
-// of one weight (11008 x 4096: 96 rows 27.2 against 26.8 us, 128 rows 27.2 against 33.0 us; 4096 x
-// 4096: 256 rows 27.1 against 26.9 us, 320 rows 27.1 against 32.8 us) and 32 rows of each of 64
-// experts (2816 x 2048: 74.2 against 83.7 us; 16 rows each: 67 against 56 us).
+// The configuration with the least time after the figures beside it (the rows of each expert are not
+// known here: their mean stands for them, a run of n rows making n / bm + 1/2 tiles, at least one).
+// They were fitted to every configuration forced on some 120 products (MI355X, weights cold); on 50
+// others the choice takes 1.03 of the best in the mean, 1.2 at most.  Both sides where it turns (us; bf16,
+// groups of 128, rows x K by N):
+//   strips of 16 or 32 columns: 1 x 4096 by 4096 4.9, 5.7;  32 x 4096 by 4096 11.6, 8.2
+//   32 or 48: 1 x 4096 by 11008 8.2, 7.2;  48 or 64: 96 x 2048 by 2048 9.9, 6.8
+//   64 or 96: 96 x 4096 by 4096 15.2, 18.2;  16 x 4096 by 22016 18.5, 14.7
+//   16-row strips or 32-row tiles in two parts of K: 128 x 4096 by 4096 15.8, 18.5; 192 rows 21.1, 18.9;
+//   those, or whole: 256 x 4096 by 4096 19.1, 23.1; 256 x 4096 by 11008 41.1, 39.3
+//   32-row or 64-row tiles in two parts: 256 x 4096 by 4096 19.1, 26.3; 512 x 11008 by 4096 67.1, 60.7
+//   32-row or 64-row tiles: 384 x 4096 by 11008 61.4, 58.3; 32 rows of each of 64 experts 66.0, 69.6
+// Not fitted but measured: up to 16 rows in the mean no tile of more rows is taken (16 x 4096 by 22016
+// 14.7, tiles 16.7), and 96-column strips only for one weight (98 rows of 32 experts, 1024 by 2816, 15.4
+// by 64 columns and 23.7; 320 rows of 64, 4096 by 1024, 31.9 and 34.9).
 int choose(const GroupedParams& q) {
     if (const char* s = std::getenv("SG_FORCE_INT4")) {
         const int c = std::atoi(s);
         if (*s && c >= 0 && c < kNumInt4Cfg) return c;
     }
     const double runs = q.experts < q.rows ? q.experts : q.rows, mean = q.rows / runs;
-    const double strips = (double)cdiv(q.g.N, 16), tiles_k = (double)cdiv(q.g.K, 128);
-    auto high = [&](int bm) {
-        return q.experts == 1 ? (double)cdiv(q.rows, bm) : runs * std::fmax(1.0, mean / bm + 0.5);
-    };
-    const double pieces = high(16) * strips;
-    const double rounds = std::ceil(high(64) * cdiv(q.g.N, 128) / 256.0);
-    const bool parts = rounds <= 1.0 && tiles_k >= 4.0;
-    const double many = parts          ? 8.5 + 0.6 * tiles_k
-                        : rounds > 1.0 ? 6.0 + tiles_k * (0.62 * rounds - 0.05)
-                                       : 7.0 + 0.8 * tiles_k;
-    const double few = 3.9 + (0.6 + 0.155 * tiles_k) * pieces / 1024.0;
-    if (mean > 16.0 && many < few) return parts ? 6 : 5;
-    if (pieces <= 256.0) return 0;
-    if (pieces <= 512.0) return 1;
-    if (pieces <= 768.0) return 2;
-    return pieces <= 1024.0 || pieces > 8192.0 ? 3 : 4;
+    const double tiles_k = (double)cdiv(q.g.K, 128);
+    int best = 0;
+    double least = INFINITY;
+    for (int i = 0; i < (mean > 16.0 ? kNumInt4Cfg : kNumInt4Few); ++i) {
+        const Int4Cfg& c = kInt4Cfg[i];
+        if (c.NT == 6 && q.experts > 1) continue;
+        const int bm = 16 * c.MT;
+        const double high = q.experts == 1 ? (double)cdiv(q.rows, bm)
+                                           : runs * std::fmax(1.0, mean / bm + 0.5);
+        const double rounds = std::ceil(high * cdiv(q.g.N, 16 * c.NT) / 256.0);
+        const double t = c.start + rounds * c.round +
+                         tiles_k * (rounds > 1.0 ? rounds * c.per + c.more : c.first);
+        if (t < least) {
+            least = t;
+            best = i;
+        }
+    }
+    return best;
 }
 
 int run_product(const char* what, int64_t experts, const int32_t* offsets, const int32_t* order,

@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows: 64 rows x 128 columns a work-group, the columns divided over its four waves, so that
-// each code is loaded and widened once and meets 64 rows, on 32 x 32 x 16 products: their operands
+// Many rows: 32 MT rows x 128 columns a work-group, the columns divided over its four waves, so that
+// each code is loaded and widened once and meets all rows, on 32 x 32 x 16 products: their operands
 // keep the vector unit, which widens the codes, from issuing for less time than those of four times
 // as many 16 x 16 x 32 ones.  A wave takes two strips of 16 columns together: lane 32 h + n loads
 // the pieces q = h and q = 2 + h of row n of the two.  The activations pass through LDS, three tiles
@@ -376,17 +376,17 @@ __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
 // of 64 with zero points, 57.6 us so and 52.3 us this way; 128 x 4096 by 11008, groups of 128, 33.2
 // and 32.2; 512 rows of the latter and groups of 32 the same both ways.)
 // KS = 2: eight waves, four for each half of K, joined through LDS, for grids that leave a CU one
-// work-group, whose waves would wait for their own operands: 1.0 us a step of 128 along K alone, 1.4
-// us for two work-groups' or two halves' steps.
-// Measured (MI355X, bf16, groups of 128): 512 x 4096 by 11008 63.8 us, 720 TFLOP/s, against 140 us
-// with 16-row pieces.  What bounds it is issue, not memory or the matrix unit: a wave's step is 18
-// products of 16 ns and 140 vector instructions, each of which the SIMD's other wave waits for.
+// work-group, whose waves would wait for their own operands.
+// Measured (MI355X, bf16, groups of 128): 512 x 4096 by 11008 62 us, 745 TFLOP/s (MT = 2; 103 us with
+// 16-row strips); 256 x 4096 by 4096 19.1 us (MT = 1, KS = 2; 25.7 us with 16-row strips, 31.7 us with
+// MT = 2, KS = 1).  What bounds it is issue, not memory or the matrix unit: with MT = 2 a wave's step is
+// 18 products of 16 ns, 140 vector instructions and 20 KB read from LDS, none of which is hidden whole.
 // Longer look-ahead on the codes and activations (2 tiles more: 5% faster alone on a CU, 8% slower
 // shared), on LDS (3 products: slower) and 256 columns (spills) did not pay.
 // ---------------------------------------------------------------------------
-template <int DT, int GROUP, bool ZEROS, int KS>
+template <int DT, int GROUP, bool ZEROS, int MT, int KS>
 __global__ void __launch_bounds__(256 * KS, 2) int4_tile_kernel(const Int4Params x) {
-    constexpr int MT = 2, BM = 64, BN = 128, PER = 128 / GROUP, STEPS = 2 * GROUP / 32;
+    constexpr int BM = 32 * MT, BN = 128, PIECES = BM / 16, PER = 128 / GROUP, STEPS = 2 * GROUP / 32;
     constexpr bool SUMS = DT == DT_BF16;
     typedef Int4Tile<GROUP, ZEROS> Tile;
     __shared__ u32x4 all_lds[KS][3][BM * 16];
@@ -406,11 +406,11 @@ __global__ void __launch_bounds__(256 * KS, 2) int4_tile_kernel(const Int4Params
     const Int4Strip strip = {
         x.codes + it.e * x.s_codes + (int64_t)tn * x.tiles_k * 1024 + 16 * (16 * lh + lr),
         x.zeros + at, x.scales + at};
-    // this thread's piece of 8 columns in rows srow, srow + 16, srow + 32 and srow + 48
+    // this thread's piece of 8 columns in rows srow, srow + 16, ...
     const int srow = tid >> 4, spiece = tid & 15;
-    const uint16_t* row[4];
+    const uint16_t* row[PIECES];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < PIECES; ++i) {
         int r = it.row0 + min(it.m0 + 16 * i + srow, it.rows - 1);
         if (x.order) r = min(max(x.order[r] / x.top_k, 0), x.T - 1);
         row[i] = q.g.A + (int64_t)r * q.g.lda + 8 * spiece;
@@ -418,15 +418,15 @@ __global__ void __launch_bounds__(256 * KS, 2) int4_tile_kernel(const Int4Params
     const int spot = srow * 16 + (spiece ^ srow);
     const Int4Magic magic = int4_magic<DT>();
     f32x16 sum[MT] = {};
-    u32x4 stage[4];
+    u32x4 stage[PIECES];
     auto load_stage = [&](int kt) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < PIECES; ++i)
             stage[i] = *reinterpret_cast<const u32x4_a2*>(row[i] + (int64_t)kt * 128);
     };
     auto store_stage = [&](u32x4* buf) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) buf[spot + 256 * i] = stage[i];
+        for (int i = 0; i < PIECES; ++i) buf[spot + 256 * i] = stage[i];
     };
     // t: pieces q = h; more: pieces q = 2 + h
     Tile t[2];
@@ -435,8 +435,9 @@ __global__ void __launch_bounds__(256 * KS, 2) int4_tile_kernel(const Int4Params
         int4_load(t[to], strip, 0, kt);
         more[to] = *reinterpret_cast<const u32x4*>(strip.codes + (int64_t)kt * 1024 + 512);
     };
-    // Minus the group sums of this wave's 16 rows.
+    // Minus the group sums of this wave's 16 rows (32 rows: the first two waves').
     auto add_up = [&](f32x4* to, const u32x4* buf) {
+        if (PIECES < 4 && wave >= PIECES) return;
         const uint32_t c = 0xBF80BF80u;                          // -1, twice
 #pragma unroll
         for (int p = 0; p < PER; ++p) {
@@ -577,7 +578,7 @@ __global__ void __launch_bounds__(256 * KS, 2) int4_tile_kernel(const Int4Params
     if (K % 128 != 0) {
         load_codes(even, full);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < PIECES; ++i)
             stage[i] = int4_act(row[i] - 8 * spiece, full * 128 + 8 * spiece, K);
         t[0].cut(K - full * 128);
         __syncthreads();                  // the sums of the last whole tile are read
@@ -597,17 +598,17 @@ __global__ void __launch_bounds__(256 * KS, 2) int4_tile_kernel(const Int4Params
     }
     if constexpr (KS > 1) {
         // the second part's sums reach the first through LDS
-        f32x4* pass = reinterpret_cast<f32x4*>(all_lds) + 8 * (wave * 64) + lane;
+        f32x4* pass = reinterpret_cast<f32x4*>(all_lds) + 4 * MT * (wave * 64) + lane;
         __syncthreads();
         if (part == 1)
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
+            for (int v = 0; v < 4 * MT; ++v)
                 pass[64 * v] = f32x4{sum[v / 4][4 * (v % 4)], sum[v / 4][4 * (v % 4) + 1],
                                      sum[v / 4][4 * (v % 4) + 2], sum[v / 4][4 * (v % 4) + 3]};
         __syncthreads();
         if (part == 1) return;
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
+        for (int v = 0; v < 4 * MT; ++v) {
             const f32x4 d = pass[64 * v];
 #pragma unroll
             for (int r = 0; r < 4; ++r) sum[v / 4][4 * (v % 4) + r] += d[r];
@@ -812,25 +813,32 @@ __global__ void __launch_bounds__(256) int4_dequantize_kernel(const Int4PackPara
     }
 }
 
-// Configurations of the product: rows and columns of a work-group in tiles of 16, and its waves.
+// Configurations of the product: rows and columns of a work-group in tiles of 16, and its waves; then
+// what one takes in us, for the choice: start + rounds * round + tiles of K * (first, where there is
+// one round of 256 work-groups, else rounds * per + more).
 // Index = configuration id (SG_FORCE_INT4=<id> overrides the choice).
 struct Int4Cfg {
     int MT, NT, NW;
+    double start, round, first, per, more;
     const char* name;
 };
-#define SG_INT4_FEW(X) \
-    X(0, 1, 1, 8)      \
-    X(1, 1, 2, 8)      \
-    X(2, 1, 3, 8)      \
-    X(3, 1, 4, 4)      \
-    X(4, 1, 6, 4)
-#define SG_INT4_MANY(X) \
-    X(5, 4, 8, 4)       \
-    X(6, 4, 8, 8)
-#define SG_INT4_ROW(ID, MT, NT, NW) {MT, NT, NW, #MT "x" #NT " " #NW "w"},
+#define SG_INT4_FEW(X)                                \
+    X(0, 1, 1, 8, 3.0, 0.5, 0.107, 0.107, 0.0)        \
+    X(1, 1, 2, 8, 2.5, 1.0, 0.138, 0.138, 0.0)        \
+    X(2, 1, 3, 8, 2.2, 1.4, 0.155, 0.155, 0.0)        \
+    X(3, 1, 4, 4, 4.1, 0.4, 0.154, 0.154, 0.0)        \
+    X(4, 1, 6, 4, 4.8, 0.5, 0.193, 0.193, 0.0)
+#define SG_INT4_MANY(X)                               \
+    X(5, 4, 8, 4, 6.0, 1.3, 0.79, 0.555, 0.0)         \
+    X(6, 4, 8, 8, 7.2, 1.3, 0.60, 0.70, -0.08)        \
+    X(7, 2, 8, 8, 5.6, 0.65, 0.40, 0.34, 0.03)        \
+    X(8, 2, 8, 4, 5.0, 0.65, 0.545, 0.31, 0.10)
+#define SG_INT4_ROW(ID, MT, NT, NW, START, ROUND, FIRST, PER, MORE) \
+    {MT, NT, NW, START, ROUND, FIRST, PER, MORE, #MT "x" #NT " " #NW "w"},
 constexpr Int4Cfg kInt4Cfg[] = {SG_INT4_FEW(SG_INT4_ROW) SG_INT4_MANY(SG_INT4_ROW)};
 #undef SG_INT4_ROW
 constexpr int kNumInt4Cfg = sizeof(kInt4Cfg) / sizeof(kInt4Cfg[0]);
+constexpr int kNumInt4Few = 5;                           // those of SG_INT4_FEW
 
 template <int DT, bool ZEROS>
 hipError_t launch_int4(int group, int cfg, const Int4Params& x, unsigned blocks, hipStream_t st);

@@ -8,15 +8,15 @@ namespace sg {
 
 template <int DT, bool ZEROS, int GROUP>
 hipError_t launch_int4_group(int cfg, const Int4Params& x, unsigned blocks, hipStream_t st) {
-#define SG_INT4_CASE(ID, MT, NT, NW)                                                   \
-    case ID:                                                                           \
-        hipLaunchKernelGGL((int4_kernel<DT, GROUP, ZEROS, MT, NT, NW>), dim3(blocks),  \
-                           dim3(64 * NW), 0, st, x);                                   \
+#define SG_INT4_CASE(ID, MT, NT, NW, ...)                                           \
+    case ID:                                                                        \
+        hipLaunchKernelGGL((int4_kernel<DT, GROUP, ZEROS, MT, NT, NW>),             \
+                           dim3(blocks), dim3(64 * NW), 0, st, x);                  \
         return hipGetLastError();
-#define SG_INT4_TILE(ID, MT, NT, NW)                                                   \
-    case ID:                                                                           \
-        hipLaunchKernelGGL((int4_tile_kernel<DT, GROUP, ZEROS, NW / 4>), dim3(blocks),  \
-                           dim3(64 * NW), 0, st, x);                                   \
+#define SG_INT4_TILE(ID, MT, NT, NW, ...)                                           \
+    case ID:                                                                        \
+        hipLaunchKernelGGL((int4_tile_kernel<DT, GROUP, ZEROS, MT / 2, NW / 4>),    \
+                           dim3(blocks), dim3(64 * NW), 0, st, x);                  \
         return hipGetLastError();
     switch (cfg) {
         SG_INT4_FEW(SG_INT4_CASE)

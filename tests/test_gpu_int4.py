@@ -268,7 +268,7 @@ def test_nan_stays_in_its_row_and_column():
         assert torch.isfinite(C[:, [c for c in range(40) if c != 7]]).all()
 
 
-@pytest.mark.parametrize("cfg", range(7))
+@pytest.mark.parametrize("cfg", range(9))
 @pytest.mark.parametrize("group,K", [(128, 700), (32, 513), (64, 1280)])
 def test_nan_stays_in_its_row_and_column_of_every_tile(group, K, cfg, monkeypatch):
     """Rows of NaN and infinity, a NaN scale in the last group: every other output is bit for bit what it
@@ -309,7 +309,7 @@ def test_no_depth_and_no_rows():
     sg.int4_swiglu_gemm(torch.empty(0, 128, **dev), codes, scales, torch.empty(0, 8, **dev))
 
 
-@pytest.mark.parametrize("cfg", range(7))
+@pytest.mark.parametrize("cfg", range(9))
 @pytest.mark.parametrize("dtype", sorted(HALF))
 def test_every_tile(dtype, cfg, monkeypatch):
     """Each tile forced on sizes that end inside it: rows, columns, depth, runs and groups."""
@@ -330,12 +330,12 @@ def test_every_tile(dtype, cfg, monkeypatch):
 
 
 def test_the_choice_of_tiles():
-    """One piece to a work-group, then more columns, then 64-row tiles, in two parts along K while each
-    has a CU, as the products grow."""
+    """One piece to a work-group, then more columns, then 32-row tiles in two parts along K, 64-row ones, and
+    tiles that are whole along K, as the products grow."""
     import swiglu_gemm_amd as sg
     dev = dict(device="cuda:0", dtype=torch.bfloat16)
-    for M, N, want in ((1, 4096, 0), (1, 8192, 1), (1, 11008, 2), (1, 16384, 3), (16, 22016, 4), (1, 140000, 3),
-                       (512, 4096, 6), (512, 11008, 5), (32, 1024, 0)):
+    for M, N, want in ((1, 4096, 0), (1, 8192, 1), (1, 11008, 2), (1, 16384, 3), (16, 22016, 4), (32, 1024, 0),
+                       (256, 4096, 7), (512, 4096, 6), (256, 11008, 8), (512, 11008, 5)):
         nc, ns = sg.int4_shapes(N, 4096)
         sg.int4_gemm(torch.zeros(M, 4096, **dev), torch.zeros(nc, device="cuda:0", dtype=U8), torch.zeros(ns, **dev),
                      torch.empty(M, N, **dev))
