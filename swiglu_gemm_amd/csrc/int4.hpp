@@ -133,8 +133,8 @@ struct Int4Tile {
             if (p * GROUP >= columns) f[p / 2] &= p % 2 ? 0x0000FFFFu : 0u;
     }
 };
-// A strip of 16 columns: the same addresses in every lane, so that a load takes its base from
-// scalar registers and only the lane's offset from a vector one.
+// A strip of 16 columns.  For few rows: the same addresses in every lane, so that a load takes its
+// base from scalar registers and only the lane's offset from a vector one.
 struct Int4Strip {
     const uint8_t *codes, *zeros;
     const uint16_t* scales;
