@@ -93,7 +93,7 @@ __device__ __forceinline__ float log_score(int scoring, float x) {
 __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
 
 constexpr double kNone = -__builtin_huge_val();
-constexpr double kNanKey = -1e300;        // a NaN logit: behind every number
+constexpr double kNanKey = -1e300;        // a NaN logit: behind every number, in front of none
 
 // Lane j < top_k holds place j of token t: its expert (-1: none) and logit x; top and total: the row's
 // largest logit and the sum of e^(x - top), where softmax is not renormalised.
@@ -149,34 +149,33 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
     double key[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) key[i] = x[i] != x[i] ? kNanKey : (double)x[i];
-    const bool scores = (p.bias || p.groups > 1) && !bad;
-    if (scores || p.groups > 1) {
+    if (p.bias || p.groups > 1) {
+        // scores of the row without its NaN logits; infinite ones share softmax's whole
         double c[NV];
-        if (scores) {
-            if (p.scoring == ROUTE_SOFTMAX) {
-                double sum = 0.0;
-#pragma unroll
-                for (int i = 0; i < NV; ++i) {
-                    c[i] = x[i] == -inf ? 0.0 : exp((double)x[i] - (double)top);
-                    sum += c[i];
-                }
-                sum = wave_sum(sum);
-#pragma unroll
-                for (int i = 0; i < NV; ++i) c[i] /= sum;
-            } else {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) c[i] = 1.0 / (1.0 + exp(-(double)x[i]));
-            }
+        if (p.scoring == ROUTE_SOFTMAX) {
+            double sum = 0.0;
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int e = lane + 64 * i;
-                if (p.bias && e < p.E) c[i] += (double)p.bias[e];
-                if (x[i] == -inf || c[i] != c[i]) c[i] = kNone;
-                if (p.bias) key[i] = c[i];
+                c[i] = !(x[i] > -inf) ? 0.0
+                       : top == inf   ? (double)(x[i] == inf)
+                                      : exp((double)x[i] - (double)top);
+                sum += c[i];
             }
+            sum = wave_sum(sum);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) c[i] /= sum;
         } else {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) c[i] = key[i];
+            for (int i = 0; i < NV; ++i) c[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int e = lane + 64 * i;
+            if (x[i] != x[i]) c[i] = 0.0;
+            if (p.bias && e < p.E) c[i] += (double)p.bias[e];
+            if (x[i] == -inf || c[i] != c[i]) c[i] = kNone;
+            if (x[i] != x[i] && c[i] != kNone) c[i] = kNanKey;
+            if (p.bias) key[i] = c[i];
         }
         if (p.groups > 1) {
 #pragma unroll
@@ -192,7 +191,7 @@ __device__ __forceinline__ void route_token(const RouteParams& p, int t, int lan
                     b = fmax(b, fmin(a, v));
                     a = fmax(a, v);
                 }
-                value = p.group_top == 2 && b != kNone ? a + b : a;
+                value = p.group_top == 2 && b > kNanKey ? a + b : a;
             }
             int rank = 0;
             for (int g = 0; g < p.groups; ++g) {
