@@ -458,8 +458,11 @@ typedef enum { SG_ROUTE_SOFTMAX = 0, SG_ROUTE_SIGMOID = 1 } sg_route_scoring;
  * computed in fp32 (renormalised ones from the chosen experts' log scores, so that they do
  * not underflow all together).
  * A logit of -infinity, or a bias of -infinity or NaN, keeps the expert from being chosen; where
- * fewer than top_k are left, the places behind get id -1 and weight 0.  A NaN logit is not chosen
- * and makes the weights of the token's chosen experts NaN, as does, with softmax, +infinity.
+ * fewer than top_k are left, the places behind get id -1 and weight 0.  NaN logits come behind every
+ * number: their experts are chosen where the others run out, the lowest index first, and count in
+ * their group only where it has no other.  The others' scores are those of the row without them;
+ * logits of +infinity share softmax's whole.  The weights of the experts chosen in a row with a NaN
+ * logit, or with softmax with +infinity, are NaN.
  *  1 X, 2 ldx   T x E logits.   3 T (0..2^30)   4 E (1..SG_ROUTE_MAX_EXPERTS)
  *  5 dtype   of X: SG_F32, SG_F16, SG_BF16.   6 top_k   1..min(E, SG_ROUTE_MAX_TOP_K).
  *  7 scoring   sg_route_scoring.   8 bias   NULL, or E fp32 values.
@@ -481,7 +484,8 @@ int sg_route_experts(const void* X, int64_t ldx, int64_t T, int64_t E, int dtype
  *     softmax            dx[e] = s_e * (G_e - sum G p), G_e = 0 where e is not chosen
  *     sigmoid            dx[id] = G s (1 - s); 0 elsewhere
  * in fp32, rounded once.  Ids outside 0..E-1 are empty places; a row of empty places gets
- * zeros and is not read.
+ * zeros and is not read.  Renormalised and sigmoid gradients read the chosen logits alone: a NaN
+ * elsewhere in the row does not show in them.
  *  1 X, 2 ldx, 3 T, 4 E, 5 dtype, 6 top_k, 7 scoring   as the forward.   8 renormalize
  *  9 scale   10 ids, 11 dweights   T x top_k.   12 dX, 13 lddx   T x E of X's type.  14 stream.
  */

@@ -967,7 +967,8 @@ def route_experts(X, top_k: int, scoring: str = "softmax", bias=None, groups: in
     group_top (1 or 2) best have the largest sum; renormalize: the weights of a token sum to 1;
     scale multiplies them.  Equal values go to the lowest index.  mask: None or bool [T], tokens
     where it is False get id -1 and weight 0 and are not read; so do places for which no expert is
-    left (a logit of -inf takes one out).  ids, weights: tensors to write."""
+    left (a logit of -inf takes one out).  NaN logits come last and make their token's weights NaN, as
+    +inf does with softmax.  ids, weights: tensors to write."""
     code = _row_type(X, "X")
     how = SCORINGS.get(scoring)
     if how is None:

@@ -105,3 +105,30 @@ def test_choice_with_nan(scoring, E, groups, top_groups, k):
             check(X, k, scoring=scoring, bias=b)
             for top in (1, 2):
                 check(X, k, scoring=scoring, bias=b, groups=groups, top_groups=top_groups, group_top=top)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("E,k", [(40, 4), (300, 10)])
+def test_gradient_with_nan(E, k):
+    """Renormalised and sigmoid gradients read the chosen logits alone; the softmax's own reads the row."""
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import routing_reference as ref
+    from experts_reference import check
+    import swiglu_gemm_amd as sg
+    g = torch.Generator().manual_seed(E)
+    X = torch.randn(6, E, generator=g)
+    dw = torch.randn(6, k, generator=g)
+    ids = ref.route(X, k)[0]
+    bad = X.clone()
+    for t in range(1, 6):
+        free = [e for e in range(E) if e not in ids[t].tolist()]
+        bad[t, free[t]] = NAN
+    for scoring, renormalize in (("softmax", True), ("sigmoid", True), ("sigmoid", False), ("softmax", False)):
+        dX = sg.route_experts_bwd(bad.cuda(), ids.cuda(), dw.cuda(), torch.empty(6, E, device="cuda:0"),
+                                  scoring=scoring, renormalize=renormalize)
+        want, tol = ref.route_bwd(X, ids, dw, scoring, renormalize, 1.0)
+        if scoring == "softmax" and not renormalize:
+            assert torch.isnan(dX[1:]).all()
+            dX, want, tol = dX[:1], want[:1], tol[:1]
+        check(dX, want, tol, "%s %s" % (scoring, renormalize))
