@@ -441,8 +441,10 @@ int sg_mxfp4_swiglu_gemm(int64_t experts, const int32_t* offsets, int64_t M, int
  * and back.  A token's place (t, j), j < top_k, is its j-th expert; flat, place t * top_k + j.
  * These calls allocate nothing and use no workspace; results are run-to-run identical.
  * Any element-aligned pointers and leading dimensions are accepted.  No result may overlap an
- * input (sg_combine_rows: out may be the residual).  Calls of more than 2^26 tokens, or of rows
- * that need as many threads, return hipErrorInvalidConfiguration.
+ * input (sg_combine_rows: out may be the residual).  Calls that need 2^32 threads return
+ * hipErrorInvalidConfiguration: more than 2^26 - 4 tokens of the router or its gradient, or places of
+ * combining's gradient; rows (of spreading and combining) from 2^24 on of more than 1024 elements, shorter
+ * ones in proportion.
  */
 typedef enum { SG_ROUTE_SOFTMAX = 0, SG_ROUTE_SIGMOID = 1 } sg_route_scoring;
 #define SG_ROUTE_MAX_EXPERTS 1024
