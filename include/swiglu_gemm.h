@@ -573,10 +573,10 @@ int sg_combine_rows_bwd(const void* dOut, int64_t lddo, const void* Z, int64_t l
  * sg_int4_quantize: the codes of W.  For each group, without zeros: scale = max |w| / 7, codes
  * w / scale + 8; with zeros: lo = min(0, w), hi = max(0, w), scale = (hi - lo) / 15, zero =
  * -lo / scale and codes w / scale + zero.  The scale is computed in fp32 and rounded to its type
- * first; zeros and codes follow from the rounded one, to the nearest integer, ties to even,
- * saturating at 0 and 15.  A group of zeros, or whose scale rounds to 0, gets scale 0, zero 8
- * and codes 8.  An infinity or a NaN, or a scale past its type's range, makes the group's scale
- * NaN (zero and codes 8).
+ * first; zeros and codes follow from the rounded one: each quotient is rounded to the nearest integer,
+ * ties to even, before the zero point (or 8) is added, and what comes out saturates at 0 and 15.
+ * A group of zeros, or whose scale rounds to 0, gets scale 0, zero 8 and codes 8.  An infinity or a
+ * NaN, or a scale past its type's range, makes the group's scale NaN (zero and codes 8).
  *  1 W, 2 ldw, 3 strideW   `batch` weights N x K, strideW elements apart.   4 batch (0..65535)
  *  5 N, 6 K   >= 0.   7 dtype   of W: SG_F32, SG_F16 or SG_BF16.   8 group.
  *  9 codes (16-byte aligned), 10 scales (8), 11 zeros (4; NULL: none).
