@@ -759,8 +759,9 @@ __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
 // expert, which behave as expert `experts`.  Every work-group reads all ids: no second launch, no
 // table between work-groups and no atomics.  Wave w owns one run of the ids, in order, so the
 // ranks are the order of the places.  Grid y divides the second walk, the one that writes.
-// What bounds it is the walk of one work-group over all ids: 64 experts (MI355X): 1024 ids 2.9 us,
-// 16384 5.0 us, 65536 9.4 us (0.2 us for the 0.8 MB at the rate of a copy, and the launch).
+// What bounds it is the latency of one work-group's walk over all ids (of a wave's cycles six in ten wait;
+// the vector unit is busy for four): 64 experts (MI355X): 1024 ids 2.9 us, 16384 5.0 us, 65536 9.4 us
+// (0.2 us for the 0.8 MB at the rate of a copy, and the launch).
 // ---------------------------------------------------------------------------
 typedef int32_t i32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
