@@ -1,5 +1,6 @@
-"""The largest calls of the routing operators: one launch has fewer than 2^32 threads along a side, so a
-call that needs more is refused before it starts (no GPU is used for that), and the largest that fits runs."""
+"""The largest calls of the routing operators and of 4-bit integer weights: one launch has fewer than 2^32
+threads along a side, and a product at most 2^22 work-groups, so a call that needs more is refused before it
+starts (no GPU is used for that), and the largest that fits runs."""
 import ctypes
 
 import pytest
@@ -32,6 +33,15 @@ def test_calls_past_the_largest_launch_are_refused(L):
     # the gradient of combining: 64 threads a place
     for T, k in ((2**24, 4), (TOKENS + 1, 1), (2**20, 64), (2**30, 65536)):
         assert L.sg_combine_rows_bwd(P, 8, P, 8, 8, 8, T, 2, P, k, P, P, 8, P, NUL) == TOO_MANY
+
+
+def test_products_past_the_largest_launch_are_refused(L):
+    for M, N in ((2**20, 2**16), (2**18 + 1, 2**17), (2**30, 2**30), (64, 2**30)):
+        args = [1, NUL, NUL, 1, M, M, N, 128, 128]
+        ends = [P, 128, P, P, NUL, P, N]
+        assert L.sg_int4_gemm(*args, 1.0, *ends, 2, 2, NUL) == TOO_MANY
+        args[6] = N // 2
+        assert L.sg_int4_swiglu_gemm(*args, *ends, 2, NUL) == TOO_MANY
 
 
 @pytest.mark.gpu
