@@ -19,10 +19,12 @@ bool group_ok(int64_t group) { return group == 32 || group == 64 || group == 128
 bool half_type(int dtype) { return dtype == SG_F16 || dtype == SG_BF16; }
 
 // The configuration with the least time after the figures beside it (the rows of each expert are not
-// known here: their mean stands for them, a run of n rows making n / bm + 1/2 tiles, at least one).
-// They were fitted to every configuration forced on some 120 products (MI355X, weights cold); on 50
-// others the choice takes 1.016 of the best in the mean, 1.11 at most.  Both sides where it turns (us;
-// bf16, groups of 128, rows x K by N):
+// known here: their mean stands for them, a run of n rows making n / bm + 1/2 tiles, at least one; a
+// load that is not even can have a run many times the mean, whose weight 16-row strips read once for
+// each 16 rows).  They were fitted to every configuration forced on some 120 products (MI355X, weights
+// cold); on 48 products, most of them drawn at random, the choice takes 1.02 of the best in the mean, 1.19 at most (1000 rows of 64
+// experts, fp16, 2048 by 2816: 54.9 us by 16-row strips of 64 columns, 46.4 by 32-row tiles; next 1.12).
+// Both sides where it turns (us; bf16, groups of 128, rows x K by N):
 //   strips of 16 or 32 columns: 1 x 4096 by 4096 4.9, 5.7;  32 x 4096 by 4096 11.6, 8.2
 //   32 or 48: 1 x 4096 by 11008 8.2, 7.2;  48 or 64: 96 x 2048 by 2048 9.9, 6.8
 //   64 or 96: 96 x 4096 by 4096 15.2, 18.2;  16 x 4096 by 22016 18.5, 14.7

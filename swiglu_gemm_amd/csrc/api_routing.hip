@@ -17,8 +17,12 @@ constexpr int64_t kMaxSide = ((int64_t)1 << 24) - 1;
 #define SG_LAUNCH(KERNEL, GRID, BLOCK, ST, P) hipLaunchKernelGGL((KERNEL), GRID, BLOCK, 0, ST, P)
 
 // Up to 256 experts and 8 choices several tokens share a wave; else each has one.  fp32 logits, 8
-// choices: 1 token of 64 experts 3.4 against 3.5 us for one wave each, 16384 tokens 4.5 against 14.5
-// us (6 choices), of 256 experts 10.0 against 21.6 us.
+// choices: 1 token of 64 experts 3.3 against 3.4 us for one wave each, 16384 tokens 4.3 and 17.1 us, of
+// 256 experts 7.7 and 21.7 us, of 256 in 8 groups with a bias 14.2 and 36.1 us.  That is for logits
+// that differ.  Tokens whose order the lanes leave to 64 bits, or that have fewer than top_k experts
+// left, hold up their wave one after the other, which the sizes do not show: logits cast from
+// bf16 to fp32, 16384 tokens of 64 experts 13.3 and 18.5 us, of 256 experts 20.6 and 22.5 us, but 77 tokens
+// 12.7 and 5.3 us; 8 choices with 6 experts left, 16384 tokens of 256 30 and 20 us, of 8 131 and 17 us.
 template <int DT>
 void launch_route(const RouteParams& p, hipStream_t st) {
     const dim3 block(256);

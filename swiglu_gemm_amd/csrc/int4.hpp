@@ -252,10 +252,10 @@ __device__ __forceinline__ void int4_put(const Int4Params& x, int64_t row, int n
 // 128 along K and their sums meet in LDS, in the order of the waves.  A wave keeps a tile of codes
 // of each of its NT strips, and the activations of a tile, under way while it works on the one
 // before.  For few rows: what bounds it is the codes from memory.  Measured (MI355X, kernel alone,
-// weights cold): bf16, 1 x 4096 by 4096 4.9 us, most of it launch and one trip to memory; fp16, 16 x
-// 4096 by 22016 (SwiGLU, groups of 128 with zero points) 14.5 us, 47 MB, 3.2 TB/s; bf16, 256 rows of
-// 64 experts, 2048 by 2816 with zero points in groups of 64, 200 MB, 48.6 us in the mean, 45.1 at best,
-// 4.4 TB/s (a plain read: 5.66 TB/s).
+// weights cold): bf16, 1 x 4096 by 4096 5.0 us, most of it launch and one trip to memory; fp16, 16 x
+// 4096 by 22016 (SwiGLU, groups of 128 with zero points) 14.2 us, 48 MB, 3.4 TB/s; bf16, 256 rows of
+// 64 experts, 2048 by 2816 with zero points in groups of 64, 200 MB, 47.5 us in the mean, 44.6 at best,
+// 4.2 to 4.5 TB/s (a plain read: 5.66 TB/s).
 template <int DT, int GROUP, bool ZEROS, int MT, int NT, int NW>
 __global__ void __launch_bounds__(64 * NW) int4_kernel(const Int4Params x) {
     constexpr int BM = 16 * MT, BN = 16 * NT, PER = 128 / GROUP;
@@ -636,7 +636,8 @@ __global__ void __launch_bounds__(256 * KS, 2) int4_tile_kernel(const Int4Params
 // A group's extremes meet over the four lanes of a row.  Quantising computes in fp32 what decides, and
 // in 64 bits where the quotient is near a tie, so that codes are the formula's.  Measured (MI355X,
 // 11008 x 4096, groups of 128): quantised from bf16 39 us, 2.9 TB/s (by one thread a group, with a
-// division in 64 bits for each code: 986 us), packed 18.6 us, 3.6 TB/s, back to bf16 21 us, 5.4 TB/s.
+// division in 64 bits for each code: 986 us), bound by the vector unit: 822 instructions a wave, 70700
+// cycles of each SIMD, busy for 0.85 of the time; packed 18.6 us, 3.6 TB/s, back to bf16 21 us, 5.4 TB/s.
 // ---------------------------------------------------------------------------
 struct Int4PackParams {
     const void* W;              // quantise

@@ -255,13 +255,18 @@ __global__ void __launch_bounds__(256) route_kernel(const RouteParams p) {
 //   16-bit logits without a bias: the value is the logit itself, in an order of unsigned numbers.
 //   Otherwise 24 bits from the row's largest value down to its smallest (at most 64 below), of
 //   scores in fp32.  Where two values that decide are closer than what they may be off by (of the
-//   scores 2^-21 for sigmoid and 2^-18 of the largest for softmax), the few that are in question
-//   are compared in 64 bits, one a lane (0.1 % of tokens with random logits).  Groups that close and
-//   everything unusual (NaN, too few experts left) go through route_token.
+//   scores 2^-21 for sigmoid and 2^-18 of the largest for softmax), equal ones among them, the few
+//   that are in question are compared in 64 bits, one a lane, a token after the other: 0.1 % of the
+//   tokens with random fp32 logits, but 22 % (64 experts) and 39 % (256) with fp32 logits cast from
+//   bf16.  Groups that close and everything unusual (NaN, too few experts left) go through route_token.
 // What bounds it is the vector unit, not memory: 16384 tokens, top 8 (MI355X, in a graph), fp32 logits:
-//   64 experts (6 choices) 4.5 us, 0.9 TB/s; 256 experts 8.0 us, 2.1 TB/s;
-//   256 experts in 8 groups, sigmoid and bias 14.5 us (one wave a token in 64 bits 35 us).
-// 1 token of 64 experts 3.4 us, nearly all of it the launch.
+//   64 experts 4.3 us, 0.9 TB/s;
+//   256 experts 7.8 us, 2.2 TB/s: 819 vector instructions a wave, 13100 cycles of each SIMD, 5.5 us;
+//     cast from bf16 20 us: 1573 and 42 of LDS, most of them for tokens redone;
+//   256 experts in 8 groups, sigmoid and bias 14.2 to 16.8 us: 1287 instructions, 20600 cycles, 8.6 us;
+//     the unit is busy for 0.7 of the time that waves run, which wait for a third of theirs.
+// 1 token of 64 experts 3.3 us, nearly all of it the launch; 77 tokens of 256 in groups 5.8 us, the
+// latency of one wave's steps, more than half of it waits.
 // ---------------------------------------------------------------------------
 template <int S>
 __device__ __forceinline__ uint32_t lane_swap(uint32_t x) {
@@ -683,8 +688,9 @@ __global__ void __launch_bounds__(256) route_lanes_kernel(const RouteParams p) {
 // softmax's own product dx = s (G - sum G s) over the row, or G s (1 - s).  One read of what it needs
 // of X (renormalised: the chosen alone), one write of dX.  A lane has NV experts in registers and the
 // choices are added to them in order, so that the same expert twice adds up the same each time.
-// Measured (MI355X, bf16, 16384 tokens, top 8): 64 experts 6.0 us, softmax not renormalised 6.3 us;
-// 256 experts 8.9 and 11.7 us (8 MB written; 17 MB moved, 1.4 TB/s): the walk over the choices bounds it.
+// Measured (MI355X, bf16, 16384 tokens, top 8): 64 experts 6.3 us, softmax not renormalised 6.4 us;
+// 256 experts 9.1 and 11.8 us (8 MB written; 17 MB moved, 1.4 TB/s): the walk over the choices bounds it,
+// 269 vector instructions a wave, which keep the unit busy for 0.9 of the time.
 // ---------------------------------------------------------------------------
 template <int DT, int NV>
 __global__ void __launch_bounds__(256) route_bwd_kernel(const RouteParams p) {
@@ -893,7 +899,8 @@ __global__ void __launch_bounds__(64 * WAVES) sort_kernel(const SortParams p) {
 //   spread    4096 x 4096 to 8 places  302 MB  61.5 us  4.9 TB/s;  128 x 4096 5.8 us;  1 x 4096 4.7 us
 //   combine   4096 x 4096 of 8 places  302 MB  62 us    4.9 TB/s;  128 x 4096 5.5 us;  1 x 4096 4.3 us
 //   combine's gradient, 16384 x 2048 of 4 places, 604 MB with Z read for the weights' dots: 131 us,
-//   4.6 TB/s (a copy of 4 GiB: 4.75 TB/s)
+//   4.6 TB/s (a copy of 4 GiB: 4.75 TB/s); of 65536 places 64 wide 19 us, 1.3 TB/s, where a wave a place
+//   has work for 8 lanes and the vector unit, 129 instructions a wave, is busy for 0.87 of the time
 // ---------------------------------------------------------------------------
 struct RowsParams {
     const void *X, *Z, *R;       // spread: X; combine: Z, R; backward: X = dOut, Z
