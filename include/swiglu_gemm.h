@@ -618,8 +618,8 @@ int sg_int4_dequantize(const void* codes, const void* scales, const void* zeros,
  * value of it above 2^120, or sums of (16 + max(15, zero)) * scale * |a| past fp32's range give NaN or
  * an infinity where they count.  Those sums are larger than the values', so an fp32 C of bf16 operands
  * is less exact than an ordinary fp32 sum: K = 4096, rms error over C's rms 2^-22 to 2^-21 for activations
- * without a mean, 2^-20 to 2^-18 with a mean of half to four times their spread (fp16: 2^-23).  A bf16 C
- * rounds off more.
+ * without a mean, up to 2^-18 with a mean of four times their spread (fp16: 2^-23).  A bf16 C rounds
+ * off more.
  * From some hundred rows on sg_int4_dequantize and a 16-bit product (sg_gemm with transB) are faster: bf16
  * by 4096 x 11008 from about 768 rows (groups of 64 with zero points: 512), 1024 rows 119 and 103 us, 4096
  * rows 433 and 304 us; by 4096 x 4096 from about 1536 rows.
